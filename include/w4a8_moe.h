@@ -575,6 +575,92 @@ int w4a8_moe_grouped_gemm_swiglu_mxfp4_prepacked(const uint8_t* a, const float* 
                                                  const uint8_t* w13, const uint8_t* s13, int64_t I, int64_t K,
                                                  float* act, float* act_pmax, int32_t algo, void* stream);
 
+/*
+ * ---- The whole layer for a few tokens -----------------------------------------
+ * All seven steps for 1 to 16 tokens in two kernels, on the GEMM storage: the
+ * calls above spend five launches and as many trips through memory on a step that
+ * reads little more than the touched experts' weights.  (One decode step of the
+ * layer: "GLM-5.3-W4A8" card, sections 量化方式 and 性能.)
+ *   ids, w as w4a8_moe_route (the same bits); qx, sx by the rule of
+ *   w4a8_moe_quant_act (_i8 form: w4a8_moe_quant_act_i8); for every f = t*k + j:
+ *   act[f, :] = silu(gate) * up of expert ids[f], sa[f] and the codes qa[f, :] by the
+ *   rule of w4a8_moe_requant (_i8); y[t, :] = sum_j w[t, j] * sa[f] * (qa[f, :] x w2).
+ *   The products run on the bf16 matrix cores with fp32 sums (INT8 form: exact int32
+ *   sums), so act and y differ from the seven calls' by rounding only; a code of
+ *   qa may then fall on the other side of a border between two codes.
+ *   x_bf16    : bf16 bit patterns [T][ld_x], 16-byte aligned, ld_x % 8 == 0, ld_x >= H.
+ *   logits    : fp32 [T][E].
+ *   w13, w2   : the GEMM storage of the experts' gate/up rows (N = 2I, K = H) and
+ *               down rows (N = H, K = I), 16-byte aligned; s13, s2 : their scales, as in
+ *               the _prepacked GEMMs of the same form (_i8 : fp32 [E][2I] and [E][H]).
+ *   ids, w    : int32 [T][k] and fp32 [T][k], written; either may be NULL.
+ *   y         : [T][H], fp32 or bf16 (y_dtype, as in w4a8_moe_unpermute; bf16 rounded
+ *               to nearest even), aligned to its elements.
+ *   workspace : device memory of w4a8_moe_few_workspace_bytes(T, k, I) bytes, 16-byte
+ *               aligned (contents need no initialisation; calls that overlap must not
+ *               share one).
+ *   Rules     : 0 <= T <= 16, 1 <= k <= E <= 1024, T*k <= 256, H > 0, H % 128 == 0,
+ *               H <= 8192, T*H <= 114688, I > 0, I % 128 == 0.  Larger batches take the
+ *               seven calls.
+ *   Logits of -infinity rank last and get weight zero.  Whatever the logits hold,
+ *   every id written is in [0, E) and no memory outside the arrays is touched.
+ */
+
+/* Bytes of device workspace the _few calls need, or -1 on sizes outside their rules. */
+int64_t w4a8_moe_few_workspace_bytes(int64_t T, int32_t k, int64_t I);
+
+int w4a8_moe_few_prepacked(const uint16_t* x_bf16, int64_t T, int64_t H, int64_t ld_x, const float* logits, int32_t E,
+                           int32_t k, int32_t renormalize, const int32_t* w13, const float* s13, const int32_t* w2,
+                           const float* s2, int64_t I, int32_t* ids, float* w, void* y, int32_t y_dtype,
+                           void* workspace, int64_t workspace_bytes, void* stream);
+
+/* The per-channel INT4 x per-token INT8 form. */
+int w4a8_moe_few_i8_prepacked(const uint16_t* x_bf16, int64_t T, int64_t H, int64_t ld_x, const float* logits,
+                              int32_t E, int32_t k, int32_t renormalize, const int32_t* w13, const float* s13,
+                              const int32_t* w2, const float* s2, int64_t I, int32_t* ids, float* w, void* y,
+                              int32_t y_dtype, void* workspace, int64_t workspace_bytes, void* stream);
+
+/* The MXFP4 form (FP8 activations). */
+int w4a8_moe_few_mxfp4_prepacked(const uint16_t* x_bf16, int64_t T, int64_t H, int64_t ld_x, const float* logits,
+                                 int32_t E, int32_t k, int32_t renormalize, const uint8_t* w13, const uint8_t* s13,
+                                 const uint8_t* w2, const uint8_t* s2, int64_t I, int32_t* ids, float* w, void* y,
+                                 int32_t y_dtype, void* workspace, int64_t workspace_bytes, void* stream);
+
+/*
+ * ---- Matrix-vector products with 4-bit weights ---------------------------------
+ * One dense 4-bit matrix times 1 to 16 bf16 activation rows, which are not
+ * quantized: the projections next to the routed experts (a shared expert, an
+ * output head) of a model that keeps them in the same weight formats.
+ * (INT4 group 128 and its MXFP4 and per-channel alternatives: "GLM-5.3-W4A8" card,
+ * section 量化方式; "GLM-5.3-Channel-INT4-w4a8" card, section 1.)
+ *   y[t, n] = sum_k x[t, k] * W[n, k], in fp32, where W[n, k] is
+ *     group 128   : w_scale[n, k / 128] * q[n, k],
+ *     per channel : w_scale[n] * q[n, k]                           (_channel),
+ *     MXFP4       : 2^(w_scale[n, k / 32] - 127) * E2M1(code[n, k])   (_mxfp4).
+ *   x_bf16  : bf16 bit patterns [T][ld_x] (first K columns used), 16-byte aligned,
+ *             ld_x % 8 == 0, ld_x >= K.
+ *   w, s    : one matrix in the stored format or, _prepacked, in the GEMM storage
+ *             (the E = 1 case of the grouped GEMMs' arrays): weights 16-byte aligned,
+ *             fp32 scales and the GEMM storage's E8M0 words 4-byte aligned.
+ *   y       : [T][N], fp32 or bf16 (y_dtype; rounded to nearest even), aligned to its
+ *             elements.
+ *   Rules   : 0 <= T <= 16; K > 0, K % 128 == 0 (stored MXFP4: K % 32 == 0); N > 0,
+ *             _prepacked: N % 16 == 0.  Larger batches take the grouped GEMMs.
+ */
+int w4a8_moe_matvec(const uint16_t* x_bf16, int64_t T, int64_t K, int64_t ld_x, const int32_t* w_packed,
+                    const float* w_scale, int64_t N, void* y, int32_t y_dtype, void* stream);
+int w4a8_moe_matvec_prepacked(const uint16_t* x_bf16, int64_t T, int64_t K, int64_t ld_x, const int32_t* w_blk,
+                              const float* s_blk, int64_t N, void* y, int32_t y_dtype, void* stream);
+int w4a8_moe_matvec_channel(const uint16_t* x_bf16, int64_t T, int64_t K, int64_t ld_x, const int32_t* w_packed,
+                            const float* w_scale, int64_t N, void* y, int32_t y_dtype, void* stream);
+int w4a8_moe_matvec_channel_prepacked(const uint16_t* x_bf16, int64_t T, int64_t K, int64_t ld_x,
+                                      const int32_t* w_blk, const float* w_scale, int64_t N, void* y, int32_t y_dtype,
+                                      void* stream);
+int w4a8_moe_matvec_mxfp4(const uint16_t* x_bf16, int64_t T, int64_t K, int64_t ld_x, const uint8_t* w_packed,
+                          const uint8_t* w_scale, int64_t N, void* y, int32_t y_dtype, void* stream);
+int w4a8_moe_matvec_mxfp4_prepacked(const uint16_t* x_bf16, int64_t T, int64_t K, int64_t ld_x, const uint8_t* w_blk,
+                                    const uint8_t* s_blk, int64_t N, void* y, int32_t y_dtype, void* stream);
+
 /* Static name of a status code ("W4A8_OK", ...). */
 const char* w4a8_moe_status_string(int status);
 

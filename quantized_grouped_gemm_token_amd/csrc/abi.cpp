@@ -12,6 +12,14 @@
 
 #include "kernels.hpp"
 
+// The newest launchers are weak references here, so that a host-only build of this
+// file (its argument checks without the kernels) also links and loads; the device
+// check keeps such a build from reaching them.
+namespace w4a8 {
+hipError_t launch_few(const FewArgs& f, hipStream_t stream) __attribute__((weak));
+hipError_t launch_matvec(const MatvecArgs& a, hipStream_t stream) __attribute__((weak));
+}  // namespace w4a8
+
 namespace {
 
 thread_local std::string g_last_error;
@@ -634,6 +642,139 @@ int w4a8_moe_combine(const float* o_tok, const int32_t* inv_pos, int64_t T, int3
   (void)hipGetLastError();
   return launched(w4a8::launch_combine(o_tok, inv_pos, T, k, H, y, y_dtype == W4A8_Y_BF16 ? 1 : 0,
                                        as_stream(stream)), "combine");
+}
+
+// ---- the whole layer for a few tokens
+int64_t w4a8_moe_few_workspace_bytes(int64_t T, int32_t k, int64_t I) {
+  if (T < 0 || T > w4a8::kFewMaxTokens || k < 1 || T * (int64_t)k > w4a8::kFewMaxRows || I <= 0 || I % 128 ||
+      I >= kMaxRows)
+    return -1;
+  return w4a8::few_workspace_bytes(T * (int64_t)k, I);
+}
+
+static int run_few(const char* name, Form form, const uint16_t* x, int64_t T, int64_t H, int64_t ld_x,
+                   const float* logits, int32_t E, int32_t k, int32_t renormalize, const void* w13, const void* s13,
+                   const void* w2, const void* s2, int64_t I, int32_t* ids, float* w, void* y, int32_t y_dtype,
+                   void* workspace, int64_t workspace_bytes, void* stream) {
+  if (T < 0 || T > w4a8::kFewMaxTokens)
+    return fail(W4A8_ERR_SHAPE, "%s: T=%lld must be in [0, %d]", name, (long long)T, w4a8::kFewMaxTokens);
+  if (E < 1 || E > 1024 || k < 1 || k > E)
+    return fail(W4A8_ERR_SHAPE, "%s: need 1 <= k <= E <= 1024 (k=%d, E=%d)", name, k, E);
+  if (T * (int64_t)k > w4a8::kFewMaxRows)
+    return fail(W4A8_ERR_SHAPE, "%s: T*k=%lld must be at most %d", name, (long long)(T * (int64_t)k),
+                w4a8::kFewMaxRows);
+  if (H <= 0 || H % 128 || H > w4a8::kFewMaxH || T * H > w4a8::kFewMaxCodes)
+    return fail(W4A8_ERR_SHAPE, "%s: H=%lld must be a positive multiple of 128 up to %lld, and T*H at most %lld", name,
+                (long long)H, (long long)w4a8::kFewMaxH, (long long)w4a8::kFewMaxCodes);
+  if (ld_x < H || ld_x % 8)
+    return fail(W4A8_ERR_SHAPE, "%s: ld_x=%lld must be >= H and a multiple of 8", name, (long long)ld_x);
+  if (I <= 0 || I % 128 || I >= kMaxRows)
+    return fail(W4A8_ERR_SHAPE, "%s: I=%lld must be a positive multiple of 128", name, (long long)I);
+  if (y_dtype != W4A8_Y_F32 && y_dtype != W4A8_Y_BF16)
+    return fail(W4A8_ERR_SHAPE, "%s: y_dtype=%d must be W4A8_Y_F32 or W4A8_Y_BF16", name, y_dtype);
+  if (T == 0) return ok();
+  if (!x || !logits || !w13 || !s13 || !w2 || !s2 || !y || !workspace)
+    return fail(W4A8_ERR_NULL, "%s: null pointer", name);
+  const int64_t need = w4a8::few_workspace_bytes(T * (int64_t)k, I);
+  if (workspace_bytes < need)
+    return fail(W4A8_ERR_WORKSPACE, "%s: workspace of %lld bytes, need %lld", name, (long long)workspace_bytes,
+                (long long)need);
+  if (!aligned(x, 16) || !aligned(w13, 16) || !aligned(w2, 16) || !aligned(workspace, 16) || !aligned(logits, 4) ||
+      !aligned(s13, 4) || !aligned(s2, 4) || !aligned(ids, 4) || !aligned(w, 4) ||
+      !aligned(y, y_dtype == W4A8_Y_F32 ? 4 : 2))
+    return fail(W4A8_ERR_ALIGN, "%s: x, the weights and the workspace must be 16-byte aligned, the rest to their "
+                "elements", name);
+  if (int st = check_device()) return st;
+  (void)hipGetLastError();
+  const w4a8::FewArgs f{(int)form, x, T, H, ld_x, logits, E, k, renormalize ? 1 : 0, w13, s13, w2, s2, I, ids, w, y,
+                        y_dtype == W4A8_Y_BF16 ? 1 : 0, workspace};
+  return launched(w4a8::launch_few(f, as_stream(stream)), name);
+}
+
+int w4a8_moe_few_prepacked(const uint16_t* x_bf16, int64_t T, int64_t H, int64_t ld_x, const float* logits, int32_t E,
+                           int32_t k, int32_t renormalize, const int32_t* w13, const float* s13, const int32_t* w2,
+                           const float* s2, int64_t I, int32_t* ids, float* w, void* y, int32_t y_dtype,
+                           void* workspace, int64_t workspace_bytes, void* stream) {
+  return run_few("few_prepacked", Form::kG128, x_bf16, T, H, ld_x, logits, E, k, renormalize, w13, s13, w2, s2, I,
+                 ids, w, y, y_dtype, workspace, workspace_bytes, stream);
+}
+
+int w4a8_moe_few_i8_prepacked(const uint16_t* x_bf16, int64_t T, int64_t H, int64_t ld_x, const float* logits,
+                              int32_t E, int32_t k, int32_t renormalize, const int32_t* w13, const float* s13,
+                              const int32_t* w2, const float* s2, int64_t I, int32_t* ids, float* w, void* y,
+                              int32_t y_dtype, void* workspace, int64_t workspace_bytes, void* stream) {
+  return run_few("few_i8_prepacked", Form::kChannel, x_bf16, T, H, ld_x, logits, E, k, renormalize, w13, s13, w2, s2,
+                 I, ids, w, y, y_dtype, workspace, workspace_bytes, stream);
+}
+
+int w4a8_moe_few_mxfp4_prepacked(const uint16_t* x_bf16, int64_t T, int64_t H, int64_t ld_x, const float* logits,
+                                 int32_t E, int32_t k, int32_t renormalize, const uint8_t* w13, const uint8_t* s13,
+                                 const uint8_t* w2, const uint8_t* s2, int64_t I, int32_t* ids, float* w, void* y,
+                                 int32_t y_dtype, void* workspace, int64_t workspace_bytes, void* stream) {
+  return run_few("few_mxfp4_prepacked", Form::kMx, x_bf16, T, H, ld_x, logits, E, k, renormalize, w13, s13, w2, s2, I,
+                 ids, w, y, y_dtype, workspace, workspace_bytes, stream);
+}
+
+// ---- matrix-vector products
+static int run_matvec(const char* name, Form form, bool row_major, const uint16_t* x, int64_t T, int64_t K,
+                      int64_t ld_x, const void* w, const void* s, int64_t N, void* y, int32_t y_dtype, void* stream) {
+  if (T < 0 || T > w4a8::kMatvecMaxTokens)
+    return fail(W4A8_ERR_SHAPE, "%s: T=%lld must be in [0, %d]", name, (long long)T, w4a8::kMatvecMaxTokens);
+  const int64_t kmult = form == Form::kMx && row_major ? 32 : 128;
+  if (K <= 0 || K % kmult || K >= kMaxRows)
+    return fail(W4A8_ERR_SHAPE, "%s: K=%lld must be a positive multiple of %lld", name, (long long)K,
+                (long long)kmult);
+  if (ld_x < K || ld_x % 8)
+    return fail(W4A8_ERR_SHAPE, "%s: ld_x=%lld must be >= K and a multiple of 8", name, (long long)ld_x);
+  const int64_t nmult = row_major ? 1 : 16;
+  if (N <= 0 || N % nmult || N >= kMaxRows)
+    return fail(W4A8_ERR_SHAPE, "%s: N=%lld must be a positive multiple of %lld", name, (long long)N,
+                (long long)nmult);
+  if (y_dtype != W4A8_Y_F32 && y_dtype != W4A8_Y_BF16)
+    return fail(W4A8_ERR_SHAPE, "%s: y_dtype=%d must be W4A8_Y_F32 or W4A8_Y_BF16", name, y_dtype);
+  if (T == 0) return ok();
+  if (!x || !w || !s || !y) return fail(W4A8_ERR_NULL, "%s: null pointer", name);
+  if (!aligned(x, 16) || !aligned(w, 16) || !aligned(s, form == Form::kMx && row_major ? 1 : 4) ||
+      !aligned(y, y_dtype == W4A8_Y_F32 ? 4 : 2))
+    return fail(W4A8_ERR_ALIGN, "%s: x and the weights must be 16-byte aligned, the rest to their elements", name);
+  if (int st = check_device()) return st;
+  (void)hipGetLastError();
+  const w4a8::MatvecArgs a{(int)form, row_major, x, T, K, ld_x, w, s, N, y, y_dtype == W4A8_Y_BF16 ? 1 : 0};
+  return launched(w4a8::launch_matvec(a, as_stream(stream)), name);
+}
+
+int w4a8_moe_matvec(const uint16_t* x_bf16, int64_t T, int64_t K, int64_t ld_x, const int32_t* w_packed,
+                    const float* w_scale, int64_t N, void* y, int32_t y_dtype, void* stream) {
+  return run_matvec("matvec", Form::kG128, true, x_bf16, T, K, ld_x, w_packed, w_scale, N, y, y_dtype, stream);
+}
+
+int w4a8_moe_matvec_prepacked(const uint16_t* x_bf16, int64_t T, int64_t K, int64_t ld_x, const int32_t* w_blk,
+                              const float* s_blk, int64_t N, void* y, int32_t y_dtype, void* stream) {
+  return run_matvec("matvec_prepacked", Form::kG128, false, x_bf16, T, K, ld_x, w_blk, s_blk, N, y, y_dtype, stream);
+}
+
+int w4a8_moe_matvec_channel(const uint16_t* x_bf16, int64_t T, int64_t K, int64_t ld_x, const int32_t* w_packed,
+                            const float* w_scale, int64_t N, void* y, int32_t y_dtype, void* stream) {
+  return run_matvec("matvec_channel", Form::kChannel, true, x_bf16, T, K, ld_x, w_packed, w_scale, N, y, y_dtype,
+                    stream);
+}
+
+int w4a8_moe_matvec_channel_prepacked(const uint16_t* x_bf16, int64_t T, int64_t K, int64_t ld_x,
+                                      const int32_t* w_blk, const float* w_scale, int64_t N, void* y, int32_t y_dtype,
+                                      void* stream) {
+  return run_matvec("matvec_channel_prepacked", Form::kChannel, false, x_bf16, T, K, ld_x, w_blk, w_scale, N, y,
+                    y_dtype, stream);
+}
+
+int w4a8_moe_matvec_mxfp4(const uint16_t* x_bf16, int64_t T, int64_t K, int64_t ld_x, const uint8_t* w_packed,
+                          const uint8_t* w_scale, int64_t N, void* y, int32_t y_dtype, void* stream) {
+  return run_matvec("matvec_mxfp4", Form::kMx, true, x_bf16, T, K, ld_x, w_packed, w_scale, N, y, y_dtype, stream);
+}
+
+int w4a8_moe_matvec_mxfp4_prepacked(const uint16_t* x_bf16, int64_t T, int64_t K, int64_t ld_x, const uint8_t* w_blk,
+                                    const uint8_t* s_blk, int64_t N, void* y, int32_t y_dtype, void* stream) {
+  return run_matvec("matvec_mxfp4_prepacked", Form::kMx, false, x_bf16, T, K, ld_x, w_blk, s_blk, N, y, y_dtype,
+                    stream);
 }
 
 }  // extern "C"

@@ -102,6 +102,50 @@ struct FrontArgs {
 };
 bool front_fits(int64_t T, int64_t H, int k);
 hipError_t launch_front(const FrontArgs& f, bool int8, hipStream_t stream);
+// the whole layer for a few tokens in two kernels (few.hip), on the GEMM storage
+constexpr int kFewMaxTokens = 16;        // one 16-row block of the matrix cores
+constexpr int kFewMaxRows = 256;         // T k
+constexpr int64_t kFewMaxH = 8192;       // 8 K groups for each of a workgroup's 8 waves
+// bytes of activation codes a workgroup holds in LDS (T H), next to 32 KB of partial
+// tiles and 13 KB of routing
+constexpr int64_t kFewMaxCodes = 112 << 10;
+// the workspace: the routing (count, experts, weights, slots), then act [R][I] and its block maxima [R][I/16]
+constexpr int64_t kFewHeadBytes = 16 + 8 * kFewMaxRows + 2 * kFewMaxRows * kFewMaxTokens;
+constexpr int64_t few_workspace_bytes(int64_t R, int64_t I) { return kFewHeadBytes + 4 * R * (I + I / 16); }
+// dynamic LDS of the first kernel: the codes, then two buffers of partial tiles (or 1024 ints)
+constexpr int64_t few_gate_up_smem(int64_t T, int64_t H) { return T * H + (T >= 2 ? 2048 * T : 4096); }
+struct FewArgs {
+  int form;               // WeightForm
+  const uint16_t* x;
+  int64_t T, H, ld;
+  const float* logits;
+  int E, k, renormalize;
+  const void* w13;
+  const void* s13;
+  const void* w2;
+  const void* s2;
+  int64_t I;
+  int32_t* ids;           // may be null, with w
+  float* w;
+  void* y;
+  int y_bf16;
+  void* workspace;
+};
+hipError_t launch_few(const FewArgs& f, hipStream_t stream);
+// y [T][N] = x [T][K] (bf16) times 4-bit weights (matvec.hip), T <= kMatvecMaxTokens
+constexpr int kMatvecMaxTokens = 16;
+struct MatvecArgs {
+  int form;               // WeightForm
+  bool row_major;
+  const uint16_t* x;
+  int64_t T, K, ld;
+  const void* w;
+  const void* s;
+  int64_t N;
+  void* y;
+  int y_bf16;
+};
+hipError_t launch_matvec(const MatvecArgs& a, hipStream_t stream);
 hipError_t launch_unpermute(const float* o, const int32_t* inv_pos, const float* w, int64_t T, int k, int64_t H,
                             void* y, int bf16_out, hipStream_t stream);
 // row_src[p] = f and row_scale[p] = a_scale[p] * w[f] for every routed index f (inv_pos[f] = p >= 0)

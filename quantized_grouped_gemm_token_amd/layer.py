@@ -22,6 +22,10 @@ W4A8MoEChannel is the per-channel INT4 x per-token INT8 variant: fp32 [E][N]
 scales, INT8 activations.  W4A8MoEMxfp4 holds MXFP4 group-32 experts (E2M1
 codes uint8 [E][N][K/2], E8M0 scales uint8 [E][N][K/32]) and uses the same
 FP8 activations.
+With few=True a forward of at most 16 tokens runs as one call of two kernels
+(w4a8_moe_few_prepacked and its forms) instead of the steps; larger batches, and
+sizes outside that call's rules, take the steps as before.  Its results differ from
+the steps' by rounding.
 Intermediate buffers are allocated once per token count and reused, so a
 forward pass enqueues kernels only: no allocation, no host synchronisation.
 That also makes a step capturable: capture() records one forward into a HIP
@@ -40,10 +44,12 @@ class W4A8MoE:
     GEMM = staticmethod(ops.w4a8_moe_grouped_gemm_prepacked)
     GEMM_SWIGLU = staticmethod(ops.w4a8_moe_grouped_gemm_swiglu_prepacked)
     GEMM_SCATTER = staticmethod(ops.w4a8_moe_grouped_gemm_scatter_prepacked)
+    FEW = staticmethod(ops.w4a8_moe_few_prepacked)
     SCATTER_MIN_ROWS = 1 << 62                            # scatter=None: the gather combine at every size
 
     def __init__(self, w13: torch.Tensor, s13: torch.Tensor, w2: torch.Tensor, s2: torch.Tensor, k: int,
-                 renormalize: bool = True, fused: bool = True, front: bool = True, scatter: bool | None = None):
+                 renormalize: bool = True, fused: bool = True, front: bool = True, scatter: bool | None = None,
+                 few: bool = False):
         E, N13, KW13 = w13.shape
         E2, H, KW2 = w2.shape
         c = self.K_PER_ITEM
@@ -54,6 +60,7 @@ class W4A8MoE:
         self.renormalize = renormalize
         self.fused = fused
         self.scatter = scatter
+        self.few = few                                    # up to 16 tokens as one call of two kernels
         self.front = front                                # steps 1-3 as one call (w4a8_moe_front)
         self.steps = (("front",) if front else ("quant_act", "route", "permute")) + self.STEPS[3:]
         self._bufs: dict[int, dict] = {}
@@ -93,15 +100,33 @@ class W4A8MoE:
         """Whether a forward over T tokens folds the routing weights into the down GEMM."""
         return self.scatter if self.scatter is not None else T * self.k >= self.SCATTER_MIN_ROWS
 
+    def uses_few(self, T: int) -> bool:
+        """Whether a forward over T tokens is the one call for a few tokens."""
+        return self.few and T > 0 and ops.w4a8_moe_few_fits(T, self.H, self.k)
+
+    def _forward_few(self, x, logits, y, y_dtype, events):
+        # the call allocates its workspace: forwards on several streams, or captured
+        # into several graphs, share none
+        ev = events.get("few") if events else None
+        if ev:
+            ev[0].record()
+        y = self.FEW(x, logits, self.k, self.w13, self.s13, self.w2, self.s2, self.renormalize, y, y_dtype)
+        if ev:
+            ev[1].record()
+        return y
+
     def forward(self, x: torch.Tensor, logits: torch.Tensor, y: torch.Tensor | None = None,
                 y_dtype: torch.dtype = torch.float32, algo: int = ops.W4A8_GG_AUTO,
                 events: dict | None = None) -> torch.Tensor:
         """x bf16 [T, H], router logits fp32 [T, E] -> y [T, H].
 
-        events, if given, maps step names (self.steps) to (start, end) CUDA
-        events that are recorded on the current stream around each step.
+        events, if given, maps step names (self.steps, or "few" for a forward that
+        is that one call) to (start, end) CUDA events that are recorded on the
+        current stream around each step.
         """
         T = x.shape[0]
+        if self.uses_few(T):
+            return self._forward_few(x, logits, y, y_dtype, events)
         b = self.buffers(T)
         R = T * self.k
 
@@ -162,6 +187,7 @@ class W4A8MoE:
 class W4A8MoEChannel(W4A8MoE):
     """The per-channel INT4 x per-token INT8 variant: s13 [E, 2I] and s2 [E, H]
     are per-channel scales; steps 1, 4, 5 and 6 use the INT8 calls."""
+    FEW = staticmethod(ops.w4a8_moe_few_i8_prepacked)
 
     @staticmethod
     def prepack(w13, s13, w2, s2):
@@ -183,6 +209,8 @@ class W4A8MoEChannel(W4A8MoE):
                 y_dtype: torch.dtype = torch.float32, algo: int = ops.W4A8_GG_AUTO,
                 events: dict | None = None) -> torch.Tensor:
         T = x.shape[0]
+        if self.uses_few(T):
+            return self._forward_few(x, logits, y, y_dtype, events)
         b = self.buffers(T)
         R = T * self.k
 
@@ -234,6 +262,7 @@ class W4A8MoEMxfp4(W4A8MoE):
     GEMM = staticmethod(ops.w4a8_moe_grouped_gemm_mxfp4_prepacked)
     GEMM_SWIGLU = staticmethod(ops.w4a8_moe_grouped_gemm_swiglu_mxfp4_prepacked)
     GEMM_SCATTER = staticmethod(ops.w4a8_moe_grouped_gemm_scatter_mxfp4_prepacked)
+    FEW = staticmethod(ops.w4a8_moe_few_mxfp4_prepacked)
 
     @staticmethod
     def prepack(w13, s13, w2, s2):

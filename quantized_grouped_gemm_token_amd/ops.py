@@ -82,6 +82,12 @@ _SIGNATURES = {
     "w4a8_moe_grouped_gemm_scatter_mxfp4_prepacked": (ctypes.c_int,
         [_c_p, _c_p, _c_p, _i64, _c_p, _i32, _c_p, _c_p, _i64, _i64, _c_p, _c_p, _i32, _c_p]),
     "w4a8_moe_combine": (ctypes.c_int, [_c_p, _c_p, _i64, _i32, _i64, _c_p, _i32, _c_p]),
+    "w4a8_moe_few_workspace_bytes": (ctypes.c_int64, [_i64, _i32, _i64]),
+    **{f"w4a8_moe_few{form}_prepacked": (ctypes.c_int,
+        [_c_p, _i64, _i64, _i64, _c_p, _i32, _i32, _i32, _c_p, _c_p, _c_p, _c_p, _i64, _c_p, _c_p, _c_p, _i32, _c_p,
+         _i64, _c_p]) for form in ("", "_i8", "_mxfp4")},
+    **{f"w4a8_moe_matvec{form}": (ctypes.c_int, [_c_p, _i64, _i64, _i64, _c_p, _c_p, _i64, _c_p, _i32, _c_p])
+       for form in ("", "_prepacked", "_channel", "_channel_prepacked", "_mxfp4", "_mxfp4_prepacked")},
     "w4a8_moe_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "w4a8_moe_last_error": (ctypes.c_char_p, []),
     "w4a8_moe_device_supported": (ctypes.c_int, []),
@@ -903,3 +909,203 @@ def w4a8_moe_grouped_gemm_swiglu_mxfp4_prepacked(a: torch.Tensor, a_scale: torch
                                                  act_pmax: torch.Tensor | None = None, algo: int = W4A8_GG_AUTO):
     """The same on the GEMM storage of w13 and s13."""
     return _gemm_swiglu("mxfp4", True, a, a_scale, None, a_rows, offsets, w13, s13, M_total, act, act_pmax, algo)
+
+
+# ------------------------------------------------- a few tokens: the whole layer, and matrix-vector products
+FEW_MAX_TOKENS = 16
+
+
+def _need_x(x: torch.Tensor) -> None:
+    """x bf16 [T, K] on the GPU, its rows contiguous and any multiple of 8 elements apart."""
+    if not isinstance(x, torch.Tensor):
+        raise TypeError("x must be a torch.Tensor")
+    if x.dtype != torch.bfloat16:
+        raise TypeError(f"x must be {torch.bfloat16}, got {x.dtype}")
+    if x.dim() != 2:
+        raise ValueError(f"x must have 2 dims, got shape {tuple(x.shape)}")
+    if not x.is_cuda:
+        raise ValueError("x must be a GPU tensor")
+    if x.shape[1] > 1 and x.stride(1) != 1:
+        raise ValueError("x must have contiguous rows")
+
+
+def _ld(x: torch.Tensor) -> int:
+    """Elements between two rows of x (a single row has no such distance)."""
+    return x.stride(0) if x.shape[0] > 1 else x.shape[1]
+
+
+def _y(y, y_dtype, T: int, N: int, dev):
+    if y is None:
+        if y_dtype not in (torch.float32, torch.bfloat16):
+            raise TypeError("y must be float32 or bfloat16")
+        y = torch.empty((T, N), dtype=y_dtype, device=dev)
+    else:
+        if not isinstance(y, torch.Tensor) or y.dtype not in (torch.float32, torch.bfloat16):
+            raise TypeError("y must be a float32 or bfloat16 tensor")
+        _need(y, "y", y.dtype, 2, dev)
+        if tuple(y.shape) != (T, N):
+            raise ValueError(f"y must be [{T}, {N}]")
+    return y, W4A8_Y_F32 if y.dtype == torch.float32 else W4A8_Y_BF16
+
+
+def _call_on(dev: torch.device, name: str, *args) -> None:
+    """The library call on dev's current stream, with dev the current device."""
+    if dev.index == torch.cuda.current_device():
+        status = getattr(lib(), name)(*args, _stream(dev))
+    else:
+        with torch.cuda.device(dev):
+            status = getattr(lib(), name)(*args, _stream(dev))
+    _check(name, status)
+
+
+def w4a8_moe_few_fits(T: int, H: int, k: int) -> bool:
+    """Whether the few-token layer's size rules admit T tokens of H, k experts each (H and I multiples of 128)."""
+    return 0 <= T <= FEW_MAX_TOKENS and T * k <= 256 and H <= 8192 and T * H <= 114688
+
+
+def w4a8_moe_few_workspace_bytes(T: int, k: int, I: int) -> int:
+    n = lib().w4a8_moe_few_workspace_bytes(T, k, I)
+    if n < 0:
+        raise ValueError(f"sizes outside the rules of the few-token layer: T={T} k={k} I={I}")
+    return n
+
+
+def _few(form, x, logits, k, w13, s13, w2, s2, renormalize, y, y_dtype, ids, w, workspace):
+    _need_x(x)
+    dev = x.device
+    T, H = x.shape
+    _need(logits, "logits", torch.float32, 2, dev)
+    E = logits.shape[1]
+    if logits.shape[0] != T:
+        raise ValueError("logits must be [T, E] for x [T, H]")
+    if form == "mxfp4":
+        E13, N13, K13 = _mx_weights(w13, s13, ("w13", "s13"), dev, True)
+        E2, N2, K2 = _mx_weights(w2, s2, ("w2", "s2"), dev, True)
+    else:
+        E13, N13, K13 = _int4_storage(w13, "w13", dev)
+        E2, N2, K2 = _int4_storage(w2, "w2", dev)
+        for s, name, n, kk in ((s13, "s13", N13, K13), (s2, "s2", N2, K2)):
+            if form == "i8":
+                _need(s, name, torch.float32, 2, dev)
+                if tuple(s.shape) != (E, n):
+                    raise ValueError(f"{name} must be [{E}, {n}]")
+            else:
+                _g128_scales(s, name, dev, E, n, kk, True)
+    if E13 != E or E2 != E or K13 != H or N2 != H or 2 * K2 != N13:
+        raise ValueError("w13 must hold [E] experts of 2I rows of H, w2 of H rows of I, for x [T, H] and logits [T, E]")
+    y, code = _y(y, y_dtype, T, H, dev)
+    for t, name, dt in ((ids, "ids", torch.int32), (w, "w", torch.float32)):
+        if t is not None:
+            _need(t, name, dt, 2, dev)
+            if tuple(t.shape) != (T, k):
+                raise ValueError(f"{name} must be [T, k]")
+    nbytes = lib().w4a8_moe_few_workspace_bytes(T, k, K2)           # -1 on sizes the library refuses below
+    if workspace is None:
+        workspace = torch.empty((max(nbytes, 16),), dtype=torch.uint8, device=dev)
+    else:
+        _need(workspace, "workspace", torch.uint8, 1, dev)
+    _call_on(dev, "w4a8_moe_few" + ("" if form == "g128" else "_" + form) + "_prepacked", _p(x), T, H, _ld(x),
+             _p(logits), E, k, int(bool(renormalize)), _p(w13), _p(s13), _p(w2), _p(s2), K2, _p(ids), _p(w), _p(y),
+             code, _p(workspace), workspace.numel())
+    return y
+
+
+def w4a8_moe_few_prepacked(x: torch.Tensor, logits: torch.Tensor, k: int, w13: torch.Tensor, s13: torch.Tensor,
+                           w2: torch.Tensor, s2: torch.Tensor, renormalize: bool = True,
+                           y: torch.Tensor | None = None, y_dtype: torch.dtype = torch.float32,
+                           ids: torch.Tensor | None = None, w: torch.Tensor | None = None,
+                           workspace: torch.Tensor | None = None):
+    """The whole layer for 1 to 16 tokens in two kernels: x bf16 [T, H] (rows any multiple of 8 elements apart),
+    router logits fp32 [T, E], experts in the GEMM storage (w13 int32 [E, 2I/16, H/128, 16, 16], s13 fp32
+    [E, H/128, 2I], w2 int32 [E, H/16, I/128, 16, 16], s2 fp32 [E, I/128, H]) -> y [T, H] (fp32 or bf16).
+
+    ids int32 [T, k] and w fp32 [T, k], if given, receive the routing.  workspace: uint8
+    [w4a8_moe_few_workspace_bytes(T, k, I)], allocated here if not given."""
+    return _few("g128", x, logits, k, w13, s13, w2, s2, renormalize, y, y_dtype, ids, w, workspace)
+
+
+def w4a8_moe_few_i8_prepacked(x: torch.Tensor, logits: torch.Tensor, k: int, w13: torch.Tensor, s13: torch.Tensor,
+                              w2: torch.Tensor, s2: torch.Tensor, renormalize: bool = True,
+                              y: torch.Tensor | None = None, y_dtype: torch.dtype = torch.float32,
+                              ids: torch.Tensor | None = None, w: torch.Tensor | None = None,
+                              workspace: torch.Tensor | None = None):
+    """The per-channel INT4 x INT8 form of w4a8_moe_few_prepacked (s13 fp32 [E, 2I], s2 fp32 [E, H])."""
+    return _few("i8", x, logits, k, w13, s13, w2, s2, renormalize, y, y_dtype, ids, w, workspace)
+
+
+def w4a8_moe_few_mxfp4_prepacked(x: torch.Tensor, logits: torch.Tensor, k: int, w13: torch.Tensor, s13: torch.Tensor,
+                                 w2: torch.Tensor, s2: torch.Tensor, renormalize: bool = True,
+                                 y: torch.Tensor | None = None, y_dtype: torch.dtype = torch.float32,
+                                 ids: torch.Tensor | None = None, w: torch.Tensor | None = None,
+                                 workspace: torch.Tensor | None = None):
+    """The MXFP4 form of w4a8_moe_few_prepacked (w13 uint8 [E, 2I/16, H/128, 16, 64], s13 uint8 [E, H/128, 2I, 4];
+    w2 and s2 alike)."""
+    return _few("mxfp4", x, logits, k, w13, s13, w2, s2, renormalize, y, y_dtype, ids, w, workspace)
+
+
+def _matvec(name, form, prepacked, x, w, s, y, y_dtype):
+    _need_x(x)
+    dev = x.device
+    T, K = x.shape
+    wdt = torch.uint8 if form == "mxfp4" else torch.int32
+    _need(w, "w", wdt, 4 if prepacked else 2, dev)
+    if prepacked:
+        NB, G, sixteen, last = w.shape
+        N, kw = 16 * NB, 128 * G
+        if (sixteen, last) != (16, 64 if form == "mxfp4" else 16):
+            raise ValueError("w must be one matrix of the GEMM storage, [N/16, K/128, 16, "
+                             f"{64 if form == 'mxfp4' else 16}]")
+    else:
+        N, kw = w.shape[0], w.shape[1] * (2 if form == "mxfp4" else 8)
+    if kw != K:
+        raise ValueError(f"w holds rows of {kw}, x rows of {K}")
+    if form == "channel":
+        want = (N,)
+    elif form == "mxfp4":
+        want = (K // 128, N, 4) if prepacked else (N, K // 32)
+    else:
+        want = (K // 128, N) if prepacked else (N, K // 128)
+    _need(s, "s", torch.uint8 if form == "mxfp4" else torch.float32, len(want), dev)
+    if tuple(s.shape) != want:
+        raise ValueError(f"s must be {list(want)}, got {list(s.shape)}")
+    y, code = _y(y, y_dtype, T, N, dev)
+    _call_on(dev, name, _p(x), T, K, _ld(x), _p(w), _p(s), N, _p(y), code)
+    return y
+
+
+def w4a8_moe_matvec(x: torch.Tensor, w: torch.Tensor, s: torch.Tensor, y: torch.Tensor | None = None,
+                    y_dtype: torch.dtype = torch.float32):
+    """x bf16 [T, K] (T <= 16, rows any multiple of 8 elements apart, not quantized) times one stored INT4 matrix
+    (w int32 [N, K/8], s fp32 [N, K/128]) -> y [T, N] (fp32 or bf16)."""
+    return _matvec("w4a8_moe_matvec", "g128", False, x, w, s, y, y_dtype)
+
+
+def w4a8_moe_matvec_prepacked(x: torch.Tensor, w: torch.Tensor, s: torch.Tensor, y: torch.Tensor | None = None,
+                              y_dtype: torch.dtype = torch.float32):
+    """The same on one matrix of the GEMM storage (w int32 [N/16, K/128, 16, 16], s fp32 [K/128, N]): expert e of
+    w4a8_moe_prepack_int4's arrays."""
+    return _matvec("w4a8_moe_matvec_prepacked", "g128", True, x, w, s, y, y_dtype)
+
+
+def w4a8_moe_matvec_channel(x: torch.Tensor, w: torch.Tensor, s: torch.Tensor, y: torch.Tensor | None = None,
+                            y_dtype: torch.dtype = torch.float32):
+    """w4a8_moe_matvec with per-channel scales s fp32 [N]."""
+    return _matvec("w4a8_moe_matvec_channel", "channel", False, x, w, s, y, y_dtype)
+
+
+def w4a8_moe_matvec_channel_prepacked(x: torch.Tensor, w: torch.Tensor, s: torch.Tensor,
+                                      y: torch.Tensor | None = None, y_dtype: torch.dtype = torch.float32):
+    """The same on the GEMM storage of the weights."""
+    return _matvec("w4a8_moe_matvec_channel_prepacked", "channel", True, x, w, s, y, y_dtype)
+
+
+def w4a8_moe_matvec_mxfp4(x: torch.Tensor, w: torch.Tensor, s: torch.Tensor, y: torch.Tensor | None = None,
+                          y_dtype: torch.dtype = torch.float32):
+    """w4a8_moe_matvec on one stored MXFP4 matrix (w uint8 [N, K/2], s uint8 [N, K/32]; K % 32 == 0)."""
+    return _matvec("w4a8_moe_matvec_mxfp4", "mxfp4", False, x, w, s, y, y_dtype)
+
+
+def w4a8_moe_matvec_mxfp4_prepacked(x: torch.Tensor, w: torch.Tensor, s: torch.Tensor,
+                                    y: torch.Tensor | None = None, y_dtype: torch.dtype = torch.float32):
+    """The same on the GEMM storage (w uint8 [N/16, K/128, 16, 64], s uint8 [K/128, N, 4])."""
+    return _matvec("w4a8_moe_matvec_mxfp4_prepacked", "mxfp4", True, x, w, s, y, y_dtype)
