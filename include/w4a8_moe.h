@@ -600,8 +600,8 @@ int w4a8_moe_grouped_gemm_swiglu_mxfp4_prepacked(const uint8_t* a, const float* 
  *               aligned (contents need no initialisation; calls that overlap must not
  *               share one).
  *   Rules     : 0 <= T <= 16, 1 <= k <= E <= 1024, T*k <= 256, H > 0, H % 128 == 0,
- *               H <= 8192, T*H <= 114688, I > 0, I % 128 == 0.  Larger batches take the
- *               seven calls.
+ *               H <= 8192, T*H <= 114688, 0 < I <= 65536, I % 128 == 0.  Larger batches
+ *               take the seven calls.
  *   Logits of -infinity rank last and get weight zero.  Whatever the logits hold,
  *   every id written is in [0, E) and no memory outside the arrays is touched.
  */
@@ -644,8 +644,9 @@ int w4a8_moe_few_mxfp4_prepacked(const uint16_t* x_bf16, int64_t T, int64_t H, i
  *             fp32 scales and the GEMM storage's E8M0 words 4-byte aligned.
  *   y       : [T][N], fp32 or bf16 (y_dtype; rounded to nearest even), aligned to its
  *             elements.
- *   Rules   : 0 <= T <= 16; K > 0, K % 128 == 0 (stored MXFP4: K % 32 == 0); N > 0,
- *             _prepacked: N % 16 == 0.  Larger batches take the grouped GEMMs.
+ *   Rules   : 0 <= T <= 16; 0 < K <= 2^22, K % 128 == 0 (stored MXFP4: K % 32 == 0);
+ *             0 < N <= 2^24, _prepacked: N % 16 == 0.  Larger batches take the grouped
+ *             GEMMs.
  */
 int w4a8_moe_matvec(const uint16_t* x_bf16, int64_t T, int64_t K, int64_t ld_x, const int32_t* w_packed,
                     const float* w_scale, int64_t N, void* y, int32_t y_dtype, void* stream);

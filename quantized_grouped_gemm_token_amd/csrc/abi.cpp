@@ -647,7 +647,7 @@ int w4a8_moe_combine(const float* o_tok, const int32_t* inv_pos, int64_t T, int3
 // ---- the whole layer for a few tokens
 int64_t w4a8_moe_few_workspace_bytes(int64_t T, int32_t k, int64_t I) {
   if (T < 0 || T > w4a8::kFewMaxTokens || k < 1 || T * (int64_t)k > w4a8::kFewMaxRows || I <= 0 || I % 128 ||
-      I >= kMaxRows)
+      I > w4a8::kFewMaxI)
     return -1;
   return w4a8::few_workspace_bytes(T * (int64_t)k, I);
 }
@@ -668,8 +668,9 @@ static int run_few(const char* name, Form form, const uint16_t* x, int64_t T, in
                 (long long)H, (long long)w4a8::kFewMaxH, (long long)w4a8::kFewMaxCodes);
   if (ld_x < H || ld_x % 8)
     return fail(W4A8_ERR_SHAPE, "%s: ld_x=%lld must be >= H and a multiple of 8", name, (long long)ld_x);
-  if (I <= 0 || I % 128 || I >= kMaxRows)
-    return fail(W4A8_ERR_SHAPE, "%s: I=%lld must be a positive multiple of 128", name, (long long)I);
+  if (I <= 0 || I % 128 || I > w4a8::kFewMaxI)
+    return fail(W4A8_ERR_SHAPE, "%s: I=%lld must be a positive multiple of 128 up to %lld", name, (long long)I,
+                (long long)w4a8::kFewMaxI);
   if (y_dtype != W4A8_Y_F32 && y_dtype != W4A8_Y_BF16)
     return fail(W4A8_ERR_SHAPE, "%s: y_dtype=%d must be W4A8_Y_F32 or W4A8_Y_BF16", name, y_dtype);
   if (T == 0) return ok();
@@ -721,15 +722,15 @@ static int run_matvec(const char* name, Form form, bool row_major, const uint16_
   if (T < 0 || T > w4a8::kMatvecMaxTokens)
     return fail(W4A8_ERR_SHAPE, "%s: T=%lld must be in [0, %d]", name, (long long)T, w4a8::kMatvecMaxTokens);
   const int64_t kmult = form == Form::kMx && row_major ? 32 : 128;
-  if (K <= 0 || K % kmult || K >= kMaxRows)
-    return fail(W4A8_ERR_SHAPE, "%s: K=%lld must be a positive multiple of %lld", name, (long long)K,
-                (long long)kmult);
+  if (K <= 0 || K % kmult || K > w4a8::kMatvecMaxK)
+    return fail(W4A8_ERR_SHAPE, "%s: K=%lld must be a positive multiple of %lld up to %lld", name, (long long)K,
+                (long long)kmult, (long long)w4a8::kMatvecMaxK);
   if (ld_x < K || ld_x % 8)
     return fail(W4A8_ERR_SHAPE, "%s: ld_x=%lld must be >= K and a multiple of 8", name, (long long)ld_x);
   const int64_t nmult = row_major ? 1 : 16;
-  if (N <= 0 || N % nmult || N >= kMaxRows)
-    return fail(W4A8_ERR_SHAPE, "%s: N=%lld must be a positive multiple of %lld", name, (long long)N,
-                (long long)nmult);
+  if (N <= 0 || N % nmult || N > w4a8::kMatvecMaxN)
+    return fail(W4A8_ERR_SHAPE, "%s: N=%lld must be a positive multiple of %lld up to %lld", name, (long long)N,
+                (long long)nmult, (long long)w4a8::kMatvecMaxN);
   if (y_dtype != W4A8_Y_F32 && y_dtype != W4A8_Y_BF16)
     return fail(W4A8_ERR_SHAPE, "%s: y_dtype=%d must be W4A8_Y_F32 or W4A8_Y_BF16", name, y_dtype);
   if (T == 0) return ok();

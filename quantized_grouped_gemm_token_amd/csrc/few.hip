@@ -44,22 +44,19 @@ __device__ __forceinline__ float div_by(float x, float s, float r) {
 
 // four codes of four values of a row with scale s (r = 1 / s), the first in byte 0.
 // The FP8 conversion instruction rounds to nearest even like e4m3_encode (equal on
-// every fp32 magnitude up to 448); quotients a rounding above 448 are clamped.
+// every fp32 magnitude up to 448).  No clamp: a quotient is at most a rounding above
+// 448 (127), which rounds to the largest code.
 template <bool kInt8>
 __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d, float s, float r) {
   const float v[4] = {div_by(a, s, r), div_by(b, s, r), div_by(c, s, r), div_by(d, s, r)};
   if constexpr (kInt8) {
     uint32_t o = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      o |= ((uint32_t)(int)fminf(fmaxf(rintf(v[i]), -127.0f), 127.0f) & 0xffu) << (8 * i);
+    for (int i = 0; i < 4; ++i) o |= ((uint32_t)(int)rintf(v[i]) & 0xffu) << (8 * i);
     return o;
   } else {
-    float u[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) u[i] = fminf(fmaxf(v[i], -kFp8Max), kFp8Max);
-    int o = __builtin_amdgcn_cvt_pk_fp8_f32(u[0], u[1], 0, false);
-    return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(u[2], u[3], o, true);
+    const int o = __builtin_amdgcn_cvt_pk_fp8_f32(v[0], v[1], 0, false);
+    return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(v[2], v[3], o, true);
   }
 }
 
@@ -95,21 +92,19 @@ __device__ __forceinline__ uint32_t wave_max_key(uint32_t v) {
   return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
 }
 
+constexpr int kRouteSlots = 16;                // 1024 experts
+
 // The k experts of a logits row and their weights, with the order, ties and sums of
 // w4a8_moe_route (the same bits): slot s of lane l is expert l + 64 s.  Every id
 // written is in [0, E), whatever the logits hold.
+// v: the row's logits, loaded before.  picked: a bit for each expert.
 template <int S>
-__device__ __forceinline__ void route_token(const float* __restrict__ lr, int E, int k, int renormalize, int* ids,
-                                            float* w) {
+__device__ __forceinline__ void route_token(const float (&v)[kRouteSlots], int E, int k, int renormalize, int* ids,
+                                            float* w, uint32_t* picked) {
   const int lane = threadIdx.x & 63;
-  float v[S];
   uint32_t key[S];
 #pragma unroll
-  for (int s = 0; s < S; ++s) {
-    const int e = lane + s * kWave;
-    v[s] = e < E ? lr[e] : 0.0f;
-    key[s] = e < E ? order_key(v[s]) : 0u;
-  }
+  for (int s = 0; s < S; ++s) key[s] = lane + s * kWave < E ? order_key(v[s]) : 0u;
   for (int j = 0; j < k; ++j) {
     uint32_t best = key[0];
 #pragma unroll
@@ -131,6 +126,7 @@ __device__ __forceinline__ void route_token(const float* __restrict__ lr, int E,
     if (lane == 0) {
       ids[j] = id;
       w[j] = key_value(best);
+      atomicOr(&picked[id >> 5], 1u << (id & 31));
     }
   }
   wave_lds_fence();
@@ -146,15 +142,6 @@ __device__ __forceinline__ void route_token(const float* __restrict__ lr, int E,
   denom = wave_sum(denom);
   wave_lds_fence();
   for (int j = lane; j < k; j += kWave) w[j] = expf(w[j] - m) / denom;
-}
-
-__device__ __forceinline__ void route_any(const float* __restrict__ lr, int E, int k, int renormalize, int* ids,
-                                          float* w) {
-  if (E <= 64) route_token<1>(lr, E, k, renormalize, ids, w);
-  else if (E <= 128) route_token<2>(lr, E, k, renormalize, ids, w);
-  else if (E <= 256) route_token<4>(lr, E, k, renormalize, ids, w);
-  else if (E <= 512) route_token<8>(lr, E, k, renormalize, ids, w);
-  else route_token<16>(lr, E, k, renormalize, ids, w);
 }
 
 // ---- what the first kernel leaves for the second ------------------------------
@@ -190,7 +177,7 @@ struct FewProduct {
   i32x4 ab[4];            // FP8 forms: the codes as bf16 operands
   v8i ai;                 // INT8 form: the codes
   Acc bias;
-  __device__ __forceinline__ void set_a(v8i a) {
+  __device__ __forceinline__ void set_codes(v8i a) {
     if constexpr (kInt8) {
       ai = a;
       const i32x4 m = {(int)0xf8f8f8f8, (int)0xf8f8f8f8, (int)0xf8f8f8f8, (int)0xf8f8f8f8};   // -8
@@ -198,9 +185,12 @@ struct FewProduct {
     } else {
 #pragma unroll
       for (int c = 0; c < 4; ++c) ab[c] = e4m3x8_to_bf16((uint32_t)a[2 * c], (uint32_t)a[2 * c + 1], 1.0f);
-      if constexpr (kForm == kFormG128) bias = minus8_product(ab);
-      else bias = Acc{0, 0, 0, 0};
+      set_bias();
     }
+  }
+  __device__ __forceinline__ void set_bias() {
+    if constexpr (kForm == kFormG128) bias = minus8_product(ab);
+    else bias = Acc{0, 0, 0, 0};
   }
   __device__ __forceinline__ void add(i32x4 w, uint32_t s, Acc& acc) const {
     if constexpr (kInt8) {
@@ -215,15 +205,15 @@ struct FewProduct {
 
 // ---- kernel 1: routing, quantization, gate/up, SwiGLU -----------------------
 // A task is 16 columns of act for one distinct expert: 16 gate and 16 up rows of
-// w13, K split over the 8 waves.  The grid walks the tasks; a wave has all of a
-// task's loads in flight, and issues the next task's as it uses them up.
-// GW: the most K groups of a wave (H <= 1024 GW).
-template <int kForm, int GW>
+// w13, K split over the 8 waves.  The workgroups walk the tasks; a wave refills each
+// weight register with the next task's as it uses it up.
+// GW: the most K groups of a wave (H <= 1024 GW).  S: logits per lane (E <= 64 S).
+template <int kForm, int GW, int S>
 __global__ __launch_bounds__(kFewThreads) void few_gate_up_kernel(const uint16_t* __restrict__ x, int T, int64_t H,
                                                                   int64_t ld, const float* __restrict__ logits, int E,
                                                                   int k, int renormalize,
                                                                   const uint8_t* __restrict__ w13,
-                                                                  const uint32_t* __restrict__ s13, int64_t I,
+                                                                  const uint8_t* __restrict__ s13, int64_t I,
                                                                   int32_t* __restrict__ ids_out,
                                                                   float* __restrict__ w_out, void* workspace) {
   using P = FewProduct<kForm>;
@@ -235,7 +225,7 @@ __global__ __launch_bounds__(kFewThreads) void few_gate_up_kernel(const uint16_t
   __shared__ int experts[kFewMaxRows];
   __shared__ __attribute__((aligned(16))) int16_t slot[kFewMaxRows][kFewMaxTokens];
   __shared__ float wave_amax[kFewMaxTokens][kFewWaves];
-  __shared__ int distinct, wave_firsts[kFewWaves];
+  __shared__ uint32_t picked[32];
 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -243,18 +233,25 @@ __global__ __launch_bounds__(kFewThreads) void few_gate_up_kernel(const uint16_t
   const int G = (int)(H >> 7), R = T * k;
   uint8_t* codes = smem;                                          // [G][4][T][32]
   float* red = reinterpret_cast<float*>(smem + (size_t)T * H);    // [2][waves][2][T][16]; int32 for INT8
-  int* first = reinterpret_cast<int*>(red);                       // [max(E, R)], before red is used
 
-  // row maxima of x: the waves share the rows, wpr waves to a row
+  // The waves share the rows of x, wpr waves to a row; every load of the prologue that
+  // depends on nothing is issued here.
   const int wpr = T == 1 ? 8 : T == 2 ? 4 : T <= 4 ? 2 : 1;       // waves per row
-  const int rows_at_once = kFewWaves / wpr;
+  const int rows_at_once = kFewWaves / wpr;                       // T <= 16: at most two rows per wave
   const int part = wave % wpr;
-  const int chunks = (int)(H >> 3);
-  for (int t0 = 0; t0 < T; t0 += rows_at_once) {
+  const int chunks = (int)(H >> 3);                               // of 8 elements
+  float lg[kRouteSlots];
+  const bool routes = wave < T;                                   // waves 0 .. T-1 route (and wave + 8 for T > 8)
+#pragma unroll
+  for (int s = 0; s < S; ++s) lg[s] = routes && lane + s * kWave < E ? logits[(int64_t)wave * E + lane + s * kWave] : 0.0f;
+  if (threadIdx.x < 32) picked[threadIdx.x] = 0u;
+  for (int i = threadIdx.x; i < R * kFewMaxTokens / 2; i += kFewThreads) reinterpret_cast<int*>(slot)[i] = -1;
+  for (int t0 = 0; t0 < T; t0 += rows_at_once) {                  // row maxima of x
     const int t = t0 + wave / wpr;
     if (t < T) {
       const uint4* xr = reinterpret_cast<const uint4*>(x + (int64_t)t * ld);
       float amax = 0.0f;
+#pragma unroll 4
       for (int c = part * 64 + lane; c < chunks; c += 64 * wpr) {
         const uint4 v = xr[c];
         const uint32_t u[4] = {v.x, v.y, v.z, v.w};
@@ -265,45 +262,79 @@ __global__ __launch_bounds__(kFewThreads) void few_gate_up_kernel(const uint16_t
       if (lane == 0) wave_amax[t][part] = amax;
     }
   }
-  for (int t = wave; t < T; t += kFewWaves)
-    route_any(logits + (int64_t)t * E, E, k, renormalize, ids + t * k, wts + t * k);
-  for (int e = threadIdx.x; e < E; e += kFewThreads) first[e] = 0x7fffffff;
-  for (int i = threadIdx.x; i < R * kFewMaxTokens / 2; i += kFewThreads) reinterpret_cast<int*>(slot)[i] = -1;
+  __syncthreads();                                                // picked and slot are set
+  if (routes) route_token<S>(lg, E, k, renormalize, ids + wave * k, wts + wave * k, picked);
+  if (wave + kFewWaves < T) {
+    const int t = wave + kFewWaves;
+#pragma unroll
+    for (int s = 0; s < S; ++s) lg[s] = lane + s * kWave < E ? logits[(int64_t)t * E + lane + s * kWave] : 0.0f;
+    route_token<S>(lg, E, k, renormalize, ids + t * k, wts + t * k, picked);
+  }
+  __syncthreads();                                                // ids, weights, picked and row maxima are there
+
+  // The distinct experts in ascending order: expert e is number (bits of picked below e).
+  // Lane l holds word l and the bits in the words before it.
+  const uint32_t word = lane < 32 ? picked[lane] : 0u;
+  int below = __builtin_popcount(word);
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int o = __shfl_up(below, off, kWave);
+    if (lane >= off) below += o;
+  }
+  const int D = __builtin_amdgcn_readlane(below, 31);
+  below -= __builtin_popcount(word);
+  const int f = threadIdx.x;                                      // R <= 256 < 512 threads
+  {
+    const int e = f < R ? ids[f] : 0;
+    const uint32_t we = (uint32_t)__shfl((int)word, e >> 5, kWave);
+    const int number = __shfl(below, e >> 5, kWave) + __builtin_popcount(we & ((1u << (e & 31)) - 1u));
+    if (f < R) {
+      slot[number][f / k] = (int16_t)f;
+      experts[number] = e;                                        // the same value from every token that picked it
+    }
+  }
   __syncthreads();
 
-  // the distinct experts in the order of their first routed index
-  const int f = threadIdx.x;                                      // R <= 256 < 512 threads
-  if (f < R) atomicMin(&first[ids[f]], f);
-  __syncthreads();
-  const bool is_first = f < R && first[ids[f]] == f;
-  const uint64_t ball = __ballot(is_first);
-  if (lane == 0) wave_firsts[wave] = __builtin_popcountll(ball);
-  __syncthreads();
-  int before = __builtin_popcountll(ball & ((1ull << lane) - 1)), all = 0;
+  const FewWorkspace ws = few_workspace(workspace, R, I);
+  const int blocks = (int)(I >> 4);                               // column blocks of act
+  const int ntasks = D * blocks;
+  const int gpw = (G + kFewWaves - 1) / kFewWaves;                // <= GW
+  const int g0 = wave * gpw, ng = max(0, min(gpw, G - g0));
+  i32x4 wg[GW], wu[GW];
+  uint32_t sg[GW], su[GW];
+  __amdgpu_buffer_rsrc_t rg = buffer_of(w13, 0), ru = rg, rs = buffer_of(s13, 0);
+  auto point = [&](int task) {                                    // the task's weights of this wave; none past the last task
+    const bool on = task < ntasks && ng > 0;
+    const int d = on ? task / blocks : 0, cb = on ? task - d * blocks : 0;
+    const int64_t e = __builtin_amdgcn_readfirstlane(experts[d]);
+    const uint8_t* p = w13 + ((e * (I >> 3) + cb) * G + g0) * 1024;
+    rg = buffer_of(p, on ? ng * 1024 : 0);
+    ru = buffer_of(p + (I >> 4) * G * 1024, on ? ng * 1024 : 0);
+    if constexpr (!kInt8) rs = buffer_of(s13 + (((e * G + g0) * 2 * I) + 16 * cb) * 4, on ? ((int64_t)ng * 2 * I - 16 * cb) * 4 : 0);
+  };
+  auto load = [&](int i) {
+    wg[i] = buffer_load16_nt(rg, col * 64 + kq * 16 + i * 1024);
+    wu[i] = buffer_load16_nt(ru, col * 64 + kq * 16 + i * 1024);
+    if constexpr (!kInt8) {
+      sg[i] = buffer_load4(rs, (uint32_t)(i * 2 * I + col) * 4);
+      su[i] = buffer_load4(rs, (uint32_t)(i * 2 * I + I + col) * 4);
+    }
+  };
+  int task = blockIdx.x, buf = 0;
+  point(task);
 #pragma unroll
-  for (int v = 0; v < kFewWaves; ++v) {
-    before += v < wave ? wave_firsts[v] : 0;
-    all += wave_firsts[v];
-  }
-  int my_first = 0;
-  if (f < R) my_first = first[ids[f]];
-  __syncthreads();                                                // first[] read by everyone: reuse it as index of f
-  if (is_first) {
-    experts[before] = ids[f];
-    first[f] = before;                                            // position of the expert first seen at f
-  }
-  if (threadIdx.x == 0) distinct = all;
-  __syncthreads();
-  if (f < R) slot[first[my_first]][f / k] = (int16_t)f;
-  if (blockIdx.x == 0) {
-    const FewWorkspace ws = few_workspace(workspace, R, I);
-    if (f == 0) *ws.count = all;
-    if (f < all) ws.experts[f] = experts[f];
+  for (int i = 0; i < GW; ++i) load(i);
+
+  if (blockIdx.x == 0) {                                          // the routing, for the second kernel and the caller
+    if (f == 0) *ws.count = D;
+    if (f < D) ws.experts[f] = experts[f];
     if (f < R) {
       ws.weights[f] = wts[f];
       if (ids_out) ids_out[f] = ids[f];
       if (w_out) w_out[f] = wts[f];
     }
+    for (int i = threadIdx.x; i < D * kFewMaxTokens / 2; i += kFewThreads)
+      reinterpret_cast<int*>(ws.slot)[i] = reinterpret_cast<const int*>(slot)[i];
   }
 
   // the codes, in operand order: byte o of lane group kq of row t, group g
@@ -325,40 +356,9 @@ __global__ __launch_bounds__(kFewThreads) void few_gate_up_kernel(const uint16_t
     }
   }
   __syncthreads();
-  const int D = distinct;
-  if (blockIdx.x == 0) {
-    const FewWorkspace ws = few_workspace(workspace, R, I);
-    for (int i = threadIdx.x; i < D * kFewMaxTokens / 2; i += kFewThreads)
-      reinterpret_cast<int*>(ws.slot)[i] = reinterpret_cast<const int*>(slot)[i];
-  }
 
-  const FewWorkspace ws = few_workspace(workspace, R, I);
-  const int blocks = (int)(I >> 4);                               // column blocks of act
-  const int ntasks = D * blocks;
-  const int gpw = (G + kFewWaves - 1) / kFewWaves;                // <= GW
-  const int g0 = wave * gpw, ng = max(0, min(gpw, G - g0));
   const uint8_t* arow = codes + ((size_t)(4 * g0 + kq) * T + min(col, T - 1)) * 32;
   const size_t astep = (size_t)128 * T;
-
-  i32x4 wg[GW], wu[GW];
-  uint32_t sg[GW], su[GW];
-  const uint8_t *pg = nullptr, *pu = nullptr;
-  const uint32_t* ps = nullptr;
-  auto point = [&](int task) {                                    // the task's weights of this wave
-    const int d = task / blocks, cb = task - d * blocks;
-    const int64_t e = experts[d];
-    pg = w13 + ((e * (I >> 3) + cb) * G + g0) * 1024 + col * 64 + kq * 16;
-    pu = pg + (I >> 4) * G * 1024;
-    if constexpr (!kInt8) ps = s13 + (e * G + g0) * 2 * I + 16 * cb + col;
-  };
-  auto load = [&](int i) {
-    wg[i] = __builtin_nontemporal_load(reinterpret_cast<const i32x4*>(pg + i * 1024));
-    wu[i] = __builtin_nontemporal_load(reinterpret_cast<const i32x4*>(pu + i * 1024));
-    if constexpr (!kInt8) {
-      sg[i] = ps[(int64_t)i * 2 * I];
-      su[i] = ps[(int64_t)i * 2 * I + I];
-    }
-  };
   // this thread's token scale (threads below 16 T finish the tiles: token threadIdx.x / 16)
   float sx = 1.0f;
   if ((int)threadIdx.x < 16 * T) {
@@ -366,22 +366,14 @@ __global__ __launch_bounds__(kFewThreads) void few_gate_up_kernel(const uint16_t
     for (int p = 0; p < wpr; ++p) amax = fmaxf(amax, wave_amax[threadIdx.x >> 4][p]);
     sx = row_scale<kInt8>(amax);
   }
-  int task = blockIdx.x, buf = 0;
-  if (task < ntasks) {
-    point(task);
-#pragma unroll
-    for (int i = 0; i < GW; ++i)
-      if (i < ng) load(i);
-  }
   for (; task < ntasks; task += gridDim.x, buf ^= 1) {
-    const bool more = task + (int)gridDim.x < ntasks;
-    if (more) point(task + gridDim.x);
+    point(task + (int)gridDim.x);
     Acc ag = Acc{0, 0, 0, 0}, au = Acc{0, 0, 0, 0};
 #pragma unroll
     for (int i = 0; i < GW; ++i) {
       if (i < ng) {
         P p;
-        p.set_a(*reinterpret_cast<const v8i*>(arow + i * astep));
+        p.set_codes(*reinterpret_cast<const v8i*>(arow + i * astep));
         uint32_t fg = 0, fu = 0;
         if constexpr (!kInt8) {
           fg = kForm == kFormMx ? (sg[i] >> (8 * kq)) & 0xffu : sg[i];
@@ -389,8 +381,8 @@ __global__ __launch_bounds__(kFewThreads) void few_gate_up_kernel(const uint16_t
         }
         p.add(wg[i], fg, ag);
         p.add(wu[i], fu, au);
-        if (more) load(i);
       }
+      load(i);
     }
     // the partial tiles: red[buf][wave][gate, up][t][col]
     float* rb = red + (size_t)buf * kFewWaves * 2 * T * 16;
@@ -448,35 +440,90 @@ __global__ __launch_bounds__(kFewThreads) void few_gate_up_kernel(const uint16_t
 
 // ---- kernel 2: requantization, down, the routing-weighted sum ----------------
 // A workgroup owns 16 columns of y for every token.  Its waves take the (distinct
-// expert, 4-group K chunk) pieces in turn: each requantizes its routed tokens' act
-// of those K elements into LDS of its own, multiplies, and adds the result to its
-// 16x16 tile of y with the factor w[t, j] sa[f] of each routed token.
+// expert, 4-group K chunk) pieces in turn: each requantizes the act of the expert's
+// tokens over those K elements into LDS of its own, up to 4 tokens at a time as rows
+// 0..3 of the A operand (an expert has one or two of the few tokens as a rule; the
+// weights stay in registers for the next 4), multiplies, and adds the rows with the
+// factors w[t, j] sa[f] to its own sums of y in LDS.  The next piece's weights, and
+// the act of its first two tokens, are loaded meanwhile.
+// The FP8 codes are held as the bf16 values they stand for: converting them once per
+// token and piece instead of once per operand read takes 16 of about 80 instructions
+// out of a K group's product, which are what bounds this kernel besides HBM.
 template <int kForm>
 __global__ __launch_bounds__(kFewThreads) void few_down_kernel(int T, int64_t H, int k, const uint8_t* __restrict__ w2,
-                                                               const uint32_t* __restrict__ s2, int64_t I,
+                                                               const uint8_t* __restrict__ s2, int64_t I,
                                                                const void* __restrict__ workspace,
                                                                void* __restrict__ y, int y_bf16) {
   using P = FewProduct<kForm>;
   using Acc = typename P::Acc;
   constexpr bool kInt8 = P::kInt8;
   constexpr int CG = kFewDownGroups;
-  extern __shared__ __attribute__((aligned(16))) unsigned char smem[];   // [waves][CG][4][T][32], then [waves][T][16] floats
+  constexpr int kRows = 4;                                               // rows of A in use
+  constexpr int kQuads = CG * kGroup / 4 / 64;                           // float4 of act per lane, token and piece
+  // the wave's A rows: FP8 forms [CG][4 products][4 lane groups][rows][16 bytes], INT8 form [CG][4][rows][32 bytes]
+  __shared__ __attribute__((aligned(16))) uint8_t a_sm[kFewWaves][CG * kGroup * kRows * (kInt8 ? 1 : 2)];
   __shared__ float scale[kFewMaxRows], factor[kFewMaxRows];              // sa[f], w[f] sa[f]
-  __shared__ __attribute__((aligned(16))) int16_t slot[kFewMaxRows][kFewMaxTokens];
   __shared__ int experts[kFewMaxRows];
+  __shared__ uint32_t routed[kFewMaxRows];                               // bit t: token t picked the expert
+  __shared__ __attribute__((aligned(16))) int16_t slot[kFewMaxRows][kFewMaxTokens];
+  extern __shared__ float y_sm[];                                        // [waves][T][16]
 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 15, kq = lane >> 4;
   const int G = (int)(I >> 7), R = T * k;
+  const int nch = (G + CG - 1) / CG;                                     // K chunks of an expert
   const int64_t cb = blockIdx.x;
   const FewWorkspace ws = few_workspace(const_cast<void*>(workspace), R, I);
-  const int D = *ws.count;
+
+  // The weights of a piece, and the act of two of its tokens.  Loads past the last piece,
+  // or of a token that is not there, read nothing.
+  i32x4 w[CG];
+  uint32_t s[CG];
+  float4 av0[kQuads], av1[kQuads];
+  __amdgpu_buffer_rsrc_t rw, rs;
+  auto point = [&](int64_t e, int g0, bool on) {
+    const int n = min(CG, G - g0);
+    rw = buffer_of(w2 + ((e * (H >> 4) + cb) * G + g0) * 1024, on ? n * 1024 : 0);
+    if constexpr (!kInt8) rs = buffer_of(s2 + ((e * G + g0) * H + 16 * cb) * 4, on ? (n * H - 16 * cb) * 4 : 0);
+  };
+  auto load = [&](int i) {
+    w[i] = buffer_load16_nt(rw, col * 64 + kq * 16 + i * 1024);
+    if constexpr (!kInt8) s[i] = buffer_load4(rs, (uint32_t)(i * H + col) * 4);
+  };
+  auto load_act = [&](float4 (&v)[kQuads], int f, int g0) {              // f < 0: nothing
+    const __amdgpu_buffer_rsrc_t ra = buffer_of(ws.act + (int64_t)max(f, 0) * I + (int64_t)g0 * kGroup,
+                                                f >= 0 ? min(CG, G - g0) * kGroup * 4 : 0);
+#pragma unroll
+    for (int q = 0; q < kQuads; ++q)
+      v[q] = __builtin_bit_cast(float4, __builtin_amdgcn_raw_buffer_load_b128(ra, (lane + 64 * q) * 16, 0, 0));
+  };
+  // the first piece of the wave, from what the first kernel left in memory
+  const int items = __builtin_amdgcn_readfirstlane(*ws.count) * nch;
+  {
+    const bool on = wave < items;
+    const int d = on ? wave / nch : 0, g0 = on ? (wave - d * nch) * CG : 0;
+    const int e = __builtin_amdgcn_readfirstlane(ws.experts[d]);
+    const int f = ws.slot[(int64_t)d * kFewMaxTokens + col];
+    const uint32_t any = (uint32_t)__ballot(f >= 0) & 0xffffu, rest = any & (any - 1);
+    const int f0 = __builtin_amdgcn_readlane(f, any ? __builtin_ctz(any) : 0);
+    const int f1 = __builtin_amdgcn_readlane(f, rest ? __builtin_ctz(rest) : 0);
+    load_act(av0, on && any ? f0 : -1, g0);
+    load_act(av1, on && rest ? f1 : -1, g0);
+    point(e, g0, on);
+#pragma unroll
+    for (int i = 0; i < CG; ++i) load(i);
+  }
+  const int D = items / nch;
   for (int i = threadIdx.x; i < D; i += kFewThreads) experts[i] = ws.experts[i];
-  for (int i = threadIdx.x; i < D * kFewMaxTokens / 2; i += kFewThreads)
-    reinterpret_cast<int*>(slot)[i] = reinterpret_cast<const int*>(ws.slot)[i];
+  for (int i = threadIdx.x; i < D * kFewMaxTokens; i += kFewThreads) {   // 16 lanes per expert
+    const int f = ws.slot[i];
+    slot[i >> 4][i & 15] = (int16_t)f;
+    const uint64_t any = __ballot(f >= 0);
+    if ((i & 15) == 0) routed[i >> 4] = (uint32_t)(any >> (lane & 48)) & 0xffffu;
+  }
   const int blocks = (int)(I >> 4);
-  for (int f = wave; f < R; f += kFewWaves) {                     // the row maxima
+  for (int f = wave; f < R; f += kFewWaves) {                            // the row maxima
     float m = 0.0f;
     for (int b = lane; b < blocks; b += 64) m = fmaxf(m, ws.pmax[(int64_t)f * blocks + b]);
     m = wave_max(m);
@@ -486,114 +533,158 @@ __global__ __launch_bounds__(kFewThreads) void few_down_kernel(int T, int64_t H,
       factor[f] = ws.weights[f] * sa;
     }
   }
+  for (int i = threadIdx.x; i < kFewWaves * T * 16; i += kFewThreads) y_sm[i] = 0.0f;
   __syncthreads();
 
-  const int nch = (G + CG - 1) / CG;                              // K chunks of an expert
-  const int items = D * nch;
-  uint8_t* mine = smem + (size_t)wave * CG * 128 * T;             // this wave's codes
-  const uint8_t* arow = mine + ((size_t)kq * T + min(col, T - 1)) * 32;
-
-  i32x4 w[CG], wn[CG];
-  uint32_t s[CG], sn[CG];
-  auto load = [&](int it, i32x4 (&wv)[CG], uint32_t (&sv)[CG]) {
-    const int d = it / nch, g0 = (it - d * nch) * CG;
-    const int64_t e = experts[d];
-    const uint8_t* p = w2 + ((e * (H >> 4) + cb) * G + g0) * 1024 + col * 64 + kq * 16;
-    const uint32_t* ps = s2 + (e * G + g0) * H + 16 * cb + col;
+  uint8_t* mine = a_sm[wave];
+  float* ymine = y_sm + (size_t)wave * T * 16;
+  auto put = [&](const float4 (&v)[kQuads], int row, int f) {            // one token's codes of a piece
+    const float sc = scale[f], rc = 1.0f / sc;
 #pragma unroll
-    for (int i = 0; i < CG; ++i) {
-      if (g0 + i < G) {
-        wv[i] = __builtin_nontemporal_load(reinterpret_cast<const i32x4*>(p + i * 1024));
-        if constexpr (!kInt8) sv[i] = ps[(int64_t)i * H];
+    for (int i = 0; i < kQuads; ++i) {
+      // 4 elements: group q / 32, lane group (q / 8) % 4, elements 4 (q % 8) of its 32 (past the piece's
+      // groups: zeros, which nothing reads)
+      const int q = lane + 64 * i;
+      const uint32_t c4 = codes4<kInt8>(v[i].x, v[i].y, v[i].z, v[i].w, sc, rc);
+      if constexpr (kInt8) {
+        *reinterpret_cast<uint32_t*>(mine + ((q >> 3) * kRows + row) * 32 + 4 * (q & 7)) = c4;
+      } else {
+        uint2 b;
+        b.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c4, 1.0f, false));
+        b.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c4, 1.0f, true));
+        const int g = q >> 5, c = (q & 7) >> 1, l = (q >> 3) & 3;
+        *reinterpret_cast<uint2*>(mine + (((g * 4 + c) * 4 + l) * kRows + row) * 16 + 8 * (q & 1)) = b;
       }
     }
   };
-  v4f yacc = {0.f, 0.f, 0.f, 0.f};
-  if (wave < items) load(wave, w, s);
-  for (int it = wave; it < items; it += kFewWaves) {
-    const int d = it / nch, g0 = (it - d * nch) * CG, ng = min(CG, G - g0);
-    if (it + kFewWaves < items) load(it + kFewWaves, wn, sn);
-    for (int t = 0; t < T; ++t) {
-      const int f = __builtin_amdgcn_readfirstlane((int)slot[d][t]);
-      if (f < 0) continue;
-      const float sc = scale[f], rc = 1.0f / sc;
-      const float4* ar = reinterpret_cast<const float4*>(ws.act + (int64_t)f * I + (int64_t)g0 * kGroup);
-      for (int q = lane; q < ng * 32; q += 64) {                  // 4 elements each: group q / 32, lane group (q / 8) % 4
-        const float4 v = ar[q];
-        *reinterpret_cast<uint32_t*>(mine + ((size_t)(q >> 3) * T + t) * 32 + 4 * (q & 7)) =
-            codes4<kInt8>(v.x, v.y, v.z, v.w, sc, rc);
-      }
+  // rows of A: the tokens of `set` from row `row` on, their act loaded here
+  auto put_rest = [&](uint32_t set, int d, int row, int g0) {
+    for (; set && row < kRows; set &= set - 1, ++row) {
+      const int f = __builtin_amdgcn_readfirstlane((int)slot[d][__builtin_ctz(set)]);
+      load_act(av0, f, g0);
+      put(av0, row, f);
     }
-    wave_lds_fence();
-    Acc acc = Acc{0, 0, 0, 0};
+    return set;
+  };
+  auto product = [&](int i, Acc& acc, int rows) {
+    const int row = col < rows ? col : 0;
+    P p;
+    if constexpr (kInt8) {
+      p.set_codes(*reinterpret_cast<const v8i*>(mine + ((i * 4 + kq) * kRows + row) * 32));
+    } else {
 #pragma unroll
-    for (int i = 0; i < CG; ++i) {
-      if (i < ng) {
-        P p;
-        p.set_a(*reinterpret_cast<const v8i*>(arow + (size_t)i * 128 * T));
-        uint32_t fs = 0;
-        if constexpr (!kInt8) fs = kForm == kFormMx ? (s[i] >> (8 * kq)) & 0xffu : s[i];
-        p.add(w[i], fs, acc);
-      }
+      for (int c = 0; c < 4; ++c)
+        p.ab[c] = *reinterpret_cast<const i32x4*>(mine + (((i * 4 + c) * 4 + kq) * kRows + row) * 16);
+      p.set_bias();
     }
+    uint32_t fs = 0;
+    if constexpr (!kInt8) fs = kForm == kFormMx ? (s[i] >> (8 * kq)) & 0xffu : s[i];
+    p.add(w[i], fs, acc);
+  };
+  // row r of the tile (lanes 0..15) to the sums of the r-th token of `set`
+  auto add_rows = [&](const Acc& acc, uint32_t set, int d) {
     float ws_n = 1.0f;
     if constexpr (kInt8) ws_n = reinterpret_cast<const float*>(s2)[(int64_t)experts[d] * H + 16 * cb + col];
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int t = 4 * kq + r;
-      const int f = t < T ? (int)slot[d][t] : -1;
-      // a token that did not pick the expert multiplied whatever the LDS held: dropped here
-      if (f >= 0) yacc[r] = fmaf(factor[f], kInt8 ? (float)acc[r] * ws_n : (float)acc[r], yacc[r]);
+    for (int r = 0; r < kRows; ++r) {
+      if (set) {
+        const int t = __builtin_ctz(set);
+        set &= set - 1;
+        if (lane < 16) {
+          float* at = ymine + t * 16 + col;
+          *at = fmaf(factor[slot[d][t]], kInt8 ? (float)acc[r] * ws_n : (float)acc[r], *at);
+        }
+      }
+    }
+  };
+  for (int it = wave; it < items; it += kFewWaves) {
+    const int d = it / nch, g0 = (it - d * nch) * CG, ng = min(CG, G - g0);
+    uint32_t tokens = __builtin_amdgcn_readfirstlane(routed[d]);         // at least one bit
+    int rows = min(__builtin_popcount(tokens), kRows);
+    put(av0, 0, __builtin_amdgcn_readfirstlane((int)slot[d][__builtin_ctz(tokens)]));
+    uint32_t next = tokens & (tokens - 1);
+    if (next) {
+      put(av1, 1, __builtin_amdgcn_readfirstlane((int)slot[d][__builtin_ctz(next)]));
+      next = put_rest(next & (next - 1), d, 2, g0);
+    }
+    while (next) {                                                       // more than 4 tokens: the same weights again
+      // (opaque here: hoisted out of the loop, the unpacked weights would take a third more registers)
+#pragma unroll
+      for (int i = 0; i < CG; ++i) asm volatile("" : "+v"(w[i]));
+      wave_lds_fence();
+      Acc acc = Acc{0, 0, 0, 0};
+#pragma unroll
+      for (int i = 0; i < CG; ++i)
+        if (i < ng) product(i, acc, rows);
+      add_rows(acc, tokens, d);
+      wave_lds_fence();
+      tokens = next;
+      rows = min(__builtin_popcount(tokens), kRows);
+      next = put_rest(tokens, d, 0, g0);
     }
     wave_lds_fence();
+    {
+      const int nx = it + kFewWaves;
+      const bool on = nx < items;
+      const int dn = on ? nx / nch : 0, gn = on ? (nx - dn * nch) * CG : 0;
+      const uint32_t tn = __builtin_amdgcn_readfirstlane(routed[dn]), rest = tn & (tn - 1);
+      const int f0 = __builtin_amdgcn_readfirstlane((int)slot[dn][__builtin_ctz(tn)]);
+      const int f1 = __builtin_amdgcn_readfirstlane((int)slot[dn][rest ? __builtin_ctz(rest) : 0]);
+      load_act(av0, on ? f0 : -1, gn);
+      load_act(av1, on && rest ? f1 : -1, gn);
+      point(__builtin_amdgcn_readfirstlane(experts[dn]), gn, on);
+    }
+    Acc acc = Acc{0, 0, 0, 0};
 #pragma unroll
     for (int i = 0; i < CG; ++i) {
-      w[i] = wn[i];
-      s[i] = sn[i];
+      if (i < ng) product(i, acc, rows);
+      load(i);
     }
+    add_rows(acc, tokens, d);
+    wave_lds_fence();
   }
-  __syncthreads();                                                // the codes are done with: reuse the LDS
-  float* red = reinterpret_cast<float*>(smem);
-#pragma unroll
-  for (int r = 0; r < 4; ++r)
-    if (4 * kq + r < T) red[((size_t)wave * T + 4 * kq + r) * 16 + col] = yacc[r];
   __syncthreads();
   if ((int)threadIdx.x < 16 * T) {
     const int t = threadIdx.x >> 4, c = threadIdx.x & 15;
     float sum = 0.0f;
 #pragma unroll
-    for (int v = 0; v < kFewWaves; ++v) sum += red[((size_t)v * T + t) * 16 + c];
+    for (int v = 0; v < kFewWaves; ++v) sum += y_sm[((size_t)v * T + t) * 16 + c];
     if (y_bf16) static_cast<uint16_t*>(y)[(int64_t)t * H + 16 * cb + c] = __builtin_bit_cast(uint16_t, (__bf16)sum);
     else static_cast<float*>(y)[(int64_t)t * H + 16 * cb + c] = sum;
   }
 }
 
 // ---- launches ------------------------------------------------------------------
-template <int kForm, int GW>
+template <int kForm, int GW, int S>
 static hipError_t launch_few_form(const FewArgs& a, hipStream_t stream) {
   const int64_t R = a.T * a.k;
-  const int64_t tasks = (R < a.E ? R : (int64_t)a.E) * (a.I >> 4);       // at most
+  const int64_t tasks = (R < a.E ? R : a.E) * (a.I >> 4);                // at most
   const unsigned grid = (unsigned)(tasks < 512 ? tasks : 512);
   const size_t smem = (size_t)few_gate_up_smem(a.T, a.H);
-  hipLaunchKernelGGL((few_gate_up_kernel<kForm, GW>), dim3(grid), dim3(kFewThreads), smem, stream, a.x, (int)a.T, a.H,
+  hipLaunchKernelGGL((few_gate_up_kernel<kForm, GW, S>), dim3(grid), dim3(kFewThreads), smem, stream, a.x, (int)a.T, a.H,
                      a.ld, a.logits, a.E, a.k, a.renormalize, static_cast<const uint8_t*>(a.w13),
-                     static_cast<const uint32_t*>(a.s13), a.I, a.ids, a.w, a.workspace);
+                     static_cast<const uint8_t*>(a.s13), a.I, a.ids, a.w, a.workspace);
   if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
-  const size_t smem2 = (size_t)kFewWaves * kFewDownGroups * 128 * a.T;
+  const size_t smem2 = (size_t)kFewWaves * a.T * 16 * sizeof(float);
   hipLaunchKernelGGL((few_down_kernel<kForm>), dim3((unsigned)(a.H >> 4)), dim3(kFewThreads), smem2, stream, (int)a.T,
-                     a.H, a.k, static_cast<const uint8_t*>(a.w2), static_cast<const uint32_t*>(a.s2), a.I,
+                     a.H, a.k, static_cast<const uint8_t*>(a.w2), static_cast<const uint8_t*>(a.s2), a.I,
                      a.workspace, a.y, a.y_bf16);
   return hipGetLastError();
+}
+
+template <int kForm, int GW>
+static hipError_t launch_few_experts(const FewArgs& a, hipStream_t stream) {
+  if (a.E <= 256) return launch_few_form<kForm, GW, 4>(a, stream);
+  return launch_few_form<kForm, GW, kRouteSlots>(a, stream);
 }
 
 template <int kForm>
 static hipError_t launch_few_groups(const FewArgs& a, hipStream_t stream) {
   const int64_t gpw = (a.H / kGroup + kFewWaves - 1) / kFewWaves;
-  if (gpw <= 1) return launch_few_form<kForm, 1>(a, stream);
-  if (gpw <= 2) return launch_few_form<kForm, 2>(a, stream);
-  if (gpw <= 4) return launch_few_form<kForm, 4>(a, stream);
-  if (gpw <= 6) return launch_few_form<kForm, 6>(a, stream);
-  return launch_few_form<kForm, 8>(a, stream);
+  if (gpw <= 2) return launch_few_experts<kForm, 2>(a, stream);
+  if (gpw <= 4) return launch_few_experts<kForm, 4>(a, stream);
+  if (gpw <= 6) return launch_few_experts<kForm, 6>(a, stream);
+  return launch_few_experts<kForm, 8>(a, stream);
 }
 
 hipError_t launch_few(const FewArgs& a, hipStream_t stream) {

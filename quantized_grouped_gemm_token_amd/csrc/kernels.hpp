@@ -112,8 +112,9 @@ constexpr int64_t kFewMaxCodes = 112 << 10;
 // the workspace: the routing (count, experts, weights, slots), then act [R][I] and its block maxima [R][I/16]
 constexpr int64_t kFewHeadBytes = 16 + 8 * kFewMaxRows + 2 * kFewMaxRows * kFewMaxTokens;
 constexpr int64_t few_workspace_bytes(int64_t R, int64_t I) { return kFewHeadBytes + 4 * R * (I + I / 16); }
-// dynamic LDS of the first kernel: the codes, then two buffers of partial tiles (or 1024 ints)
-constexpr int64_t few_gate_up_smem(int64_t T, int64_t H) { return T * H + (T >= 2 ? 2048 * T : 4096); }
+// dynamic LDS of the first kernel: the codes, then two buffers of partial tiles
+constexpr int64_t few_gate_up_smem(int64_t T, int64_t H) { return T * H + 2048 * T; }
+constexpr int64_t kFewMaxI = 65536;      // byte offsets of an expert's scales stay below 2^31
 struct FewArgs {
   int form;               // WeightForm
   const uint16_t* x;
@@ -134,6 +135,7 @@ struct FewArgs {
 hipError_t launch_few(const FewArgs& f, hipStream_t stream);
 // y [T][N] = x [T][K] (bf16) times 4-bit weights (matvec.hip), T <= kMatvecMaxTokens
 constexpr int kMatvecMaxTokens = 16;
+constexpr int64_t kMatvecMaxN = (int64_t)1 << 24, kMatvecMaxK = (int64_t)1 << 22;   // 32-bit offsets within 32 rows
 struct MatvecArgs {
   int form;               // WeightForm
   bool row_major;

@@ -1,14 +1,15 @@
 // Matrix-vector products with 4-bit weights: y[t, n] = sum_k x[t, k] w[n, k] for
 // 1 to 16 bf16 activation rows, the activations as they are (no quantization).
 //
-// Bound by reading the weights once.  A workgroup owns 16 NS weight rows (output
-// columns) and its 8 waves split K: wave v takes the K groups v gpw .. +gpw of
-// every subtile, so a projection of a few thousand outputs still puts 8 loads
-// in flight for every 16 rows.  Each wave multiplies on the bf16 matrix cores
-// (w4_bf16.hpp); the eight partial 16x16 tiles meet in LDS and are summed in wave
-// order (fp32; the same bits at every run).
-// The activation rows come from the cache for each group: 64 bytes per lane, rows
-// past T repeating row T - 1 (their products are never stored).
+// Bound by reading the weights once.  A step is 16 NS weight rows (output columns);
+// the 8 waves of a workgroup split its K: wave v takes up to GW K groups of every
+// subtile, so a projection of a few thousand outputs still puts 8 waves on every 16
+// rows.  The workgroups walk the steps; a wave holds its part of the activations in
+// registers as matrix-core operands (w4_bf16.hpp) for all of them, and refills each
+// weight register with the next step's as it is used up, so that a step's loads are
+// in flight while the one before is multiplied and summed.  The eight partial 16x16
+// tiles meet in LDS and are summed in wave order (fp32; the same bits at every run).
+// Rows of A past T repeat row T - 1; their products are never stored.
 #include "kernels.hpp"
 #include "w4_bf16.hpp"
 
@@ -17,92 +18,160 @@ namespace w4a8 {
 constexpr int kMvWaves = 8;
 constexpr int kMvThreads = 64 * kMvWaves;
 
-template <int kForm, bool kRM, int NS>
+// kParts: K is longer than the 8 GW groups held at once; a step then goes over parts of
+// K and fetches each part's activations again (a path of its own: their loads would
+// otherwise be waited for in every step).
+template <int kForm, bool kRM, int GW, int NS, bool kParts>
 __global__ __launch_bounds__(kMvThreads) void matvec_kernel(const uint16_t* __restrict__ x, int T, int64_t K,
                                                             int64_t ld, const uint8_t* __restrict__ w,
-                                                            const uint32_t* __restrict__ s, int64_t N,
+                                                            const uint8_t* __restrict__ s, int64_t N,
                                                             void* __restrict__ y, int y_bf16) {
-  constexpr int kBatch = 4;                    // groups loaded together
-  __shared__ float red[kMvWaves][NS][16][16];
+  constexpr bool kMx = kForm == kFormMx;
+  __shared__ float red[2][kMvWaves][NS][16][16];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 15, kq = lane >> 4;
-  const int64_t n0 = (int64_t)blockIdx.x * (16 * NS);
   const int G = (int)((K + kGroup - 1) / kGroup);
-  const int gpw = (G + kMvWaves - 1) / kMvWaves;
-  const int g_begin = wave * gpw, g_end = min(G, g_begin + gpw);
+  const uint32_t row_bytes = (uint32_t)(K >> 1);
+  const int steps = (int)((N + 16 * NS - 1) / (16 * NS));
+  const int nch = kParts ? (G + kMvWaves * GW - 1) / (kMvWaves * GW) : 1;   // parts of K
 
-  // the lane's weight bytes of subtile s and group g: pw[s] + g kGStride
-  constexpr int kGStride = kRM ? 64 : 1024;
-  const uint8_t* pw[NS];
-  int64_t nrow[NS];                            // the lane's weight row (clamped: a row past N is not stored)
-#pragma unroll
-  for (int i = 0; i < NS; ++i) {
-    const int64_t n = n0 + 16 * i + col;
-    nrow[i] = n < N ? n : N - 1;
-    if constexpr (kRM) pw[i] = w + nrow[i] * (K >> 1) + kq * 16;
-    else pw[i] = w + ((nrow[i] - (nrow[i] & 15)) * (K >> 1)) + (nrow[i] & 15) * 64 + kq * 16;
-  }
+  // the wave's groups of a part of K: g0 .. g0 + ng - 1
+  auto groups_of = [&](int ch, int& g0, int& ng) {
+    const int all = min(kMvWaves * GW, G - ch * kMvWaves * GW);
+    const int gpw = (all + kMvWaves - 1) / kMvWaves;
+    g0 = ch * kMvWaves * GW + wave * gpw;
+    ng = max(0, min(gpw, all - wave * gpw));
+  };
+  auto inside = [&](int g) { return !(kMx && kRM) || g * kGroup + 32 * kq < K; };   // a last group that is not whole
+
+  i32x4 av[GW][4], wv[GW][NS];
+  uint32_t sv[GW][NS];
+  v4f bias[GW];
   const uint16_t* xr = x + (int64_t)min(col, T - 1) * ld + 32 * kq;
-
-  v4f acc[NS];
+  auto load_a = [&](int g0, int ng) {
 #pragma unroll
-  for (int i = 0; i < NS; ++i) acc[i] = v4f{0.f, 0.f, 0.f, 0.f};
-  for (int g0 = g_begin; g0 < g_end; g0 += kBatch) {
-    i32x4 wv[kBatch][NS], av[kBatch][4];
-    uint32_t sv[kBatch][NS];
-#pragma unroll
-    for (int b = 0; b < kBatch; ++b) {
-      const int g = g0 + b;
-      // a lane past K (a last group that is not whole) multiplies zeros
-      const bool in = g < g_end && (int64_t)g * kGroup + 32 * kq < K;
-#pragma unroll
-      for (int i = 0; i < NS; ++i) {
-        wv[b][i] = in ? __builtin_nontemporal_load(reinterpret_cast<const i32x4*>(pw[i] + (int64_t)g * kGStride))
-                      : i32x4{0, 0, 0, 0};
-        if constexpr (kForm == kFormG128)
-          sv[b][i] = in ? s[kRM ? nrow[i] * G + g : (int64_t)g * N + nrow[i]] : 0u;
-        else if constexpr (kForm == kFormMx)
-          sv[b][i] = in ? reinterpret_cast<const uint8_t*>(s)[kRM ? nrow[i] * (K >> 5) + 4 * g + kq
-                                                                  : ((int64_t)g * N + nrow[i]) * 4 + kq]
-                        : 127u;
-        else sv[b][i] = 0u;
-      }
+    for (int i = 0; i < GW; ++i)
 #pragma unroll
       for (int c = 0; c < 4; ++c)
-        av[b][c] = in ? *reinterpret_cast<const i32x4*>(xr + (int64_t)g * kGroup + 8 * c) : i32x4{0, 0, 0, 0};
+        av[i][c] = i < ng && inside(g0 + i) ? *reinterpret_cast<const i32x4*>(xr + (int64_t)(g0 + i) * kGroup + 8 * c)
+                                            : i32x4{0, 0, 0, 0};
+  };
+  __amdgpu_buffer_rsrc_t rw = buffer_of(w, 0), rs = buffer_of(s, 0);
+  int lg0 = 0, lng = 0;                                        // the groups being loaded
+  auto point = [&](int step, int ch) {                         // the weights of (step, part); none past the last step
+    groups_of(ch, lg0, lng);
+    const int64_t n0 = (int64_t)step * (16 * NS);
+    const int64_t rows = step < steps ? (N - n0 < 16 * NS ? N - n0 : 16 * NS) : 0;
+    rw = buffer_of(w + n0 * row_bytes, rows * row_bytes);
+    if constexpr (kForm == kFormG128) {
+      if constexpr (kRM) rs = buffer_of(s + n0 * G * 4, rows * G * 4);
+      else rs = buffer_of(s + ((int64_t)lg0 * N + n0) * 4, rows ? ((int64_t)(G - lg0) * N - n0) * 4 : 0);
+    } else if constexpr (kMx) {
+      if constexpr (kRM) rs = buffer_of(s + n0 * (K >> 5), rows * (K >> 5));
+      else rs = buffer_of(s + ((int64_t)lg0 * N + n0) * 4, rows ? ((int64_t)(G - lg0) * N - n0) * 4 : 0);
+    }
+  };
+  auto load_w = [&](int i) {
+    const bool on = i < lng;
+#pragma unroll
+    for (int j = 0; j < NS; ++j) {
+      const uint32_t g = (uint32_t)(lg0 + i);
+      const uint32_t wo = kRM ? (16 * j + col) * row_bytes + 64 * g + 16 * kq
+                              : 16 * j * row_bytes + 1024 * g + 64 * col + 16 * kq;
+      wv[i][j] = buffer_load16_nt(rw, on ? wo : kNowhere);
+      if constexpr (kForm == kFormG128) {
+        const uint32_t so = kRM ? ((16 * j + col) * G + g) * 4 : (uint32_t)(i * N + 16 * j + col) * 4;
+        sv[i][j] = buffer_load4(rs, on ? so : kNowhere);
+      } else if constexpr (kMx) {
+        const uint32_t so = kRM ? (16 * j + col) * (uint32_t)(K >> 5) + 4 * g + kq
+                                : (uint32_t)(i * N + 16 * j + col) * 4;
+        if constexpr (kRM) sv[i][j] = buffer_load1(rs, on ? so : kNowhere);
+        else sv[i][j] = buffer_load4(rs, on ? so : kNowhere);
+      }
+    }
+  };
+
+  int step = blockIdx.x, buf = 0, g0, ng;
+  point(step, 0);
+#pragma unroll
+  for (int i = 0; i < GW; ++i) load_w(i);
+  groups_of(0, g0, ng);
+  load_a(g0, ng);
+  auto all_bias = [&]() {
+    if constexpr (!kMx) {
+#pragma unroll
+      for (int i = 0; i < GW; ++i)
+        if (i < ng) bias[i] = minus8_product(av[i]);
+    }
+  };
+  all_bias();
+  for (; step < steps; step += gridDim.x, buf ^= 1) {
+    v4f acc[NS];
+#pragma unroll
+    for (int j = 0; j < NS; ++j) acc[j] = v4f{0.f, 0.f, 0.f, 0.f};
+    for (int ch = 0; ch < nch; ++ch) {
+      if constexpr (kParts) {                                  // the activations of this part (from the cache)
+        groups_of(ch, g0, ng);
+        load_a(g0, ng);
+        all_bias();
+      }
+      const bool last = ch + 1 == nch;
+      point(last ? step + (int)gridDim.x : step, last ? 0 : ch + 1);
+#pragma unroll
+      for (int i = 0; i < GW; ++i) {
+        if (i < ng) {
+#pragma unroll
+          for (int j = 0; j < NS; ++j) {
+            uint32_t f = 0;
+            if constexpr (kForm == kFormG128) f = sv[i][j];
+            else if constexpr (kMx) f = kRM ? (inside(g0 + i) ? sv[i][j] : 127u) : (sv[i][j] >> (8 * kq)) & 0xffu;
+            group_product<kForm, kRM>(av[i], wv[i][j], f, kMx ? v4f{0.f, 0.f, 0.f, 0.f} : bias[i], acc[j]);
+          }
+        }
+        load_w(i);
+      }
     }
 #pragma unroll
-    for (int b = 0; b < kBatch; ++b) {
-      const v4f bias = kForm == kFormMx ? v4f{0.f, 0.f, 0.f, 0.f} : minus8_product(av[b]);
+    for (int j = 0; j < NS; ++j)
 #pragma unroll
-      for (int i = 0; i < NS; ++i) group_product<kForm, kRM>(av[b], wv[b][i], sv[b][i], bias, acc[i]);
+      for (int r = 0; r < 4; ++r) red[buf][wave][j][4 * kq + r][col] = acc[j][r];
+    __syncthreads();                                           // one per step: the other buffer's readers passed the last one
+    const int v = threadIdx.x;
+    if (v < T * 16 * NS) {
+      const int c = v & 15, j = (v >> 4) % NS, t = (v >> 4) / NS;
+      const int64_t n = (int64_t)step * (16 * NS) + 16 * j + c;
+      if (n < N) {
+        float sum = 0.0f;
+#pragma unroll
+        for (int u = 0; u < kMvWaves; ++u) sum += red[buf][u][j][t][c];
+        if constexpr (kForm == kFormChannel) sum *= reinterpret_cast<const float*>(s)[n];
+        if (y_bf16) static_cast<uint16_t*>(y)[(int64_t)t * N + n] = __builtin_bit_cast(uint16_t, (__bf16)sum);
+        else static_cast<float*>(y)[(int64_t)t * N + n] = sum;
+      }
     }
   }
-#pragma unroll
-  for (int i = 0; i < NS; ++i)
-#pragma unroll
-    for (int r = 0; r < 4; ++r) red[wave][i][4 * kq + r][col] = acc[i][r];
-  __syncthreads();
-  for (int v = threadIdx.x; v < T * 16 * NS; v += kMvThreads) {
-    const int c = v & 15, i = (v >> 4) % NS, t = (v >> 4) / NS;
-    const int64_t n = n0 + 16 * i + c;
-    if (n >= N) continue;
-    float sum = 0.0f;
-#pragma unroll
-    for (int u = 0; u < kMvWaves; ++u) sum += red[u][i][t][c];
-    if constexpr (kForm == kFormChannel) sum *= __uint_as_float(s[n]);
-    if (y_bf16) static_cast<uint16_t*>(y)[(int64_t)t * N + n] = __builtin_bit_cast(uint16_t, (__bf16)sum);
-    else static_cast<float*>(y)[(int64_t)t * N + n] = sum;
-  }
+}
+
+template <int kForm, bool kRM, int GW, bool kParts = false>
+static void launch_matvec_steps(const MatvecArgs& a, hipStream_t stream) {
+  auto go = [&](auto kernel, int ns) {
+    const int64_t steps = (a.N + 16 * ns - 1) / (16 * ns), wgs = 512;
+    hipLaunchKernelGGL(kernel, dim3((unsigned)(steps < wgs ? steps : wgs)), dim3(kMvThreads), 0, stream, a.x,
+                       (int)a.T, a.K, a.ld, static_cast<const uint8_t*>(a.w), static_cast<const uint8_t*>(a.s), a.N,
+                       a.y, a.y_bf16);
+  };
+  if (a.N >= 32 * 512) go(matvec_kernel<kForm, kRM, GW, 2, kParts>, 2);
+  else go(matvec_kernel<kForm, kRM, GW, 1, kParts>, 1);
 }
 
 template <int kForm, bool kRM>
 static void launch_matvec_form(const MatvecArgs& a, hipStream_t stream) {
-  constexpr int NS = 1;
-  hipLaunchKernelGGL((matvec_kernel<kForm, kRM, NS>), dim3((unsigned)((a.N + 16 * NS - 1) / (16 * NS))),
-                     dim3(kMvThreads), 0, stream, a.x, (int)a.T, a.K, a.ld, static_cast<const uint8_t*>(a.w),
-                     static_cast<const uint32_t*>(a.s), a.N, a.y, a.y_bf16);
+  const int64_t gpw = ((a.K + kGroup - 1) / kGroup + kMvWaves - 1) / kMvWaves;   // K groups per wave
+  if (gpw <= 2) launch_matvec_steps<kForm, kRM, 2>(a, stream);
+  else if (gpw <= 4) launch_matvec_steps<kForm, kRM, 4>(a, stream);
+  else if (gpw <= 6) launch_matvec_steps<kForm, kRM, 6>(a, stream);
+  else launch_matvec_steps<kForm, kRM, 6, true>(a, stream);
 }
 
 hipError_t launch_matvec(const MatvecArgs& a, hipStream_t stream) {

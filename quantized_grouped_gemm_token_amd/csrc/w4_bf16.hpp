@@ -74,6 +74,26 @@ __device__ __forceinline__ i32x4 e2m1x8_to_bf16(uint32_t w, float scale) {
   return r;
 }
 
+// Loads of weights and scales through buffer resources: an offset past the resource's
+// size reads as zero without touching memory, so a load of nothing (a wave's missing
+// group, the step after the last) is the same instruction as any other, and a loop
+// that refills registers as it uses them up needs no branch around its loads.  (With
+// a branch, the compiler waits for each load at the branch's end.)
+constexpr uint32_t kNowhere = 0x80000000u;                     // past every resource
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void* base, int64_t bytes) {
+  const int n = (int)(bytes < 0 ? 0 : bytes < 0x7fffffff ? bytes : 0x7fffffff);
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, n, 0x00020000);   // gfx9: raw, untyped
+}
+__device__ __forceinline__ i32x4 buffer_load16_nt(__amdgpu_buffer_rsrc_t r, uint32_t off) {
+  return __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(r, (int)off, 0, 2));   // 2: read once (nt)
+}
+__device__ __forceinline__ uint32_t buffer_load4(__amdgpu_buffer_rsrc_t r, uint32_t off) {
+  return __builtin_amdgcn_raw_buffer_load_b32(r, (int)off, 0, 0);
+}
+__device__ __forceinline__ uint32_t buffer_load1(__amdgpu_buffer_rsrc_t r, uint32_t off) {
+  return __builtin_amdgcn_raw_buffer_load_b8(r, (int)off, 0, 0);
+}
+
 constexpr int kMinus8 = (int)0xc100c100u;                      // two bf16 -8
 
 // A x (-8) over one K group: what A x U is too large by
