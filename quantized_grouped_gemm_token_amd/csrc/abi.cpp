@@ -649,7 +649,7 @@ int64_t w4a8_moe_few_workspace_bytes(int64_t T, int32_t k, int64_t I) {
   if (T < 0 || T > w4a8::kFewMaxTokens || k < 1 || T * (int64_t)k > w4a8::kFewMaxRows || I <= 0 || I % 128 ||
       I > w4a8::kFewMaxI)
     return -1;
-  return w4a8::few_workspace_bytes(T * (int64_t)k, I);
+  return w4a8::few_workspace_bytes(T, k, I);
 }
 
 static int run_few(const char* name, Form form, const uint16_t* x, int64_t T, int64_t H, int64_t ld_x,
@@ -676,7 +676,7 @@ static int run_few(const char* name, Form form, const uint16_t* x, int64_t T, in
   if (T == 0) return ok();
   if (!x || !logits || !w13 || !s13 || !w2 || !s2 || !y || !workspace)
     return fail(W4A8_ERR_NULL, "%s: null pointer", name);
-  const int64_t need = w4a8::few_workspace_bytes(T * (int64_t)k, I);
+  const int64_t need = w4a8::few_workspace_bytes(T, k, I);
   if (workspace_bytes < need)
     return fail(W4A8_ERR_WORKSPACE, "%s: workspace of %lld bytes, need %lld", name, (long long)workspace_bytes,
                 (long long)need);

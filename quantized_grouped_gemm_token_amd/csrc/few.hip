@@ -30,7 +30,7 @@ namespace w4a8 {
 
 constexpr int kFewWaves = 8;
 constexpr int kFewThreads = 64 * kFewWaves;
-constexpr int kFewDownGroups = 4;              // K groups of one (expert, K chunk) piece of the down product
+constexpr int kFewDownGroups = 8;              // most K groups of one (expert, K chunk) piece of the down product
 
 // ---- values -----------------------------------------------------------------
 // x / s rounded to fp32 from r = 1 / s rounded: q = fl(x r) is within an ulp, its
@@ -94,77 +94,97 @@ __device__ __forceinline__ uint32_t wave_max_key(uint32_t v) {
 
 constexpr int kRouteSlots = 16;                // 1024 experts
 
-// The k experts of a logits row and their weights, with the order, ties and sums of
-// w4a8_moe_route (the same bits): slot s of lane l is expert l + 64 s.  Every id
-// written is in [0, E), whatever the logits hold.
-// v: the row's logits, loaded before.  picked: a bit for each expert.
+// The k experts of a logits row in descending order, equal logits by the lower expert
+// (the order of w4a8_moe_route): slot s of lane l is expert l + 64 s, v its logit.  Every
+// id written is in [0, E), whatever the logits hold.  keys: the picks' order keys;
+// picked: a bit for each expert.  A round is one DPP maximum of the wave, then the
+// lowest slot and lane that hold it; picks stay in registers (lane j holds pick j) and
+// reach LDS 64 at a time.
 template <int S>
-__device__ __forceinline__ void route_token(const float (&v)[kRouteSlots], int E, int k, int renormalize, int* ids,
-                                            float* w, uint32_t* picked) {
+__device__ __forceinline__ void pick_experts(const float (&v)[kRouteSlots], int E, int k, int* ids, uint32_t* keys,
+                                             uint32_t* picked) {
   const int lane = threadIdx.x & 63;
   uint32_t key[S];
 #pragma unroll
   for (int s = 0; s < S; ++s) key[s] = lane + s * kWave < E ? order_key(v[s]) : 0u;
+  int my_id = 0;
+  uint32_t my_key = 0u;
   for (int j = 0; j < k; ++j) {
     uint32_t best = key[0];
 #pragma unroll
     for (int s = 1; s < S; ++s) best = max(best, key[s]);
     best = wave_max_key(best);
-    // the lowest expert that holds it: the first slot with a match, its lowest lane
     int id = 0;
-    bool found = false;
 #pragma unroll
-    for (int s = 0; s < S; ++s) {
+    for (int s = S - 1; s >= 0; --s) {
       const uint64_t hit = __ballot(key[s] == best);
-      if (!found && hit) {
-        found = true;
-        const int l = __builtin_ctzll(hit);
-        id = s * kWave + l;
-        if (lane == l) key[s] = 0u;
+      id = hit ? s * kWave + __builtin_ctzll(hit) : id;
+    }
+#pragma unroll
+    for (int s = 0; s < S; ++s) key[s] = lane + s * kWave == id ? 0u : key[s];
+    my_id = lane == (j & 63) ? id : my_id;
+    my_key = lane == (j & 63) ? best : my_key;
+    if ((j & 63) == 63 || j == k - 1) {
+      const int at = (j & ~63) + lane;
+      if (at <= j) {
+        ids[at] = my_id;
+        keys[at] = my_key;
+        atomicOr(&picked[my_id >> 5], 1u << (my_id & 31));
       }
     }
-    if (lane == 0) {
-      ids[j] = id;
-      w[j] = key_value(best);
-      atomicOr(&picked[id >> 5], 1u << (id & 31));
-    }
   }
-  wave_lds_fence();
-  const float m = w[0];
+}
+
+// The routing weights of one row from its picks' logits, by one wave, with the sums of
+// w4a8_moe_route (the same bits).  lr: the logits row.
+__device__ __forceinline__ void route_weights(const uint32_t* keys, const float* __restrict__ lr, int E, int k,
+                                              int renormalize, float* __restrict__ w, float* __restrict__ w_out) {
+  const int lane = threadIdx.x & 63;
+  const float m = key_value(keys[0]);
   float denom = 0.0f;
   if (renormalize) {
-    for (int j = lane; j < k; j += kWave) denom += expf(w[j] - m);
+    for (int j = lane; j < k; j += kWave) denom += expf(key_value(keys[j]) - m);
   } else {
-#pragma unroll
-    for (int s = 0; s < S; ++s)
-      if (lane + s * kWave < E) denom += expf(v[s] - m);
+    for (int e = lane; e < E; e += kWave) denom += expf(lr[e] - m);
   }
   denom = wave_sum(denom);
-  wave_lds_fence();
-  for (int j = lane; j < k; j += kWave) w[j] = expf(w[j] - m) / denom;
+  for (int j = lane; j < k; j += kWave) {
+    const float p = expf(key_value(keys[j]) - m) / denom;
+    w[j] = p;
+    if (w_out) w_out[j] = p;
+  }
 }
 
 // ---- what the first kernel leaves for the second ------------------------------
 // Views into the caller's workspace (16-byte aligned): the number of distinct
-// experts, the experts, the routed index of (expert, token) or -1, the routing
-// weights, act [R][I] and the maxima of |act| over its 16-column blocks [R][I/16].
+// experts; of each, the expert, the routed index of its first token (bits 16 up) and the
+// set of its tokens; the routed index of (expert, token) or -1; the routing weights, act [R][I] and the maxima of |act| over its 16-column blocks [R][I/16]; then
+// what the second kernel's workgroups leave for each other: their sums of a column block
+// that they share, [workgroup][2][T][16], and a count of arrivals for each of the H/16
+// column blocks (set to zero by the first kernel).
 struct FewWorkspace {
   int32_t* count;
-  int32_t* experts;       // [kFewMaxRows]
+  int32_t* experts;       // [kFewMaxRows] expert | first routed index << 16
+  uint32_t* tokens;       // [kFewMaxRows] bit t: token t picked the expert
   int16_t* slot;          // [kFewMaxRows][16]
   float* weights;         // [kFewMaxRows]
   float* act;
   float* pmax;
+  float* partial;
+  uint32_t* arrived;
 };
-__device__ __host__ __forceinline__ FewWorkspace few_workspace(void* p, int64_t R, int64_t I) {
+__device__ __forceinline__ FewWorkspace few_workspace(void* p, int64_t T, int64_t R, int64_t I) {
   unsigned char* b = static_cast<unsigned char*>(p);
   FewWorkspace v;
   v.count = reinterpret_cast<int32_t*>(b);
   v.experts = reinterpret_cast<int32_t*>(b + 16);
   v.weights = reinterpret_cast<float*>(b + 16 + 4 * kFewMaxRows);
-  v.slot = reinterpret_cast<int16_t*>(b + 16 + 8 * kFewMaxRows);
+  v.tokens = reinterpret_cast<uint32_t*>(b + 16 + 8 * kFewMaxRows);
+  v.slot = reinterpret_cast<int16_t*>(b + 16 + 12 * kFewMaxRows);
   v.act = reinterpret_cast<float*>(b + kFewHeadBytes);
   v.pmax = v.act + R * I;
+  v.partial = v.pmax + R * (I >> 4);
+  v.arrived = reinterpret_cast<uint32_t*>(v.partial + kFewDownMaxGrid * 2 * T * 16);
   return v;
 }
 
@@ -209,7 +229,7 @@ struct FewProduct {
 // weight register with the next task's as it uses it up.
 // GW: the most K groups of a wave (H <= 1024 GW).  S: logits per lane (E <= 64 S).
 template <int kForm, int GW, int S>
-__global__ __launch_bounds__(kFewThreads) void few_gate_up_kernel(const uint16_t* __restrict__ x, int T, int64_t H,
+__global__ __launch_bounds__(kFewThreads, GW <= 6 ? 4 : 2) void few_gate_up_kernel(const uint16_t* __restrict__ x, int T, int64_t H,
                                                                   int64_t ld, const float* __restrict__ logits, int E,
                                                                   int k, int renormalize,
                                                                   const uint8_t* __restrict__ w13,
@@ -221,7 +241,7 @@ __global__ __launch_bounds__(kFewThreads) void few_gate_up_kernel(const uint16_t
   constexpr bool kInt8 = P::kInt8;
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
   __shared__ int ids[kFewMaxRows];
-  __shared__ float wts[kFewMaxRows];
+  __shared__ uint32_t keys[kFewMaxRows];
   __shared__ int experts[kFewMaxRows];
   __shared__ __attribute__((aligned(16))) int16_t slot[kFewMaxRows][kFewMaxTokens];
   __shared__ float wave_amax[kFewMaxTokens][kFewWaves];
@@ -234,43 +254,72 @@ __global__ __launch_bounds__(kFewThreads) void few_gate_up_kernel(const uint16_t
   uint8_t* codes = smem;                                          // [G][4][T][32]
   float* red = reinterpret_cast<float*>(smem + (size_t)T * H);    // [2][waves][2][T][16]; int32 for INT8
 
-  // The waves share the rows of x, wpr waves to a row; every load of the prologue that
-  // depends on nothing is issued here.
+  // The waves share the first 8 rows of x, wpr waves to a row, and wave v takes row v + 8.
+  // A part of a row that is short enough stays in registers until the weights are on
+  // their way (up to 4 tokens, or rows of 2048); the others are read twice before that.
   const int wpr = T == 1 ? 8 : T == 2 ? 4 : T <= 4 ? 2 : 1;       // waves per row
-  const int rows_at_once = kFewWaves / wpr;                       // T <= 16: at most two rows per wave
-  const int part = wave % wpr;
+  const int part = wave % wpr, row = wave / wpr;
   const int chunks = (int)(H >> 3);                               // of 8 elements
+  constexpr int XC = GW <= 2 ? 2 * GW : GW;                       // chunks per lane held; a whole row has 2 GW
+  const bool has_row = row < T && (GW <= 2 || wpr > 1);
   float lg[kRouteSlots];
-  const bool routes = wave < T;                                   // waves 0 .. T-1 route (and wave + 8 for T > 8)
+  const bool routes = wave < T;                                   // wave v routes rows v and v + 8
 #pragma unroll
   for (int s = 0; s < S; ++s) lg[s] = routes && lane + s * kWave < E ? logits[(int64_t)wave * E + lane + s * kWave] : 0.0f;
+  const __amdgpu_buffer_rsrc_t rx = buffer_of(x + (int64_t)(has_row ? row : 0) * ld, has_row ? chunks * 16 : 0);
+  uint4 xv[XC];
+#pragma unroll
+  for (int i = 0; i < XC; ++i)                                    // past the row: zeros, which count nothing in the maximum
+    xv[i] = __builtin_bit_cast(uint4, buffer_load16(rx, (part * 64 + lane + 64 * wpr * i) * 16));
   if (threadIdx.x < 32) picked[threadIdx.x] = 0u;
   for (int i = threadIdx.x; i < R * kFewMaxTokens / 2; i += kFewThreads) reinterpret_cast<int*>(slot)[i] = -1;
-  for (int t0 = 0; t0 < T; t0 += rows_at_once) {                  // row maxima of x
-    const int t = t0 + wave / wpr;
-    if (t < T) {
-      const uint4* xr = reinterpret_cast<const uint4*>(x + (int64_t)t * ld);
-      float amax = 0.0f;
-#pragma unroll 4
-      for (int c = part * 64 + lane; c < chunks; c += 64 * wpr) {
-        const uint4 v = xr[c];
-        const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+  auto amax8 = [](float m, uint4 v) {
+    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(u[i])), fabsf(bf16_hi(u[i]))));
-      }
-      amax = wave_max(amax);
-      if (lane == 0) wave_amax[t][part] = amax;
-    }
-  }
+    for (int i = 0; i < 4; ++i) m = fmaxf(m, fmaxf(fabsf(bf16_lo(u[i])), fabsf(bf16_hi(u[i]))));
+    return m;
+  };
+  // the codes of chunk c of row t, in operand order: elements 8 c .. +7 are group c / 16, lane group
+  // (c / 4) % 4, bytes 8 (c % 4) .. +7 of its 32
+  auto put_codes = [&](uint4 v, int c, int t, float sc, float rc) {
+    uint2 o;
+    o.x = codes4<kInt8>(bf16_lo(v.x), bf16_hi(v.x), bf16_lo(v.y), bf16_hi(v.y), sc, rc);
+    o.y = codes4<kInt8>(bf16_lo(v.z), bf16_hi(v.z), bf16_lo(v.w), bf16_hi(v.w), sc, rc);
+    *reinterpret_cast<uint2*>(codes + ((size_t)(c >> 2) * T + t) * 32 + 8 * (c & 3)) = o;
+  };
   __syncthreads();                                                // picked and slot are set
-  if (routes) route_token<S>(lg, E, k, renormalize, ids + wave * k, wts + wave * k, picked);
-  if (wave + kFewWaves < T) {
-    const int t = wave + kFewWaves;
+  if (routes) pick_experts<S>(lg, E, k, ids + wave * k, keys + wave * k, picked);
+  auto quantize_row = [&](int t) {
+    const __amdgpu_buffer_rsrc_t rt = buffer_of(x + (int64_t)t * ld, chunks * 16);
+    float m = 0.0f;
+    for (int c = lane; c < chunks; c += 256) {
+      uint4 v[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = __builtin_bit_cast(uint4, buffer_load16(rt, (c + 64 * i) * 16));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) m = amax8(m, v[i]);
+    }
+    m = wave_max(m);
+    if (lane == 0) wave_amax[t][0] = m;
+    const float sc = row_scale<kInt8>(m), rc = 1.0f / sc;
+    for (int c = lane; c < chunks; c += 256) {
+      uint4 v[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = __builtin_bit_cast(uint4, buffer_load16(rt, (c + 64 * i) * 16));
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (c + 64 * i < chunks) put_codes(v[i], c + 64 * i, t, sc, rc);
+    }
+  };
+  if (GW > 2 && wpr == 1 && wave < T) quantize_row(wave);
+  if (wave + 8 < T) {
+    const int t = wave + 8;
 #pragma unroll
     for (int s = 0; s < S; ++s) lg[s] = lane + s * kWave < E ? logits[(int64_t)t * E + lane + s * kWave] : 0.0f;
-    route_token<S>(lg, E, k, renormalize, ids + t * k, wts + t * k, picked);
+    quantize_row(t);
+    pick_experts<S>(lg, E, k, ids + t * k, keys + t * k, picked);
   }
-  __syncthreads();                                                // ids, weights, picked and row maxima are there
+  __syncthreads();                                                // ids and picked are there
 
   // The distinct experts in ascending order: expert e is number (bits of picked below e).
   // Lane l holds word l and the bits in the words before it.
@@ -295,13 +344,14 @@ __global__ __launch_bounds__(kFewThreads) void few_gate_up_kernel(const uint16_t
   }
   __syncthreads();
 
-  const FewWorkspace ws = few_workspace(workspace, R, I);
+  const FewWorkspace ws = few_workspace(workspace, T, R, I);
   const int blocks = (int)(I >> 4);                               // column blocks of act
   const int ntasks = D * blocks;
   const int gpw = (G + kFewWaves - 1) / kFewWaves;                // <= GW
   const int g0 = wave * gpw, ng = max(0, min(gpw, G - g0));
+  constexpr int SW = (GW + 3) / 4;                                // scale words: one for four groups
   i32x4 wg[GW], wu[GW];
-  uint32_t sg[GW], su[GW];
+  uint32_t sg[SW], su[SW];
   __amdgpu_buffer_rsrc_t rg = buffer_of(w13, 0), ru = rg, rs = buffer_of(s13, 0);
   auto point = [&](int task) {                                    // the task's weights of this wave; none past the last task
     const bool on = task < ntasks && ng > 0;
@@ -315,45 +365,65 @@ __global__ __launch_bounds__(kFewThreads) void few_gate_up_kernel(const uint16_t
   auto load = [&](int i) {
     wg[i] = buffer_load16_nt(rg, col * 64 + kq * 16 + i * 1024);
     wu[i] = buffer_load16_nt(ru, col * 64 + kq * 16 + i * 1024);
+  };
+  auto load_scales = [&](int j) {                                 // of the groups 4 j .. 4 j + 3; before their weights
     if constexpr (!kInt8) {
-      sg[i] = buffer_load4(rs, (uint32_t)(i * 2 * I + col) * 4);
-      su[i] = buffer_load4(rs, (uint32_t)(i * 2 * I + I + col) * 4);
+      sg[j] = buffer_load4(rs, (uint32_t)((4 * j + kq) * 2 * I + col) * 4);
+      su[j] = buffer_load4(rs, (uint32_t)((4 * j + kq) * 2 * I + I + col) * 4);
     }
   };
   int task = blockIdx.x, buf = 0;
   point(task);
 #pragma unroll
-  for (int i = 0; i < GW; ++i) load(i);
-
-  if (blockIdx.x == 0) {                                          // the routing, for the second kernel and the caller
-    if (f == 0) *ws.count = D;
-    if (f < D) ws.experts[f] = experts[f];
-    if (f < R) {
-      ws.weights[f] = wts[f];
-      if (ids_out) ids_out[f] = ids[f];
-      if (w_out) w_out[f] = wts[f];
-    }
-    for (int i = threadIdx.x; i < D * kFewMaxTokens / 2; i += kFewThreads)
-      reinterpret_cast<int*>(ws.slot)[i] = reinterpret_cast<const int*>(slot)[i];
+  for (int i = 0; i < GW; ++i) {
+    if ((i & 3) == 0) load_scales(i >> 2);
+    load(i);
   }
 
-  // the codes, in operand order: byte o of lane group kq of row t, group g
-  for (int t0 = 0; t0 < T; t0 += rows_at_once) {
-    const int t = t0 + wave / wpr;
-    if (t < T) {
-      float amax = 0.0f;
-      for (int p = 0; p < wpr; ++p) amax = fmaxf(amax, wave_amax[t][p]);
-      const float sc = row_scale<kInt8>(amax), rc = 1.0f / sc;
-      const uint4* xr = reinterpret_cast<const uint4*>(x + (int64_t)t * ld);
-      for (int c = part * 64 + lane; c < chunks; c += 64 * wpr) {
-        const uint4 v = xr[c];
-        uint2 o;
-        o.x = codes4<kInt8>(bf16_lo(v.x), bf16_hi(v.x), bf16_lo(v.y), bf16_hi(v.y), sc, rc);
-        o.y = codes4<kInt8>(bf16_lo(v.z), bf16_hi(v.z), bf16_lo(v.w), bf16_hi(v.w), sc, rc);
-        // elements 8 c .. +7: group c / 16, lane group (c / 4) % 4, byte 8 (c % 4)
-        *reinterpret_cast<uint2*>(codes + ((size_t)(c >> 2) * T + t) * 32 + 8 * (c & 3)) = o;
-      }
+  {
+    float m = 0.0f;
+#pragma unroll
+    for (int i = 0; i < XC; ++i) m = amax8(m, xv[i]);
+    m = wave_max(m);
+    if (has_row && lane == 0) wave_amax[row][part] = m;           // (wave v's own row otherwise, below)
+    // (opaque: the fp32 values of the maxima are not kept for the codes, they would take twice the registers)
+#pragma unroll
+    for (int i = 0; i < XC; ++i) asm volatile("" : "+v"(xv[i].x), "+v"(xv[i].y), "+v"(xv[i].z), "+v"(xv[i].w));
+  }
+  __syncthreads();                                                // the row maxima are there
+  if (has_row) {                                                  // the codes of the rows in registers
+    float m = 0.0f;
+    for (int p = 0; p < wpr; ++p) m = fmaxf(m, wave_amax[row][p]);
+    const float sc = row_scale<kInt8>(m), rc = 1.0f / sc;
+#pragma unroll
+    for (int i = 0; i < XC; ++i) {
+      const int c = part * 64 + lane + 64 * wpr * i;
+      if (c < chunks) put_codes(xv[i], c, row, sc, rc);
+      __builtin_amdgcn_sched_barrier(0);                          // one chunk at a time: few values live
     }
+  }
+  if (blockIdx.x == 0) {                                          // the routing, for the second kernel and the caller
+    for (int t = wave; t < T; t += kFewWaves)
+      route_weights(keys + t * k, logits + (int64_t)t * E, E, k, renormalize, ws.weights + t * k,
+                    w_out ? w_out + t * k : nullptr);
+    if (f == 0) *ws.count = D;
+    if (f < D) {
+      uint32_t set = 0;
+      int fa = 0;
+      for (int t = T - 1; t >= 0; --t) {
+        const int v = slot[f][t];
+        if (v >= 0) {
+          set |= 1u << t;
+          fa = v;
+        }
+      }
+      ws.experts[f] = experts[f] | fa << 16;
+      ws.tokens[f] = set;
+    }
+    if (f < R && ids_out) ids_out[f] = ids[f];
+    for (int i = threadIdx.x; i < D * kFewMaxTokens / 2; i += kFewThreads)
+      reinterpret_cast<int*>(ws.slot)[i] = reinterpret_cast<const int*>(slot)[i];
+    for (int i = threadIdx.x; i < (int)(H >> 4); i += kFewThreads) ws.arrived[i] = 0u;
   }
   __syncthreads();
 
@@ -369,15 +439,21 @@ __global__ __launch_bounds__(kFewThreads) void few_gate_up_kernel(const uint16_t
   for (; task < ntasks; task += gridDim.x, buf ^= 1) {
     point(task + (int)gridDim.x);
     Acc ag = Acc{0, 0, 0, 0}, au = Acc{0, 0, 0, 0};
+    uint32_t g4[4], u4[4];
 #pragma unroll
     for (int i = 0; i < GW; ++i) {
+      if (!kInt8 && (i & 3) == 0) {
+        spread4(sg[i >> 2], g4);
+        spread4(su[i >> 2], u4);
+        load_scales(i >> 2);
+      }
       if (i < ng) {
         P p;
         p.set_codes(*reinterpret_cast<const v8i*>(arow + i * astep));
         uint32_t fg = 0, fu = 0;
         if constexpr (!kInt8) {
-          fg = kForm == kFormMx ? (sg[i] >> (8 * kq)) & 0xffu : sg[i];
-          fu = kForm == kFormMx ? (su[i] >> (8 * kq)) & 0xffu : su[i];
+          fg = kForm == kFormMx ? (g4[i & 3] >> (8 * kq)) & 0xffu : g4[i & 3];
+          fu = kForm == kFormMx ? (u4[i & 3] >> (8 * kq)) & 0xffu : u4[i & 3];
         }
         p.add(wg[i], fg, ag);
         p.add(wu[i], fu, au);
@@ -439,135 +515,208 @@ __global__ __launch_bounds__(kFewThreads) void few_gate_up_kernel(const uint16_t
 }
 
 // ---- kernel 2: requantization, down, the routing-weighted sum ----------------
-// A workgroup owns 16 columns of y for every token.  Its waves take the (distinct
-// expert, 4-group K chunk) pieces in turn: each requantizes the act of the expert's
-// tokens over those K elements into LDS of its own, up to 4 tokens at a time as rows
-// 0..3 of the A operand (an expert has one or two of the few tokens as a rule; the
-// weights stay in registers for the next 4), multiplies, and adds the rows with the
-// factors w[t, j] sa[f] to its own sums of y in LDS.  The next piece's weights, and
-// the act of its first two tokens, are loaded meanwhile.
-// The FP8 codes are held as the bf16 values they stand for: converting them once per
-// token and piece instead of once per operand read takes 16 of about 80 instructions
-// out of a K group's product, which are what bounds this kernel besides HBM.
+// The work is a row of pieces: for each block of 16 columns of y, the (distinct expert, K
+// chunk of up to 8 groups) products that its columns sum.  The workgroups take equal
+// ranges of that row (H/16 blocks are rarely a multiple of the CUs: whole blocks would
+// leave half the CUs with half the work of the others), so a workgroup has pieces of at
+// most two blocks, and a block is summed by one to five workgroups.  Each of them leaves
+// its sums in memory and counts itself on the block's counter; the one that arrives last
+// adds them in workgroup order (the same bits whichever that is) and writes y.  Nothing
+// waits on a counter.
+//
+// A wave takes pieces in turn: it requantizes the act of the expert's tokens over those K
+// elements into LDS of its own, up to 2 tokens at a time as rows 0 and 1 of the A operand
+// (an expert has one or two of the few tokens as a rule; the weights stay in registers for
+// the next 2), multiplies, and adds the rows with the factors w[t, j] sa[f] to its own sums
+// in LDS.  The next piece's weights, and the act of its first token, are loaded meanwhile.
+//  Besides HBM the instructions bound this kernel (53 for a K group's product,
+// about 250 for a piece): so a piece is long, and the FP8 codes are held as the bf16 values
+// they stand for, converted once per token and piece instead of once per operand read.
 template <int kForm>
-__global__ __launch_bounds__(kFewThreads) void few_down_kernel(int T, int64_t H, int k, const uint8_t* __restrict__ w2,
-                                                               const uint8_t* __restrict__ s2, int64_t I,
-                                                               const void* __restrict__ workspace,
-                                                               void* __restrict__ y, int y_bf16) {
+__global__ __launch_bounds__(kFewThreads, 4) void few_down_kernel(int T, int64_t H, int k,
+                                                                  const uint8_t* __restrict__ w2,
+                                                                  const uint8_t* __restrict__ s2, int64_t I,
+                                                                  void* __restrict__ workspace, void* __restrict__ y,
+                                                                  int y_bf16) {
   using P = FewProduct<kForm>;
   using Acc = typename P::Acc;
   constexpr bool kInt8 = P::kInt8;
+  constexpr int W = kFewWaves;
   constexpr int CG = kFewDownGroups;
-  constexpr int kRows = 4;                                               // rows of A in use
+  constexpr int SW = (CG + 3) / 4;                                       // scale words per lane
+  constexpr int kRows = 2;                                               // rows of A in use
   constexpr int kQuads = CG * kGroup / 4 / 64;                           // float4 of act per lane, token and piece
   // the wave's A rows: FP8 forms [CG][4 products][4 lane groups][rows][16 bytes], INT8 form [CG][4][rows][32 bytes]
-  __shared__ __attribute__((aligned(16))) uint8_t a_sm[kFewWaves][CG * kGroup * kRows * (kInt8 ? 1 : 2)];
-  __shared__ float scale[kFewMaxRows], factor[kFewMaxRows];              // sa[f], w[f] sa[f]
-  __shared__ int experts[kFewMaxRows];
-  __shared__ uint32_t routed[kFewMaxRows];                               // bit t: token t picked the expert
-  __shared__ __attribute__((aligned(16))) int16_t slot[kFewMaxRows][kFewMaxTokens];
-  extern __shared__ float y_sm[];                                        // [waves][T][16]
+  __shared__ __attribute__((aligned(16))) uint8_t a_sm[W][CG * kGroup * kRows * (kInt8 ? 1 : 2)];
+  extern __shared__ __attribute__((aligned(16))) unsigned char smem[];   // few_down_smem bytes
 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 15, kq = lane >> 4;
-  const int G = (int)(I >> 7), R = T * k;
-  const int nch = (G + CG - 1) / CG;                                     // K chunks of an expert
-  const int64_t cb = blockIdx.x;
-  const FewWorkspace ws = few_workspace(const_cast<void*>(workspace), R, I);
+  const int G = (int)(I >> 7), R = T * k, cols = (int)(H >> 4);
+  float4* row_sm = reinterpret_cast<float4*>(smem);                      // [R] of routed index f: sa, 1 / sa, w sa
+  int16_t(*slot)[kFewMaxTokens] = reinterpret_cast<int16_t(*)[kFewMaxTokens]>(row_sm + R);   // [R]
+  int* experts = reinterpret_cast<int*>(slot + R);                       // [R] expert | first routed index << 16
+  uint32_t* routed = reinterpret_cast<uint32_t*>(experts + R);           // [R] bit t: token t picked the expert
+  float* y_sm = reinterpret_cast<float*>(routed + R);                    // [W][2 blocks][T][16]
+  const int nch = (G + CG - 1) / CG, cg = (G + nch - 1) / nch;           // K chunks of an expert, groups of a chunk
+  const FewWorkspace ws = few_workspace(workspace, T, R, I);
 
-  // The weights of a piece, and the act of two of its tokens.  Loads past the last piece,
+  // The block maxima of act, 16 lanes to a row: the first 2 float4 per lane of rows f0 + 4 W u
+  // go out before the weights (the rest, for I > 2048 or R > 128, after them).
+  const int quads = (int)(I >> 6);                                       // float4 of maxima per row
+  const int f0 = threadIdx.x >> 4;
+  auto pmax_at = [&](int f, int j) {
+    return f < R && j < quads ? reinterpret_cast<const float4*>(ws.pmax)[(int64_t)f * quads + j]
+                              : make_float4(0.f, 0.f, 0.f, 0.f);
+  };
+  float4 pm[4][2];
+#pragma unroll
+  for (int u = 0; u < 4; ++u)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) pm[u][j] = pmax_at(f0 + 4 * W * u, col + 16 * j);
+
+  // every distinct expert's words, lane l holding numbers l, l + 64, ..: with the count they are one round trip to
+  // memory before the first weights (words past the count are not used)
+  int pe[kFewMaxRows / 64];
+  uint32_t pt[kFewMaxRows / 64];
+#pragma unroll
+  for (int i = 0; i < kFewMaxRows / 64; ++i) {
+    pe[i] = lane + 64 * i < R ? ws.experts[lane + 64 * i] : 0;
+    pt[i] = lane + 64 * i < R ? ws.tokens[lane + 64 * i] : 0u;
+  }
+
+  // the workgroup's pieces: lo .. hi - 1 of block * M + (expert number * nch + chunk); those below
+  // `second` are of block c0, the others of c0 + 1 (a range is at most M long)
+  const int D = __builtin_amdgcn_readfirstlane(*ws.count);
+  const int M = D * nch, total = cols * M;
+  const int wgs = min((int)gridDim.x, total);                            // every one of them has a piece
+  if ((int)blockIdx.x >= wgs) return;
+  auto range_start = [&](int wg) { return (int)((int64_t)total * wg / wgs); };
+  const int lo = range_start(blockIdx.x), hi = range_start(blockIdx.x + 1);
+  const int c0 = lo / M, second = (c0 + 1) * M;
+
+  // The weights of a piece, and the act of one of its tokens.  Loads past the last piece,
   // or of a token that is not there, read nothing.
+  struct Piece {
+    int d, g0, ng, block;  // ng = 0: none
+    uint32_t tokens;       // bit t: token t picked the expert
+    int f;                 // routed index of the first, -1: none
+  };
   i32x4 w[CG];
-  uint32_t s[CG];
-  float4 av0[kQuads], av1[kQuads];
+  uint32_t s[SW];
+  float4 av[kQuads];
   __amdgpu_buffer_rsrc_t rw, rs;
-  auto point = [&](int64_t e, int g0, bool on) {
-    const int n = min(CG, G - g0);
-    rw = buffer_of(w2 + ((e * (H >> 4) + cb) * G + g0) * 1024, on ? n * 1024 : 0);
-    if constexpr (!kInt8) rs = buffer_of(s2 + ((e * G + g0) * H + 16 * cb) * 4, on ? (n * H - 16 * cb) * 4 : 0);
+  auto piece_at = [&](int it) {
+    Piece p;
+    const bool on = it < hi;
+    const int b = on && it >= second ? 1 : 0, m = on ? it - (c0 + b) * M : 0;
+    p.block = b;
+    p.d = m / nch;
+    p.g0 = (m - p.d * nch) * cg;
+    p.ng = on ? min(cg, G - p.g0) : 0;
+    return p;
   };
-  auto load = [&](int i) {
-    w[i] = buffer_load16_nt(rw, col * 64 + kq * 16 + i * 1024);
-    if constexpr (!kInt8) s[i] = buffer_load4(rs, (uint32_t)(i * H + col) * 4);
+  auto point = [&](int64_t e, const Piece& p) {
+    const int cb = c0 + p.block;
+    rw = buffer_of(w2 + ((e * (H >> 4) + cb) * G + p.g0) * 1024, p.ng * 1024);
+    if constexpr (!kInt8)
+      rs = buffer_of(s2 + ((e * G + p.g0) * H + 16 * cb) * 4, p.ng ? ((int)H * p.ng - 16 * cb) * 4 : 0);
   };
-  auto load_act = [&](float4 (&v)[kQuads], int f, int g0) {              // f < 0: nothing
-    const __amdgpu_buffer_rsrc_t ra = buffer_of(ws.act + (int64_t)max(f, 0) * I + (int64_t)g0 * kGroup,
-                                                f >= 0 ? min(CG, G - g0) * kGroup * 4 : 0);
+  auto load = [&](int i) { w[i] = buffer_load16_nt(rw, col * 64 + kq * 16 + i * 1024); };
+  auto load_scales = [&]() {                                             // (before the weights)
+    if constexpr (!kInt8) {
+#pragma unroll
+      for (int j = 0; j < SW; ++j) s[j] = buffer_load4(rs, (uint32_t)((4 * j + kq) * (int)H + col) * 4);
+    }
+  };
+  auto load_act = [&](int f, int g0, int ng) {                           // f < 0: nothing
+    const __amdgpu_buffer_rsrc_t ra = buffer_of(ws.act + (int64_t)max(f, 0) * I + g0 * kGroup,
+                                                f >= 0 ? ng * kGroup * 4 : 0);
 #pragma unroll
     for (int q = 0; q < kQuads; ++q)
-      v[q] = __builtin_bit_cast(float4, __builtin_amdgcn_raw_buffer_load_b128(ra, (lane + 64 * q) * 16, 0, 0));
+      av[q] = __builtin_bit_cast(float4, buffer_load16(ra, (lane + 64 * q) * 16));
   };
   // the first piece of the wave, from what the first kernel left in memory
-  const int items = __builtin_amdgcn_readfirstlane(*ws.count) * nch;
+  Piece cur = piece_at(lo + wave);
   {
-    const bool on = wave < items;
-    const int d = on ? wave / nch : 0, g0 = on ? (wave - d * nch) * CG : 0;
-    const int e = __builtin_amdgcn_readfirstlane(ws.experts[d]);
-    const int f = ws.slot[(int64_t)d * kFewMaxTokens + col];
-    const uint32_t any = (uint32_t)__ballot(f >= 0) & 0xffffu, rest = any & (any - 1);
-    const int f0 = __builtin_amdgcn_readlane(f, any ? __builtin_ctz(any) : 0);
-    const int f1 = __builtin_amdgcn_readlane(f, rest ? __builtin_ctz(rest) : 0);
-    load_act(av0, on && any ? f0 : -1, g0);
-    load_act(av1, on && rest ? f1 : -1, g0);
-    point(e, g0, on);
+    int e = 0;
+    cur.tokens = 0;
+#pragma unroll
+    for (int i = 0; i < kFewMaxRows / 64; ++i) {
+      if (cur.d >> 6 == i) {
+        e = __builtin_amdgcn_readlane(pe[i], cur.d & 63);
+        cur.tokens = __builtin_amdgcn_readlane((int)pt[i], cur.d & 63);
+      }
+    }
+    cur.f = cur.ng ? e >> 16 : -1;
+    load_act(cur.f, cur.g0, cur.ng);
+    point(e & 0xffff, cur);
+    load_scales();
 #pragma unroll
     for (int i = 0; i < CG; ++i) load(i);
   }
-  const int D = items / nch;
-  for (int i = threadIdx.x; i < D; i += kFewThreads) experts[i] = ws.experts[i];
-  for (int i = threadIdx.x; i < D * kFewMaxTokens; i += kFewThreads) {   // 16 lanes per expert
-    const int f = ws.slot[i];
-    slot[i >> 4][i & 15] = (int16_t)f;
-    const uint64_t any = __ballot(f >= 0);
-    if ((i & 15) == 0) routed[i >> 4] = (uint32_t)(any >> (lane & 48)) & 0xffffu;
-  }
-  const int blocks = (int)(I >> 4);
-  for (int f = wave; f < R; f += kFewWaves) {                            // the row maxima
-    float m = 0.0f;
-    for (int b = lane; b < blocks; b += 64) m = fmaxf(m, ws.pmax[(int64_t)f * blocks + b]);
-    m = wave_max(m);
-    if (lane == 0) {
-      const float sa = row_scale<kInt8>(m);
-      scale[f] = sa;
-      factor[f] = ws.weights[f] * sa;
+  for (int fu = f0; fu < R; fu += 16 * W) {                              // the row scales
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int f = fu + 4 * W * u;
+      float m = 0.0f;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) m = fmaxf(m, fmaxf(fmaxf(pm[u][j].x, pm[u][j].y), fmaxf(pm[u][j].z, pm[u][j].w)));
+      for (int j = col + 32; j < quads; j += 16) {
+        const float4 v = pmax_at(f, j);
+        m = fmaxf(m, fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w)));
+      }
+      m = max16(m);
+      if (col == 0 && f < R) {
+        const float sa = row_scale<kInt8>(m);
+        row_sm[f] = make_float4(sa, 1.0f / sa, ws.weights[f] * sa, 0.0f);
+      }
+    }
+    if (fu + 16 * W < R) {
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) pm[u][j] = pmax_at(fu + 16 * W + 4 * W * u, col + 16 * j);
     }
   }
-  for (int i = threadIdx.x; i < kFewWaves * T * 16; i += kFewThreads) y_sm[i] = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kFewMaxRows / 64; ++i) {
+    if (wave == i && lane + 64 * i < R) {
+      experts[lane + 64 * i] = pe[i];
+      routed[lane + 64 * i] = pt[i];
+    }
+  }
+  for (int i = threadIdx.x; i < D * kFewMaxTokens / 2; i += kFewThreads)
+    reinterpret_cast<int*>(slot)[i] = reinterpret_cast<const int*>(ws.slot)[i];
+  for (int i = threadIdx.x; i < W * 2 * T * 16; i += kFewThreads) y_sm[i] = 0.0f;
   __syncthreads();
 
   uint8_t* mine = a_sm[wave];
-  float* ymine = y_sm + (size_t)wave * T * 16;
-  auto put = [&](const float4 (&v)[kQuads], int row, int f) {            // one token's codes of a piece
-    const float sc = scale[f], rc = 1.0f / sc;
+  // Where the lane's quad i of a piece goes, row 0: quad q = lane + 64 i holds the elements 4 (q % 8) .. +3 of
+  // lane group (q / 8) % 4 of group q / 32 (past the piece's groups: zeros, which nothing reads)
+  uint8_t* put_at = mine + (kInt8 ? (lane >> 3) * kRows * 32 + 4 * (lane & 7)
+                                  : (((lane >> 5) * 4 + ((lane & 7) >> 1)) * 4 + ((lane >> 3) & 3)) * kRows * 16 + 8 * (lane & 1));
+  constexpr int kPutStep = kInt8 ? 8 * kRows * 32 : 2 * 16 * kRows * 16;  // two groups on
+  float fac[kRows];                                                      // w sa of the rows
+  auto put = [&](int row, int f) {                                       // one token's codes of a piece, from av
+    const float4 r4 = row_sm[f];
+    fac[row] = r4.z;
 #pragma unroll
     for (int i = 0; i < kQuads; ++i) {
-      // 4 elements: group q / 32, lane group (q / 8) % 4, elements 4 (q % 8) of its 32 (past the piece's
-      // groups: zeros, which nothing reads)
-      const int q = lane + 64 * i;
-      const uint32_t c4 = codes4<kInt8>(v[i].x, v[i].y, v[i].z, v[i].w, sc, rc);
+      const uint32_t c4 = codes4<kInt8>(av[i].x, av[i].y, av[i].z, av[i].w, r4.x, r4.y);
       if constexpr (kInt8) {
-        *reinterpret_cast<uint32_t*>(mine + ((q >> 3) * kRows + row) * 32 + 4 * (q & 7)) = c4;
+        *reinterpret_cast<uint32_t*>(put_at + i * kPutStep + row * 32) = c4;
       } else {
         uint2 b;
         b.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c4, 1.0f, false));
         b.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c4, 1.0f, true));
-        const int g = q >> 5, c = (q & 7) >> 1, l = (q >> 3) & 3;
-        *reinterpret_cast<uint2*>(mine + (((g * 4 + c) * 4 + l) * kRows + row) * 16 + 8 * (q & 1)) = b;
+        *reinterpret_cast<uint2*>(put_at + i * kPutStep + row * 16) = b;
       }
     }
   };
-  // rows of A: the tokens of `set` from row `row` on, their act loaded here
-  auto put_rest = [&](uint32_t set, int d, int row, int g0) {
-    for (; set && row < kRows; set &= set - 1, ++row) {
-      const int f = __builtin_amdgcn_readfirstlane((int)slot[d][__builtin_ctz(set)]);
-      load_act(av0, f, g0);
-      put(av0, row, f);
-    }
-    return set;
-  };
-  auto product = [&](int i, Acc& acc, int rows) {
-    const int row = col < rows ? col : 0;
+  uint32_t s4[SW][4];
+  auto product = [&](int i, Acc& acc, int row) {                         // row: the lane's row of A
     P p;
     if constexpr (kInt8) {
       p.set_codes(*reinterpret_cast<const v8i*>(mine + ((i * 4 + kq) * kRows + row) * 32));
@@ -578,36 +727,40 @@ __global__ __launch_bounds__(kFewThreads) void few_down_kernel(int T, int64_t H,
       p.set_bias();
     }
     uint32_t fs = 0;
-    if constexpr (!kInt8) fs = kForm == kFormMx ? (s[i] >> (8 * kq)) & 0xffu : s[i];
+    if constexpr (!kInt8) fs = kForm == kFormMx ? (s4[i >> 2][i & 3] >> (8 * kq)) & 0xffu : s4[i >> 2][i & 3];
     p.add(w[i], fs, acc);
   };
-  // row r of the tile (lanes 0..15) to the sums of the r-th token of `set`
-  auto add_rows = [&](const Acc& acc, uint32_t set, int d) {
+  // rows 0 and 1 of the tile (lanes 0..15) to the sums of the first two tokens of `set`
+  auto add_rows = [&](const Acc& acc, uint32_t set) {
     float ws_n = 1.0f;
-    if constexpr (kInt8) ws_n = reinterpret_cast<const float*>(s2)[(int64_t)experts[d] * H + 16 * cb + col];
-#pragma unroll
-    for (int r = 0; r < kRows; ++r) {
+    if constexpr (kInt8)
+      ws_n = reinterpret_cast<const float*>(s2)[(int64_t)(experts[cur.d] & 0xffff) * H + 16 * (c0 + cur.block) + col];
+    float* base = y_sm + ((size_t)(wave * 2 + cur.block) * T) * 16 + col;
+    if (lane < 16) {
+      float* at = base + __builtin_ctz(set) * 16;
+      *at = fmaf(fac[0], kInt8 ? (float)acc[0] * ws_n : (float)acc[0], *at);
+      set &= set - 1;
       if (set) {
-        const int t = __builtin_ctz(set);
-        set &= set - 1;
-        if (lane < 16) {
-          float* at = ymine + t * 16 + col;
-          *at = fmaf(factor[slot[d][t]], kInt8 ? (float)acc[r] * ws_n : (float)acc[r], *at);
-        }
+        at = base + __builtin_ctz(set) * 16;
+        *at = fmaf(fac[1], kInt8 ? (float)acc[1] * ws_n : (float)acc[1], *at);
       }
     }
   };
-  for (int it = wave; it < items; it += kFewWaves) {
-    const int d = it / nch, g0 = (it - d * nch) * CG, ng = min(CG, G - g0);
-    uint32_t tokens = __builtin_amdgcn_readfirstlane(routed[d]);         // at least one bit
-    int rows = min(__builtin_popcount(tokens), kRows);
-    put(av0, 0, __builtin_amdgcn_readfirstlane((int)slot[d][__builtin_ctz(tokens)]));
-    uint32_t next = tokens & (tokens - 1);
-    if (next) {
-      put(av1, 1, __builtin_amdgcn_readfirstlane((int)slot[d][__builtin_ctz(next)]));
-      next = put_rest(next & (next - 1), d, 2, g0);
+  for (int it = lo + wave; it < hi; it += W) {
+    if constexpr (!kInt8) {
+#pragma unroll
+      for (int j = 0; j < SW; ++j) spread4(s[j], s4[j]);
     }
-    while (next) {                                                       // more than 4 tokens: the same weights again
+    uint32_t tokens = cur.tokens, next = tokens & (tokens - 1);          // at least one bit
+    put(0, cur.f);
+    auto put_next = [&](int row) {                                       // the next token, its act loaded here
+      const int f = __builtin_amdgcn_readfirstlane((int)slot[cur.d][__builtin_ctz(next)]);
+      next &= next - 1;
+      load_act(f, cur.g0, cur.ng);
+      put(row, f);
+    };
+    if (next) put_next(1);
+    while (next) {                                                       // more than 2 tokens: the same weights again
       // (opaque here: hoisted out of the loop, the unpacked weights would take a third more registers)
 #pragma unroll
       for (int i = 0; i < CG; ++i) asm volatile("" : "+v"(w[i]));
@@ -615,60 +768,112 @@ __global__ __launch_bounds__(kFewThreads) void few_down_kernel(int T, int64_t H,
       Acc acc = Acc{0, 0, 0, 0};
 #pragma unroll
       for (int i = 0; i < CG; ++i)
-        if (i < ng) product(i, acc, rows);
-      add_rows(acc, tokens, d);
+        if (i < cur.ng) product(i, acc, col & 1);
+      add_rows(acc, tokens);
       wave_lds_fence();
       tokens = next;
-      rows = min(__builtin_popcount(tokens), kRows);
-      next = put_rest(tokens, d, 0, g0);
+      put_next(0);
+      if (next) put_next(1);
     }
+    const int ng = cur.ng, row = tokens & (tokens - 1) ? col & 1 : 0;
     wave_lds_fence();
+    Piece nx = piece_at(it + W);
     {
-      const int nx = it + kFewWaves;
-      const bool on = nx < items;
-      const int dn = on ? nx / nch : 0, gn = on ? (nx - dn * nch) * CG : 0;
-      const uint32_t tn = __builtin_amdgcn_readfirstlane(routed[dn]), rest = tn & (tn - 1);
-      const int f0 = __builtin_amdgcn_readfirstlane((int)slot[dn][__builtin_ctz(tn)]);
-      const int f1 = __builtin_amdgcn_readfirstlane((int)slot[dn][rest ? __builtin_ctz(rest) : 0]);
-      load_act(av0, on ? f0 : -1, gn);
-      load_act(av1, on && rest ? f1 : -1, gn);
-      point(__builtin_amdgcn_readfirstlane(experts[dn]), gn, on);
+      nx.tokens = __builtin_amdgcn_readfirstlane(routed[nx.d]);
+      const int e = __builtin_amdgcn_readfirstlane(experts[nx.d]);
+      nx.f = nx.ng ? e >> 16 : -1;
+      load_act(nx.f, nx.g0, nx.ng);
+      point(e & 0xffff, nx);
+      load_scales();
     }
     Acc acc = Acc{0, 0, 0, 0};
 #pragma unroll
     for (int i = 0; i < CG; ++i) {
-      if (i < ng) product(i, acc, rows);
+      if (i < ng) product(i, acc, row);
       load(i);
     }
-    add_rows(acc, tokens, d);
+    add_rows(acc, tokens);
     wave_lds_fence();
+    cur = nx;
   }
   __syncthreads();
-  if ((int)threadIdx.x < 16 * T) {
-    const int t = threadIdx.x >> 4, c = threadIdx.x & 15;
-    float sum = 0.0f;
+
+  // The block's sums: threads 0 .. 255 take block c0, the others c0 + 1; one per (token, column).
+  const int b = threadIdx.x >> 8, t = (threadIdx.x >> 4) & 15, c = threadIdx.x & 15;
+  const int cb = c0 + b;
+  const int first = cb * M, end = first + M;                             // the block's pieces
+  const bool here = b == 0 || hi > second;                               // some are this workgroup's
+  const bool whole = here && lo <= first && end <= hi;
+  const bool sums = here && t < T;
+  float sum = 0.0f;
+  if (sums) {
 #pragma unroll
-    for (int v = 0; v < kFewWaves; ++v) sum += y_sm[((size_t)v * T + t) * 16 + c];
-    if (y_bf16) static_cast<uint16_t*>(y)[(int64_t)t * H + 16 * cb + c] = __builtin_bit_cast(uint16_t, (__bf16)sum);
-    else static_cast<float*>(y)[(int64_t)t * H + 16 * cb + c] = sum;
+    for (int v = 0; v < W; ++v) sum += y_sm[((size_t)(v * 2 + b) * T + t) * 16 + c];
+  }
+  bool writes = sums && whole;
+  if (lo > c0 * M || hi < second || hi > second) {                       // (the same for every thread) a block is shared
+    __shared__ int last_sm[2];
+    // The workgroups before and after: piece p is in number ((p + 1) wgs - 1) / total.
+    const int from = (int)(((int64_t)(first + 1) * wgs - 1) / total), to = (int)(((int64_t)end * wgs - 1) / total);
+    // The sums go to and come from the point where all XCDs' caches meet (device-scope accesses, which no cache
+    // holds back), so the order "sums, then the count" needs the stores to be done and no cache to be written
+    // back or dropped: a device-scope fence in its place took 170 us of a 50 us launch.
+    if (sums && !whole)
+      __hip_atomic_store(&ws.partial[((int64_t)(blockIdx.x * 2 + b) * T + t) * 16 + c], sum, __ATOMIC_RELAXED,
+                         __HIP_MEMORY_SCOPE_AGENT);
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+    if ((threadIdx.x & 255) == 0)
+      last_sm[b] = here && !whole &&
+                   __hip_atomic_fetch_add(&ws.arrived[cb], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
+                       (uint32_t)(to - from);
+    __syncthreads();
+    if (sums && !whole && last_sm[b]) {
+      writes = true;
+      sum = 0.0f;
+      for (int wg = from; wg <= to; ++wg) {                              // (block c is the second one of a range that starts before it)
+        const int half = range_start(wg) < first ? 1 : 0;
+        sum += __hip_atomic_load(&ws.partial[((int64_t)(wg * 2 + half) * T + t) * 16 + c], __ATOMIC_RELAXED,
+                                 __HIP_MEMORY_SCOPE_AGENT);
+      }
+    }
+  }
+  if (writes) {
+    const int64_t at = (int64_t)t * H + 16 * cb + c;
+    if (y_bf16) static_cast<uint16_t*>(y)[at] = __builtin_bit_cast(uint16_t, (__bf16)sum);
+    else static_cast<float*>(y)[at] = sum;
   }
 }
 
 // ---- launches ------------------------------------------------------------------
+// dynamic LDS of the second kernel: per routed row its scales, slots, expert and token set, then the waves' sums
+static size_t few_down_smem(int64_t R, int64_t T) { return (size_t)(56 * R + kFewWaves * 2 * T * 64); }
+
+// From 48 pieces per column block (6 per wave) on, 512 workgroups take equal ranges; below,
+// a workgroup takes a whole block, which saves the exchange of sums.  Measured, equal ranges
+// against whole blocks (I 2048, 384 blocks, group 128): 1 token (16 pieces) 17.8 against 17.2
+// us, 3 tokens (48) 33.9 against 37.2, 16 tokens (256) 139 against 162; 128 blocks, MXFP4:
+// 32 pieces 13.7 against 12.5 us, 128 pieces 25.1 against 30.9.
+constexpr int64_t kFewSplitPieces = 48;
+
 template <int kForm, int GW, int S>
 static hipError_t launch_few_form(const FewArgs& a, hipStream_t stream) {
   const int64_t R = a.T * a.k;
   const int64_t tasks = (R < a.E ? R : a.E) * (a.I >> 4);                // at most
-  const unsigned grid = (unsigned)(tasks < 512 ? tasks : 512);
   const size_t smem = (size_t)few_gate_up_smem(a.T, a.H);
+  const int64_t resident = smem + 12 * 1024 > 80 * 1024 ? 256 : 512;     // two workgroups on a CU while their LDS fits
+  const unsigned grid = (unsigned)(tasks < resident ? tasks : resident);
   hipLaunchKernelGGL((few_gate_up_kernel<kForm, GW, S>), dim3(grid), dim3(kFewThreads), smem, stream, a.x, (int)a.T, a.H,
                      a.ld, a.logits, a.E, a.k, a.renormalize, static_cast<const uint8_t*>(a.w13),
                      static_cast<const uint8_t*>(a.s13), a.I, a.ids, a.w, a.workspace);
   if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
-  const size_t smem2 = (size_t)kFewWaves * a.T * 16 * sizeof(float);
-  hipLaunchKernelGGL((few_down_kernel<kForm>), dim3((unsigned)(a.H >> 4)), dim3(kFewThreads), smem2, stream, (int)a.T,
-                     a.H, a.k, static_cast<const uint8_t*>(a.w2), static_cast<const uint8_t*>(a.s2), a.I,
-                     a.workspace, a.y, a.y_bf16);
+  const int64_t nch = (a.I / kGroup + kFewDownGroups - 1) / kFewDownGroups;
+  const int64_t pieces = (R < a.E ? R : a.E) * nch;                      // of a column block, at most
+  const unsigned cols = (unsigned)(a.H >> 4);
+  const unsigned nw = pieces >= kFewSplitPieces ? (unsigned)kFewDownMaxGrid : cols;
+  hipLaunchKernelGGL((few_down_kernel<kForm>), dim3(nw), dim3(kFewThreads),
+                     few_down_smem(R, a.T), stream, (int)a.T, a.H, a.k, static_cast<const uint8_t*>(a.w2),
+                     static_cast<const uint8_t*>(a.s2), a.I, a.workspace, a.y, a.y_bf16);
   return hipGetLastError();
 }
 

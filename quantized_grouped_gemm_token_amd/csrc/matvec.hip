@@ -45,8 +45,12 @@ __global__ __launch_bounds__(kMvThreads) void matvec_kernel(const uint16_t* __re
   };
   auto inside = [&](int g) { return !(kMx && kRM) || g * kGroup + 32 * kq < K; };   // a last group that is not whole
 
+  // Scales: a word per lane for four groups (spread4), or for the bytes of stored MXFP4
+  // rows, which need not be aligned to words, one per group.
+  constexpr bool kBytes = kMx && kRM;
+  constexpr int SP = kBytes ? 1 : 4, SW = (GW + SP - 1) / SP;  // groups per scale word
   i32x4 av[GW][4], wv[GW][NS];
-  uint32_t sv[GW][NS];
+  uint32_t sv[SW][NS];
   v4f bias[GW];
   const uint16_t* xr = x + (int64_t)min(col, T - 1) * ld + 32 * kq;
   auto load_a = [&](int g0, int ng) {
@@ -80,14 +84,18 @@ __global__ __launch_bounds__(kMvThreads) void matvec_kernel(const uint16_t* __re
       const uint32_t wo = kRM ? (16 * j + col) * row_bytes + 64 * g + 16 * kq
                               : 16 * j * row_bytes + 1024 * g + 64 * col + 16 * kq;
       wv[i][j] = buffer_load16_nt(rw, on ? wo : kNowhere);
-      if constexpr (kForm == kFormG128) {
-        const uint32_t so = kRM ? ((16 * j + col) * G + g) * 4 : (uint32_t)(i * N + 16 * j + col) * 4;
-        sv[i][j] = buffer_load4(rs, on ? so : kNowhere);
-      } else if constexpr (kMx) {
-        const uint32_t so = kRM ? (16 * j + col) * (uint32_t)(K >> 5) + 4 * g + kq
-                                : (uint32_t)(i * N + 16 * j + col) * 4;
-        if constexpr (kRM) sv[i][j] = buffer_load1(rs, on ? so : kNowhere);
-        else sv[i][j] = buffer_load4(rs, on ? so : kNowhere);
+    }
+  };
+  auto load_s = [&](int m) {                                   // scale word m, before its groups' weights
+    if constexpr (kForm != kFormChannel) {
+      const int i = SP * m + (kBytes ? 0 : kq);                // the lane's group
+#pragma unroll
+      for (int j = 0; j < NS; ++j) {
+        const uint32_t so = kBytes ? (16 * j + col) * (uint32_t)(K >> 5) + 4 * (lg0 + i) + kq
+                            : kRM  ? ((16 * j + col) * G + lg0 + i) * 4
+                                   : (uint32_t)(i * N + 16 * j + col) * 4;
+        if constexpr (kBytes) sv[m][j] = buffer_load1(rs, i < lng ? so : kNowhere);
+        else sv[m][j] = buffer_load4(rs, i < lng ? so : kNowhere);
       }
     }
   };
@@ -95,7 +103,10 @@ __global__ __launch_bounds__(kMvThreads) void matvec_kernel(const uint16_t* __re
   int step = blockIdx.x, buf = 0, g0, ng;
   point(step, 0);
 #pragma unroll
-  for (int i = 0; i < GW; ++i) load_w(i);
+  for (int i = 0; i < GW; ++i) {
+    if (i % SP == 0) load_s(i / SP);
+    load_w(i);
+  }
   groups_of(0, g0, ng);
   load_a(g0, ng);
   auto all_bias = [&]() {
@@ -118,14 +129,23 @@ __global__ __launch_bounds__(kMvThreads) void matvec_kernel(const uint16_t* __re
       }
       const bool last = ch + 1 == nch;
       point(last ? step + (int)gridDim.x : step, last ? 0 : ch + 1);
+      uint32_t s4[NS][4];
 #pragma unroll
       for (int i = 0; i < GW; ++i) {
+        if (i % SP == 0) {
+#pragma unroll
+          for (int j = 0; j < NS; ++j) {
+            if constexpr (kBytes) s4[j][0] = sv[i][j];
+            else if constexpr (kForm != kFormChannel) spread4(sv[i / SP][j], s4[j]);
+          }
+          load_s(i / SP);
+        }
         if (i < ng) {
 #pragma unroll
           for (int j = 0; j < NS; ++j) {
             uint32_t f = 0;
-            if constexpr (kForm == kFormG128) f = sv[i][j];
-            else if constexpr (kMx) f = kRM ? (inside(g0 + i) ? sv[i][j] : 127u) : (sv[i][j] >> (8 * kq)) & 0xffu;
+            if constexpr (kForm == kFormG128) f = s4[j][i & 3];
+            else if constexpr (kMx) f = kRM ? (inside(g0 + i) ? s4[j][0] : 127u) : (s4[j][i & 3] >> (8 * kq)) & 0xffu;
             group_product<kForm, kRM>(av[i], wv[i][j], f, kMx ? v4f{0.f, 0.f, 0.f, 0.f} : bias[i], acc[j]);
           }
         }
@@ -156,7 +176,7 @@ __global__ __launch_bounds__(kMvThreads) void matvec_kernel(const uint16_t* __re
 template <int kForm, bool kRM, int GW, bool kParts = false>
 static void launch_matvec_steps(const MatvecArgs& a, hipStream_t stream) {
   auto go = [&](auto kernel, int ns) {
-    const int64_t steps = (a.N + 16 * ns - 1) / (16 * ns), wgs = 512;
+    const int64_t steps = (a.N + 16 * ns - 1) / (16 * ns), wgs = GW <= 2 ? 512 : 256;
     hipLaunchKernelGGL(kernel, dim3((unsigned)(steps < wgs ? steps : wgs)), dim3(kMvThreads), 0, stream, a.x,
                        (int)a.T, a.K, a.ld, static_cast<const uint8_t*>(a.w), static_cast<const uint8_t*>(a.s), a.N,
                        a.y, a.y_bf16);

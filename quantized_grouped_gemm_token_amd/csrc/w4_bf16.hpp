@@ -87,11 +87,28 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void* base, in
 __device__ __forceinline__ i32x4 buffer_load16_nt(__amdgpu_buffer_rsrc_t r, uint32_t off) {
   return __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(r, (int)off, 0, 2));   // 2: read once (nt)
 }
+__device__ __forceinline__ i32x4 buffer_load16(__amdgpu_buffer_rsrc_t r, uint32_t off) {
+  return __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(r, (int)off, 0, 0));
+}
 __device__ __forceinline__ uint32_t buffer_load4(__amdgpu_buffer_rsrc_t r, uint32_t off) {
   return __builtin_amdgcn_raw_buffer_load_b32(r, (int)off, 0, 0);
 }
 __device__ __forceinline__ uint32_t buffer_load1(__amdgpu_buffer_rsrc_t r, uint32_t off) {
   return __builtin_amdgcn_raw_buffer_load_b8(r, (int)off, 0, 0);
+}
+
+// Scales come as one word per lane for four K groups: the word that lane group r of 16
+// lanes holds (group 4 j + r, column l % 16) goes to every lane group of out[r], by
+// three row swaps.  A load per group would cost as many load instructions as the
+// weights themselves.
+__device__ __forceinline__ void spread4(uint32_t v, uint32_t (&out)[4]) {
+  const auto ab = __builtin_amdgcn_permlane16_swap(v, v, false, false);        // rows 0 0 2 2 | 1 1 3 3
+  const auto a = __builtin_amdgcn_permlane32_swap(ab[0], ab[0], false, false);
+  const auto b = __builtin_amdgcn_permlane32_swap(ab[1], ab[1], false, false);
+  out[0] = a[0];
+  out[1] = b[0];
+  out[2] = a[1];
+  out[3] = b[1];
 }
 
 constexpr int kMinus8 = (int)0xc100c100u;                      // two bf16 -8

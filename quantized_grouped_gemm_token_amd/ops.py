@@ -915,12 +915,26 @@ def w4a8_moe_grouped_gemm_swiglu_mxfp4_prepacked(a: torch.Tensor, a_scale: torch
 FEW_MAX_TOKENS = 16
 
 
+# These calls are short (a matrix-vector product runs in a few microseconds), so the
+# binding keeps its own share small: one compound test per tensor, its message worked
+# out only when it fails, and the raw stream handle instead of a Stream object.
+_BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
+
+
+def _is(t, name: str, dtype, shape: tuple, dev: torch.device) -> None:
+    """t is a contiguous tensor of this type and shape on dev."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == dev
+            and t.is_contiguous()):
+        _need(t, name, dtype, len(shape), dev)
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+
+
 def _need_x(x: torch.Tensor) -> None:
     """x bf16 [T, K] on the GPU, its rows contiguous and any multiple of 8 elements apart."""
     if not isinstance(x, torch.Tensor):
         raise TypeError("x must be a torch.Tensor")
-    if x.dtype != torch.bfloat16:
-        raise TypeError(f"x must be {torch.bfloat16}, got {x.dtype}")
+    if x.dtype is not _BF16:
+        raise TypeError(f"x must be {_BF16}, got {x.dtype}")
     if x.dim() != 2:
         raise ValueError(f"x must have 2 dims, got shape {tuple(x.shape)}")
     if not x.is_cuda:
@@ -929,33 +943,41 @@ def _need_x(x: torch.Tensor) -> None:
         raise ValueError("x must have contiguous rows")
 
 
-def _ld(x: torch.Tensor) -> int:
+def _ld(x: torch.Tensor, T: int, K: int) -> int:
     """Elements between two rows of x (a single row has no such distance)."""
-    return x.stride(0) if x.shape[0] > 1 else x.shape[1]
+    return x.stride(0) if T > 1 else K
 
 
 def _y(y, y_dtype, T: int, N: int, dev):
     if y is None:
-        if y_dtype not in (torch.float32, torch.bfloat16):
+        if y_dtype is _BF16:
+            return torch.empty((T, N), dtype=_BF16, device=dev), W4A8_Y_BF16
+        if y_dtype is not _F32:
             raise TypeError("y must be float32 or bfloat16")
-        y = torch.empty((T, N), dtype=y_dtype, device=dev)
-    else:
-        if not isinstance(y, torch.Tensor) or y.dtype not in (torch.float32, torch.bfloat16):
-            raise TypeError("y must be a float32 or bfloat16 tensor")
-        _need(y, "y", y.dtype, 2, dev)
-        if tuple(y.shape) != (T, N):
-            raise ValueError(f"y must be [{T}, {N}]")
-    return y, W4A8_Y_F32 if y.dtype == torch.float32 else W4A8_Y_BF16
+        return torch.empty((T, N), dtype=_F32, device=dev), W4A8_Y_F32
+    if not isinstance(y, torch.Tensor) or y.dtype not in (_F32, _BF16):
+        raise TypeError("y must be a float32 or bfloat16 tensor")
+    _is(y, "y", y.dtype, (T, N), dev)
+    return y, W4A8_Y_F32 if y.dtype is _F32 else W4A8_Y_BF16
+
+
+_functions: dict = {}
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _call_on(dev: torch.device, name: str, *args) -> None:
     """The library call on dev's current stream, with dev the current device."""
-    if dev.index == torch.cuda.current_device():
-        status = getattr(lib(), name)(*args, _stream(dev))
+    f = _functions.get(name)
+    if f is None:
+        f = _functions[name] = getattr(lib(), name)
+    i = dev.index
+    if i == torch.cuda.current_device():
+        status = f(*args, _raw_stream(i) if _raw_stream else _stream(dev))
     else:
         with torch.cuda.device(dev):
-            status = getattr(lib(), name)(*args, _stream(dev))
-    _check(name, status)
+            status = f(*args, _stream(dev))
+    if status:
+        _check(name, status)
 
 
 def w4a8_moe_few_fits(T: int, H: int, k: int) -> bool:
@@ -970,43 +992,51 @@ def w4a8_moe_few_workspace_bytes(T: int, k: int, I: int) -> int:
     return n
 
 
+_FEW = {"g128": ("w4a8_moe_few_prepacked", _I32, 16), "i8": ("w4a8_moe_few_i8_prepacked", _I32, 16),
+        "mxfp4": ("w4a8_moe_few_mxfp4_prepacked", _U8, 64)}
+
+
 def _few(form, x, logits, k, w13, s13, w2, s2, renormalize, y, y_dtype, ids, w, workspace):
     _need_x(x)
     dev = x.device
     T, H = x.shape
-    _need(logits, "logits", torch.float32, 2, dev)
+    if not isinstance(logits, torch.Tensor) or logits.dim() != 2 or logits.shape[0] != T:
+        raise ValueError("logits must be a tensor [T, E] for x [T, H]")
     E = logits.shape[1]
-    if logits.shape[0] != T:
-        raise ValueError("logits must be [T, E] for x [T, H]")
-    if form == "mxfp4":
-        E13, N13, K13 = _mx_weights(w13, s13, ("w13", "s13"), dev, True)
-        E2, N2, K2 = _mx_weights(w2, s2, ("w2", "s2"), dev, True)
+    _is(logits, "logits", _F32, (T, E), dev)
+    if not isinstance(w13, torch.Tensor) or w13.dim() != 5:
+        raise ValueError("w13 must be the GEMM storage of the experts' gate/up rows")
+    name, wdt, last = _FEW[form]
+    I = 8 * w13.shape[1]
+    if H % 128 or I % 128:
+        raise ValueError(f"the hidden size {H} and the experts' size {I} must be multiples of 128")
+    G13, G2 = H // 128, I // 128
+    _is(w13, "w13", wdt, (E, I // 8, G13, 16, last), dev)
+    _is(w2, "w2", wdt, (E, H // 16, G2, 16, last), dev)
+    if form == "g128":
+        _is(s13, "s13", _F32, (E, G13, 2 * I), dev)
+        _is(s2, "s2", _F32, (E, G2, H), dev)
+    elif form == "i8":
+        _is(s13, "s13", _F32, (E, 2 * I), dev)
+        _is(s2, "s2", _F32, (E, H), dev)
     else:
-        E13, N13, K13 = _int4_storage(w13, "w13", dev)
-        E2, N2, K2 = _int4_storage(w2, "w2", dev)
-        for s, name, n, kk in ((s13, "s13", N13, K13), (s2, "s2", N2, K2)):
-            if form == "i8":
-                _need(s, name, torch.float32, 2, dev)
-                if tuple(s.shape) != (E, n):
-                    raise ValueError(f"{name} must be [{E}, {n}]")
-            else:
-                _g128_scales(s, name, dev, E, n, kk, True)
-    if E13 != E or E2 != E or K13 != H or N2 != H or 2 * K2 != N13:
-        raise ValueError("w13 must hold [E] experts of 2I rows of H, w2 of H rows of I, for x [T, H] and logits [T, E]")
+        _is(s13, "s13", _U8, (E, G13, 2 * I, 4), dev)
+        _is(s2, "s2", _U8, (E, G2, H, 4), dev)
     y, code = _y(y, y_dtype, T, H, dev)
-    for t, name, dt in ((ids, "ids", torch.int32), (w, "w", torch.float32)):
-        if t is not None:
-            _need(t, name, dt, 2, dev)
-            if tuple(t.shape) != (T, k):
-                raise ValueError(f"{name} must be [T, k]")
-    nbytes = lib().w4a8_moe_few_workspace_bytes(T, k, K2)           # -1 on sizes the library refuses below
+    if ids is not None:
+        _is(ids, "ids", _I32, (T, k), dev)
+    if w is not None:
+        _is(w, "w", _F32, (T, k), dev)
     if workspace is None:
-        workspace = torch.empty((max(nbytes, 16),), dtype=torch.uint8, device=dev)
+        # (-1 on sizes that the library refuses below)
+        nbytes = max(lib().w4a8_moe_few_workspace_bytes(T, k, I), 16)
+        workspace = torch.empty((nbytes,), dtype=_U8, device=dev)
     else:
-        _need(workspace, "workspace", torch.uint8, 1, dev)
-    _call_on(dev, "w4a8_moe_few" + ("" if form == "g128" else "_" + form) + "_prepacked", _p(x), T, H, _ld(x),
-             _p(logits), E, k, int(bool(renormalize)), _p(w13), _p(s13), _p(w2), _p(s2), K2, _p(ids), _p(w), _p(y),
-             code, _p(workspace), workspace.numel())
+        _need(workspace, "workspace", _U8, 1, dev)
+        nbytes = workspace.numel()
+    _call_on(dev, name, x.data_ptr(), T, H, _ld(x, T, H), logits.data_ptr(), E, k, 1 if renormalize else 0,
+             w13.data_ptr(), s13.data_ptr(), w2.data_ptr(), s2.data_ptr(), I, _p(ids), _p(w), y.data_ptr(), code,
+             workspace.data_ptr(), nbytes)
     return y
 
 
@@ -1047,29 +1077,22 @@ def _matvec(name, form, prepacked, x, w, s, y, y_dtype):
     _need_x(x)
     dev = x.device
     T, K = x.shape
-    wdt = torch.uint8 if form == "mxfp4" else torch.int32
-    _need(w, "w", wdt, 4 if prepacked else 2, dev)
+    mx = form == "mxfp4"
+    if not isinstance(w, torch.Tensor) or w.dim() != (4 if prepacked else 2):
+        raise ValueError("w must be one matrix of the GEMM storage" if prepacked else "w must be a stored matrix [N, ..]")
+    N = w.shape[0]
+    if K % (32 if mx and not prepacked else 128):
+        raise ValueError(f"the row length {K} must be a multiple of {32 if mx and not prepacked else 128}")
     if prepacked:
-        NB, G, sixteen, last = w.shape
-        N, kw = 16 * NB, 128 * G
-        if (sixteen, last) != (16, 64 if form == "mxfp4" else 16):
-            raise ValueError("w must be one matrix of the GEMM storage, [N/16, K/128, 16, "
-                             f"{64 if form == 'mxfp4' else 16}]")
+        _is(w, "w", _U8 if mx else _I32, (N, K // 128, 16, 64 if mx else 16), dev)
+        N *= 16
+        want = (N,) if form == "channel" else (K // 128, N, 4) if mx else (K // 128, N)
     else:
-        N, kw = w.shape[0], w.shape[1] * (2 if form == "mxfp4" else 8)
-    if kw != K:
-        raise ValueError(f"w holds rows of {kw}, x rows of {K}")
-    if form == "channel":
-        want = (N,)
-    elif form == "mxfp4":
-        want = (K // 128, N, 4) if prepacked else (N, K // 32)
-    else:
-        want = (K // 128, N) if prepacked else (N, K // 128)
-    _need(s, "s", torch.uint8 if form == "mxfp4" else torch.float32, len(want), dev)
-    if tuple(s.shape) != want:
-        raise ValueError(f"s must be {list(want)}, got {list(s.shape)}")
+        _is(w, "w", _U8 if mx else _I32, (N, K // 2 if mx else K // 8), dev)
+        want = (N,) if form == "channel" else (N, K // 32) if mx else (N, K // 128)
+    _is(s, "s", _U8 if mx else _F32, want, dev)
     y, code = _y(y, y_dtype, T, N, dev)
-    _call_on(dev, name, _p(x), T, K, _ld(x), _p(w), _p(s), N, _p(y), code)
+    _call_on(dev, name, x.data_ptr(), T, K, _ld(x, T, K), w.data_ptr(), s.data_ptr(), N, y.data_ptr(), code)
     return y
 
 
