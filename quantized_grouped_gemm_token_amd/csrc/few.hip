@@ -65,12 +65,6 @@ __device__ __forceinline__ float row_scale(float amax) {
   return amax > 0.0f ? amax / (kInt8 ? 127.0f : kFp8Max) : 1.0f;
 }
 
-// orders LDS accesses of one wave's lanes (the LDS itself serves a wave in order)
-__device__ __forceinline__ void wave_lds_fence() {
-  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-}
-
 // ---- routing of one token by one wave ---------------------------------------
 // fp32 -> uint32 with the order of the values (-0 as +0); 0 is below every value
 __device__ __forceinline__ uint32_t order_key(float v) {
@@ -107,30 +101,30 @@ __device__ __forceinline__ void pick_experts(const float (&v)[kRouteSlots], int 
   uint32_t key[S];
 #pragma unroll
   for (int s = 0; s < S; ++s) key[s] = lane + s * kWave < E ? order_key(v[s]) : 0u;
-  int my_id = 0;
-  uint32_t my_key = 0u;
-  for (int j = 0; j < k; ++j) {
-    uint32_t best = key[0];
+  for (int j0 = 0; j0 < k; j0 += kWave) {
+    int my_id = 0;
+    uint32_t my_key = 0u;
+    const int n = min(k - j0, kWave);
+    for (int j = 0; j < n; ++j) {
+      uint32_t best = key[0];
 #pragma unroll
-    for (int s = 1; s < S; ++s) best = max(best, key[s]);
-    best = wave_max_key(best);
-    int id = 0;
+      for (int s = 1; s < S; ++s) best = max(best, key[s]);
+      best = wave_max_key(best);
+      int id = 0;
 #pragma unroll
-    for (int s = S - 1; s >= 0; --s) {
-      const uint64_t hit = __ballot(key[s] == best);
-      id = hit ? s * kWave + __builtin_ctzll(hit) : id;
-    }
-#pragma unroll
-    for (int s = 0; s < S; ++s) key[s] = lane + s * kWave == id ? 0u : key[s];
-    my_id = lane == (j & 63) ? id : my_id;
-    my_key = lane == (j & 63) ? best : my_key;
-    if ((j & 63) == 63 || j == k - 1) {
-      const int at = (j & ~63) + lane;
-      if (at <= j) {
-        ids[at] = my_id;
-        keys[at] = my_key;
-        atomicOr(&picked[my_id >> 5], 1u << (my_id & 31));
+      for (int s = S - 1; s >= 0; --s) {
+        const uint64_t hit = __ballot(key[s] == best);
+        id = hit ? s * kWave + __builtin_ctzll(hit) : id;
       }
+#pragma unroll
+      for (int s = 0; s < S; ++s) key[s] = lane + s * kWave == id ? 0u : key[s];
+      my_id = lane == j ? id : my_id;
+      my_key = lane == j ? best : my_key;
+    }
+    if (lane < n) {
+      ids[j0 + lane] = my_id;
+      keys[j0 + lane] = my_key;
+      atomicOr(&picked[my_id >> 5], 1u << (my_id & 31));
     }
   }
 }
@@ -262,15 +256,25 @@ __global__ __launch_bounds__(kFewThreads, GW <= 6 ? 4 : 2) void few_gate_up_kern
   const int chunks = (int)(H >> 3);                               // of 8 elements
   constexpr int XC = GW <= 2 ? 2 * GW : GW;                       // chunks per lane held; a whole row has 2 GW
   const bool has_row = row < T && (GW <= 2 || wpr > 1);
-  float lg[kRouteSlots];
-  const bool routes = wave < T;                                   // wave v routes rows v and v + 8
+  const bool routes = wave < T, routes2 = wave + 8 < T;           // wave v routes rows v and v + 8
+  float lg[kRouteSlots], lg2[kRouteSlots];
 #pragma unroll
-  for (int s = 0; s < S; ++s) lg[s] = routes && lane + s * kWave < E ? logits[(int64_t)wave * E + lane + s * kWave] : 0.0f;
+  for (int s = 0; s < S; ++s) {
+    const int e = lane + s * kWave;
+    lg[s] = routes && e < E ? logits[(int64_t)wave * E + e] : 0.0f;
+    lg2[s] = routes2 && e < E ? logits[(int64_t)(wave + 8) * E + e] : 0.0f;
+  }
   const __amdgpu_buffer_rsrc_t rx = buffer_of(x + (int64_t)(has_row ? row : 0) * ld, has_row ? chunks * 16 : 0);
   uint4 xv[XC];
 #pragma unroll
   for (int i = 0; i < XC; ++i)                                    // past the row: zeros, which count nothing in the maximum
     xv[i] = __builtin_bit_cast(uint4, buffer_load16(rx, (part * 64 + lane + 64 * wpr * i) * 16));
+  uint4 xv2[GW <= 2 ? XC : 1];                                    // row v + 8, where rows are short
+  if constexpr (GW <= 2) {
+    const __amdgpu_buffer_rsrc_t rx2 = buffer_of(x + (int64_t)(routes2 ? wave + 8 : 0) * ld, routes2 ? chunks * 16 : 0);
+#pragma unroll
+    for (int i = 0; i < XC; ++i) xv2[i] = __builtin_bit_cast(uint4, buffer_load16(rx2, (lane + 64 * i) * 16));
+  }
   if (threadIdx.x < 32) picked[threadIdx.x] = 0u;
   for (int i = threadIdx.x; i < R * kFewMaxTokens / 2; i += kFewThreads) reinterpret_cast<int*>(slot)[i] = -1;
   auto amax8 = [](float m, uint4 v) {
@@ -312,12 +316,21 @@ __global__ __launch_bounds__(kFewThreads, GW <= 6 ? 4 : 2) void few_gate_up_kern
     }
   };
   if (GW > 2 && wpr == 1 && wave < T) quantize_row(wave);
-  if (wave + 8 < T) {
-    const int t = wave + 8;
+  if (routes2) {
+    pick_experts<S>(lg2, E, k, ids + (wave + 8) * k, keys + (wave + 8) * k, picked);
+    if constexpr (GW <= 2) {
+      float m = 0.0f;
 #pragma unroll
-    for (int s = 0; s < S; ++s) lg[s] = lane + s * kWave < E ? logits[(int64_t)t * E + lane + s * kWave] : 0.0f;
-    quantize_row(t);
-    pick_experts<S>(lg, E, k, ids + t * k, keys + t * k, picked);
+      for (int i = 0; i < XC; ++i) m = amax8(m, xv2[i]);
+      m = wave_max(m);
+      if (lane == 0) wave_amax[wave + 8][0] = m;
+      const float sc = row_scale<kInt8>(m), rc = 1.0f / sc;
+#pragma unroll
+      for (int i = 0; i < XC; ++i)
+        if (lane + 64 * i < chunks) put_codes(xv2[i], lane + 64 * i, wave + 8, sc, rc);
+    } else {
+      quantize_row(wave + 8);
+    }
   }
   __syncthreads();                                                // ids and picked are there
 
@@ -753,17 +766,23 @@ __global__ __launch_bounds__(kFewThreads, 4) void few_down_kernel(int T, int64_t
     }
     uint32_t tokens = cur.tokens, next = tokens & (tokens - 1);          // at least one bit
     put(0, cur.f);
-    auto put_next = [&](int row) {                                       // the next token, its act loaded here
+    auto take = [&]() {                                                  // the routed index of the next token
       const int f = __builtin_amdgcn_readfirstlane((int)slot[cur.d][__builtin_ctz(next)]);
       next &= next - 1;
-      load_act(f, cur.g0, cur.ng);
-      put(row, f);
+      return f;
     };
-    if (next) put_next(1);
+    if (next) {
+      const int f = take();
+      load_act(f, cur.g0, cur.ng);
+      put(1, f);
+    }
     while (next) {                                                       // more than 2 tokens: the same weights again
       // (opaque here: hoisted out of the loop, the unpacked weights would take a third more registers)
 #pragma unroll
       for (int i = 0; i < CG; ++i) asm volatile("" : "+v"(w[i]));
+      const uint32_t set = next;
+      const int fa = take();
+      load_act(fa, cur.g0, cur.ng);
       wave_lds_fence();
       Acc acc = Acc{0, 0, 0, 0};
 #pragma unroll
@@ -771,9 +790,13 @@ __global__ __launch_bounds__(kFewThreads, 4) void few_down_kernel(int T, int64_t
         if (i < cur.ng) product(i, acc, col & 1);
       add_rows(acc, tokens);
       wave_lds_fence();
-      tokens = next;
-      put_next(0);
-      if (next) put_next(1);
+      tokens = set;
+      put(0, fa);
+      if (next) {
+        const int fb = take();
+        load_act(fb, cur.g0, cur.ng);
+        put(1, fb);
+      }
     }
     const int ng = cur.ng, row = tokens & (tokens - 1) ? col & 1 : 0;
     wave_lds_fence();

@@ -28,6 +28,10 @@ __global__ __launch_bounds__(kMvThreads) void matvec_kernel(const uint16_t* __re
                                                             void* __restrict__ y, int y_bf16) {
   constexpr bool kMx = kForm == kFormMx;
   __shared__ float red[2][kMvWaves][NS][16][16];
+  // The wave's activations of one group on their way to operand order, T rows of 256 bytes.  A row is 16 bytes
+  // longer so that the 16 rows an operand read covers start in different banks.
+  constexpr int kPitch = 272;
+  extern __shared__ __attribute__((aligned(16))) unsigned char a_sm[];   // [waves][T][kPitch]
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 15, kq = lane >> 4;
@@ -43,7 +47,7 @@ __global__ __launch_bounds__(kMvThreads) void matvec_kernel(const uint16_t* __re
     g0 = ch * kMvWaves * GW + wave * gpw;
     ng = max(0, min(gpw, all - wave * gpw));
   };
-  auto inside = [&](int g) { return !(kMx && kRM) || g * kGroup + 32 * kq < K; };   // a last group that is not whole
+  auto inside = [&](int g) { return g * kGroup + 32 * kq < K; };   // of stored MXFP4 rows, a last group that is not whole
 
   // Scales: a word per lane for four groups (spread4), or for the bytes of stored MXFP4
   // rows, which need not be aligned to words, one per group.
@@ -52,14 +56,36 @@ __global__ __launch_bounds__(kMvThreads) void matvec_kernel(const uint16_t* __re
   i32x4 av[GW][4], wv[GW][NS];
   uint32_t sv[SW][NS];
   v4f bias[GW];
-  const uint16_t* xr = x + (int64_t)min(col, T - 1) * ld + 32 * kq;
+  // A row's 256 bytes of a group are read by 16 lanes side by side (an operand's lanes read 16 rows 16 bytes at a
+  // time: 64 cache lines an instruction, four times over), then change places through LDS.
+  unsigned char* a_mine = a_sm + (size_t)wave * T * kPitch;
   auto load_a = [&](int g0, int ng) {
 #pragma unroll
-    for (int i = 0; i < GW; ++i)
+    for (int i = 0; i < GW; ++i) {
 #pragma unroll
-      for (int c = 0; c < 4; ++c)
-        av[i][c] = i < ng && inside(g0 + i) ? *reinterpret_cast<const i32x4*>(xr + (int64_t)(g0 + i) * kGroup + 8 * c)
-                                            : i32x4{0, 0, 0, 0};
+      for (int j = 0; j < 4; ++j) {                            // rows 4 j + lane / 16
+        if (4 * j < T) {
+          const int k = (g0 + i) * kGroup + 8 * col;
+          av[i][j] = i < ng && k < K ? *reinterpret_cast<const i32x4*>(x + (int64_t)min(4 * j + kq, T - 1) * ld + k)
+                                     : i32x4{0, 0, 0, 0};
+        }
+      }
+    }
+  };
+  auto turn_a = [&](int ng) {
+    const int row = min(col, T - 1);
+#pragma unroll
+    for (int i = 0; i < GW; ++i) {
+      if (i < ng) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (4 * j + kq < T) *reinterpret_cast<i32x4*>(a_mine + (4 * j + kq) * kPitch + 16 * col) = av[i][j];
+        wave_lds_fence();
+#pragma unroll
+        for (int c = 0; c < 4; ++c) av[i][c] = *reinterpret_cast<const i32x4*>(a_mine + row * kPitch + 64 * kq + 16 * c);
+        wave_lds_fence();
+      }
+    }
   };
   __amdgpu_buffer_rsrc_t rw = buffer_of(w, 0), rs = buffer_of(s, 0);
   int lg0 = 0, lng = 0;                                        // the groups being loaded
@@ -109,6 +135,7 @@ __global__ __launch_bounds__(kMvThreads) void matvec_kernel(const uint16_t* __re
   }
   groups_of(0, g0, ng);
   load_a(g0, ng);
+  turn_a(ng);
   auto all_bias = [&]() {
     if constexpr (!kMx) {
 #pragma unroll
@@ -125,6 +152,7 @@ __global__ __launch_bounds__(kMvThreads) void matvec_kernel(const uint16_t* __re
       if constexpr (kParts) {                                  // the activations of this part (from the cache)
         groups_of(ch, g0, ng);
         load_a(g0, ng);
+        turn_a(ng);
         all_bias();
       }
       const bool last = ch + 1 == nch;
@@ -177,8 +205,8 @@ template <int kForm, bool kRM, int GW, bool kParts = false>
 static void launch_matvec_steps(const MatvecArgs& a, hipStream_t stream) {
   auto go = [&](auto kernel, int ns) {
     const int64_t steps = (a.N + 16 * ns - 1) / (16 * ns), wgs = GW <= 2 ? 512 : 256;
-    hipLaunchKernelGGL(kernel, dim3((unsigned)(steps < wgs ? steps : wgs)), dim3(kMvThreads), 0, stream, a.x,
-                       (int)a.T, a.K, a.ld, static_cast<const uint8_t*>(a.w), static_cast<const uint8_t*>(a.s), a.N,
+    hipLaunchKernelGGL(kernel, dim3((unsigned)(steps < wgs ? steps : wgs)), dim3(kMvThreads),
+                       (size_t)(kMvWaves * a.T * 272), stream, a.x, (int)a.T, a.K, a.ld, static_cast<const uint8_t*>(a.w), static_cast<const uint8_t*>(a.s), a.N,
                        a.y, a.y_bf16);
   };
   if (a.N >= 32 * 512) go(matvec_kernel<kForm, kRM, GW, 2, kParts>, 2);

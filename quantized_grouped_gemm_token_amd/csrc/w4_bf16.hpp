@@ -74,6 +74,12 @@ __device__ __forceinline__ i32x4 e2m1x8_to_bf16(uint32_t w, float scale) {
   return r;
 }
 
+// orders LDS accesses of one wave's lanes (the LDS itself serves a wave in order)
+__device__ __forceinline__ void wave_lds_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
 // Loads of weights and scales through buffer resources: an offset past the resource's
 // size reads as zero without touching memory, so a load of nothing (a wave's missing
 // group, the step after the last) is the same instruction as any other, and a loop
