@@ -65,6 +65,21 @@ __device__ __forceinline__ float row_scale(float amax) {
   return amax > 0.0f ? amax / (kInt8 ? 127.0f : kFp8Max) : 1.0f;
 }
 
+// What a row is divided by: values and scale times `by`, a power of two that keeps 1 / s
+// finite and the residual of div_by exact in rows of very small values; 1 in any other
+// row.  s = 0 (amax below 2^-141): the codes do not matter, 0 times a finite one.
+struct RowDivisor {
+  float s, r, by;
+};
+__device__ __forceinline__ RowDivisor row_divisor(float scale) {
+  RowDivisor d;
+  d.by = scale < 0x1p-80f ? 0x1p100f : 1.0f;
+  d.s = scale * d.by;
+  d.r = d.s > 0.0f ? 1.0f / d.s : 0.0f;
+  return d;
+}
+__device__ __forceinline__ bool rescaled(float by) { return __builtin_amdgcn_readfirstlane(__float_as_int(by)) != 0x3f800000; }
+
 // ---- routing of one token by one wave ---------------------------------------
 // fp32 -> uint32 with the order of the values (-0 as +0); 0 is below every value
 __device__ __forceinline__ uint32_t order_key(float v) {
@@ -285,10 +300,14 @@ __global__ __launch_bounds__(kFewThreads, GW <= 6 ? 4 : 2) void few_gate_up_kern
   };
   // the codes of chunk c of row t, in operand order: elements 8 c .. +7 are group c / 16, lane group
   // (c / 4) % 4, bytes 8 (c % 4) .. +7 of its 32
-  auto put_codes = [&](uint4 v, int c, int t, float sc, float rc) {
+  auto times2 = [](uint32_t v, float by) {                        // both bf16 of a word times a power of two (exact)
+    return (__float_as_uint(bf16_hi(v) * by) & 0xffff0000u) | __float_as_uint(bf16_lo(v) * by) >> 16;
+  };
+  auto put_codes = [&](uint4 v, int c, int t, RowDivisor d) {
+    if (rescaled(d.by)) v = make_uint4(times2(v.x, d.by), times2(v.y, d.by), times2(v.z, d.by), times2(v.w, d.by));
     uint2 o;
-    o.x = codes4<kInt8>(bf16_lo(v.x), bf16_hi(v.x), bf16_lo(v.y), bf16_hi(v.y), sc, rc);
-    o.y = codes4<kInt8>(bf16_lo(v.z), bf16_hi(v.z), bf16_lo(v.w), bf16_hi(v.w), sc, rc);
+    o.x = codes4<kInt8>(bf16_lo(v.x), bf16_hi(v.x), bf16_lo(v.y), bf16_hi(v.y), d.s, d.r);
+    o.y = codes4<kInt8>(bf16_lo(v.z), bf16_hi(v.z), bf16_lo(v.w), bf16_hi(v.w), d.s, d.r);
     *reinterpret_cast<uint2*>(codes + ((size_t)(c >> 2) * T + t) * 32 + 8 * (c & 3)) = o;
   };
   __syncthreads();                                                // picked and slot are set
@@ -305,14 +324,14 @@ __global__ __launch_bounds__(kFewThreads, GW <= 6 ? 4 : 2) void few_gate_up_kern
     }
     m = wave_max(m);
     if (lane == 0) wave_amax[t][0] = m;
-    const float sc = row_scale<kInt8>(m), rc = 1.0f / sc;
+    const RowDivisor d = row_divisor(row_scale<kInt8>(m));
     for (int c = lane; c < chunks; c += 256) {
       uint4 v[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) v[i] = __builtin_bit_cast(uint4, buffer_load16(rt, (c + 64 * i) * 16));
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        if (c + 64 * i < chunks) put_codes(v[i], c + 64 * i, t, sc, rc);
+        if (c + 64 * i < chunks) put_codes(v[i], c + 64 * i, t, d);
     }
   };
   if (GW > 2 && wpr == 1 && wave < T) quantize_row(wave);
@@ -324,10 +343,10 @@ __global__ __launch_bounds__(kFewThreads, GW <= 6 ? 4 : 2) void few_gate_up_kern
       for (int i = 0; i < XC; ++i) m = amax8(m, xv2[i]);
       m = wave_max(m);
       if (lane == 0) wave_amax[wave + 8][0] = m;
-      const float sc = row_scale<kInt8>(m), rc = 1.0f / sc;
+      const RowDivisor d = row_divisor(row_scale<kInt8>(m));
 #pragma unroll
       for (int i = 0; i < XC; ++i)
-        if (lane + 64 * i < chunks) put_codes(xv2[i], lane + 64 * i, wave + 8, sc, rc);
+        if (lane + 64 * i < chunks) put_codes(xv2[i], lane + 64 * i, wave + 8, d);
     } else {
       quantize_row(wave + 8);
     }
@@ -407,11 +426,11 @@ __global__ __launch_bounds__(kFewThreads, GW <= 6 ? 4 : 2) void few_gate_up_kern
   if (has_row) {                                                  // the codes of the rows in registers
     float m = 0.0f;
     for (int p = 0; p < wpr; ++p) m = fmaxf(m, wave_amax[row][p]);
-    const float sc = row_scale<kInt8>(m), rc = 1.0f / sc;
+    const RowDivisor d = row_divisor(row_scale<kInt8>(m));
 #pragma unroll
     for (int i = 0; i < XC; ++i) {
       const int c = part * 64 + lane + 64 * wpr * i;
-      if (c < chunks) put_codes(xv[i], c, row, sc, rc);
+      if (c < chunks) put_codes(xv[i], c, row, d);
       __builtin_amdgcn_sched_barrier(0);                          // one chunk at a time: few values live
     }
   }
@@ -532,7 +551,8 @@ __global__ __launch_bounds__(kFewThreads, GW <= 6 ? 4 : 2) void few_gate_up_kern
 // chunk of up to 8 groups) products that its columns sum.  The workgroups take equal
 // ranges of that row (H/16 blocks are rarely a multiple of the CUs: whole blocks would
 // leave half the CUs with half the work of the others), so a workgroup has pieces of at
-// most two blocks, and a block is summed by one to five workgroups.  Each of them leaves
+// most two blocks, and a block is summed by several workgroups (one to five at
+// H 2048 and more).  Each of them leaves
 // its sums in memory and counts itself on the block's counter; the one that arrives last
 // adds them in workgroup order (the same bits whichever that is) and writes y.  Nothing
 // waits on a counter.
@@ -567,7 +587,7 @@ __global__ __launch_bounds__(kFewThreads, 4) void few_down_kernel(int T, int64_t
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 15, kq = lane >> 4;
   const int G = (int)(I >> 7), R = T * k, cols = (int)(H >> 4);
-  float4* row_sm = reinterpret_cast<float4*>(smem);                      // [R] of routed index f: sa, 1 / sa, w sa
+  float4* row_sm = reinterpret_cast<float4*>(smem);                      // [R] of routed index f: sa and 1 / sa to divide by, w sa, `by`
   int16_t(*slot)[kFewMaxTokens] = reinterpret_cast<int16_t(*)[kFewMaxTokens]>(row_sm + R);   // [R]
   int* experts = reinterpret_cast<int*>(slot + R);                       // [R] expert | first routed index << 16
   uint32_t* routed = reinterpret_cast<uint32_t*>(experts + R);           // [R] bit t: token t picked the expert
@@ -683,7 +703,8 @@ __global__ __launch_bounds__(kFewThreads, 4) void few_down_kernel(int T, int64_t
       m = max16(m);
       if (col == 0 && f < R) {
         const float sa = row_scale<kInt8>(m);
-        row_sm[f] = make_float4(sa, 1.0f / sa, ws.weights[f] * sa, 0.0f);
+        const RowDivisor d = row_divisor(sa);
+        row_sm[f] = make_float4(d.s, d.r, ws.weights[f] * sa, d.by);
       }
     }
     if (fu + 16 * W < R) {
@@ -715,6 +736,12 @@ __global__ __launch_bounds__(kFewThreads, 4) void few_down_kernel(int T, int64_t
   auto put = [&](int row, int f) {                                       // one token's codes of a piece, from av
     const float4 r4 = row_sm[f];
     fac[row] = r4.z;
+    if (rescaled(r4.w)) {                                                // (a subnormal sa can be too small by half: clamped)
+      const float top = (kInt8 ? 127.0f : kFp8Max) * r4.x;
+      auto in = [&](float a) { return fminf(fmaxf(a * r4.w, -top), top); };
+#pragma unroll
+      for (int i = 0; i < kQuads; ++i) av[i] = make_float4(in(av[i].x), in(av[i].y), in(av[i].z), in(av[i].w));
+    }
 #pragma unroll
     for (int i = 0; i < kQuads; ++i) {
       const uint32_t c4 = codes4<kInt8>(av[i].x, av[i].y, av[i].z, av[i].w, r4.x, r4.y);

@@ -123,9 +123,10 @@ def reference(form, x_bits, logits, weights, k, renormalize=True):
         act = silu * u
         # |silu'| <= 1.1; the fast exponential and reciprocal cost 16 steps, and 2^-24 of the row in silu's far tail
         big = np.abs(act).max(1, keepdims=True)
-        dact = 1.1 * dg * np.abs(u) + np.abs(silu) * du + 1.1 * dg * du + 32 * U * np.abs(act) + U * big
+        # (two steps of the subnormals: silu and the product; half a step of sa)
+        dact = 1.1 * dg * np.abs(u) + np.abs(silu) * du + 1.1 * dg * du + 32 * U * np.abs(act) + U * big + 2.0 ** -148
         sa = np.where(big > 0, big / (127.0 if int8 else 448.0), 1.0)
-        ds = dact.max(1, keepdims=True) / np.maximum(big, 1e-300) + 4 * U        # relative error of sa
+        ds = dact.max(1, keepdims=True) / np.maximum(big, 1e-300) + 4 * U + 2.0 ** -150 / sa    # relative error of sa
         v = act / sa
         dv = dact / sa + np.abs(v) * (ds + 4 * U)
         qa = np.clip(np.rint(v), -127, 127) if int8 else \
@@ -136,7 +137,7 @@ def reference(form, x_bits, logits, weights, k, renormalize=True):
         do = flip @ np.abs(W).T * sa + np.abs(o) * ds + (g2 * (np.abs(qa) @ (np.abs(W) if int8 else B).T)) * sa
         wt = w[t, j].astype(np.float64)[:, None]
         np.add.at(y, t, wt * o)
-        np.add.at(tol, t, wt * (do * (1 + ds) + np.abs(o) * 8 * U))
+        np.add.at(tol, t, wt * (do * (1 + ds) + np.abs(o) * 8 * U) + 2.0 ** -150 * np.abs(o / sa))   # (w sa may be subnormal)
     return ids, w, y, tol + 2.0 ** -126
 
 
@@ -241,6 +242,37 @@ def test_few_zero_rows_and_outliers(form):
     y = CALL[form](bf16_to_dev(x_bits), to_dev(logits), k, *prepack(form, weights))
     assert (host(y)[0] == 0).all()
     check(form, x_bits[1:], logits[1:], weights, k, y[1:], torch.float32)
+
+
+def scale_weights(form, s, exponent):
+    """The scales times 2^exponent (MXFP4: E8M0 exponents)."""
+    if form == "mxfp4":
+        shifted = s.astype(np.int32) + exponent
+        assert shifted.min() >= 1 and shifted.max() <= 254
+        return shifted.astype(np.uint8)
+    return (s * np.float32(2.0 ** exponent)).astype(np.float32)
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("T,H", [(3, 384), (11, 384), (9, 2304)])
+def test_few_rows_of_tiny_values(form, T, H):
+    """Rows whose largest value over the largest code is subnormal: its reciprocal is infinite.  Tokens first (with
+    w13 scaled up), then act (with w13 scaled down and w2 up)."""
+    I, E, k = 256, 6, 2
+    x_bits, logits, weights = make(form, T, H, I, E, k, seed=22)
+    w13, s13, w2, s2 = weights
+    say(f"few {form} T={T} H={H} tiny rows of x")
+    tiny = oracle.f32_to_bf16_bits(oracle.bf16_bits_to_f32(x_bits) * np.float32(2.0 ** -125))
+    up = (w13, scale_weights(form, s13, 100), w2, s2)
+    y = CALL[form](bf16_to_dev(tiny), to_dev(logits), k, *prepack(form, up))
+    check(form, tiny, logits, up, k, y, torch.float32, what="tiny x")
+    for shift, bounded in ((-64, True), (-66, True), (-70, False), (-73, False), (-76, False)):
+        say(f"few {form} T={T} H={H} w13 times 2^{shift}")
+        low = (w13, scale_weights(form, s13, shift), w2, scale_weights(form, s2, 100))
+        y = CALL[form](bf16_to_dev(x_bits), to_dev(logits), k, *prepack(form, low))
+        assert torch.isfinite(y).all()
+        if bounded:                                          # (further down sa itself has few bits left)
+            check(form, x_bits, logits, low, k, y, torch.float32, what=f"tiny act {shift}")
 
 
 def test_few_strided_rows_and_neighbours_untouched():
