@@ -404,7 +404,7 @@ __global__ __launch_bounds__(kFewThreads, GW <= 6 ? 4 : 2) void few_gate_up_kern
       su[j] = buffer_load4(rs, (uint32_t)((4 * j + kq) * 2 * I + I + col) * 4);
     }
   };
-  int task = blockIdx.x, buf = 0;
+  int task = xcd_order(), buf = 0;
   point(task);
 #pragma unroll
   for (int i = 0; i < GW; ++i) {
@@ -624,9 +624,10 @@ __global__ __launch_bounds__(kFewThreads, 4) void few_down_kernel(int T, int64_t
   const int D = __builtin_amdgcn_readfirstlane(*ws.count);
   const int M = D * nch, total = cols * M;
   const int wgs = min((int)gridDim.x, total);                            // every one of them has a piece
-  if ((int)blockIdx.x >= wgs) return;
+  const int wg0 = wgs == (int)gridDim.x ? xcd_order() : (int)blockIdx.x; // the workgroup's number
+  if (wg0 >= wgs) return;
   auto range_start = [&](int wg) { return (int)((int64_t)total * wg / wgs); };
-  const int lo = range_start(blockIdx.x), hi = range_start(blockIdx.x + 1);
+  const int lo = range_start(wg0), hi = range_start(wg0 + 1);
   const int c0 = lo / M, second = (c0 + 1) * M;
 
   // The weights of a piece, and the act of one of its tokens.  Loads past the last piece,
@@ -869,7 +870,7 @@ __global__ __launch_bounds__(kFewThreads, 4) void few_down_kernel(int T, int64_t
     // holds back), so the order "sums, then the count" needs the stores to be done and no cache to be written
     // back or dropped: a device-scope fence in its place took 170 us of a 50 us launch.
     if (sums && !whole)
-      __hip_atomic_store(&ws.partial[((int64_t)(blockIdx.x * 2 + b) * T + t) * 16 + c], sum, __ATOMIC_RELAXED,
+      __hip_atomic_store(&ws.partial[((int64_t)(wg0 * 2 + b) * T + t) * 16 + c], sum, __ATOMIC_RELAXED,
                          __HIP_MEMORY_SCOPE_AGENT);
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();

@@ -126,7 +126,7 @@ __global__ __launch_bounds__(kMvThreads) void matvec_kernel(const uint16_t* __re
     }
   };
 
-  int step = blockIdx.x, buf = 0, g0, ng;
+  int step = xcd_order(), buf = 0, g0, ng;
   point(step, 0);
 #pragma unroll
   for (int i = 0; i < GW; ++i) {

@@ -117,6 +117,14 @@ __device__ __forceinline__ void spread4(uint32_t v, uint32_t (&out)[4]) {
   out[3] = b[1];
 }
 
+// This workgroup's place in an order in which neighbours share an XCD (workgroups go to the
+// 8 XCDs in turn).  Two neighbouring blocks of 16 columns share every 128-byte line of their
+// scales, which the one L2 then reads once.
+__device__ __forceinline__ int xcd_order() {
+  const int n = gridDim.x, b = blockIdx.x;
+  return n & 7 ? b : (b & 7) * (n >> 3) + (b >> 3);
+}
+
 constexpr int kMinus8 = (int)0xc100c100u;                      // two bf16 -8
 
 // A x (-8) over one K group: what A x U is too large by
