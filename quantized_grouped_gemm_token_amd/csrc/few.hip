@@ -30,7 +30,6 @@ namespace w4a8 {
 
 constexpr int kFewWaves = 8;
 constexpr int kFewThreads = 64 * kFewWaves;
-constexpr int kFewDownGroups = 8;              // most K groups of one (expert, K chunk) piece of the down product
 
 // ---- values -----------------------------------------------------------------
 // x / s rounded to fp32 from r = 1 / s rounded: q = fl(x r) is within an ulp, its
@@ -166,14 +165,14 @@ __device__ __forceinline__ void route_weights(const uint32_t* keys, const float*
 
 // ---- what the first kernel leaves for the second ------------------------------
 // Views into the caller's workspace (16-byte aligned): the number of distinct
-// experts; of each, the expert, the routed index of its first token (bits 16 up) and the
-// set of its tokens; the routed index of (expert, token) or -1; the routing weights, act [R][I] and the maxima of |act| over its 16-column blocks [R][I/16]; then
+// experts; of each, the expert (10 bits), the routed indices of its first two tokens (8 bits
+// each; one: the second counts nothing) and the set of its tokens; the routed index of (expert, token) or -1; the routing weights, act [R][I] and the maxima of |act| over its 16-column blocks [R][I/16]; then
 // what the second kernel's workgroups leave for each other: their sums of a column block
-// that they share, [workgroup][2][T][16], and a count of arrivals for each of the H/16
+// that they share, [workgroup][2][T][32], and a count of arrivals for each of the H/32
 // column blocks (set to zero by the first kernel).
 struct FewWorkspace {
   int32_t* count;
-  int32_t* experts;       // [kFewMaxRows] expert | first routed index << 16
+  uint32_t* experts;      // [kFewMaxRows] expert | first routed index << 10 | second << 18
   uint32_t* tokens;       // [kFewMaxRows] bit t: token t picked the expert
   int16_t* slot;          // [kFewMaxRows][16]
   float* weights;         // [kFewMaxRows]
@@ -186,14 +185,14 @@ __device__ __forceinline__ FewWorkspace few_workspace(void* p, int64_t T, int64_
   unsigned char* b = static_cast<unsigned char*>(p);
   FewWorkspace v;
   v.count = reinterpret_cast<int32_t*>(b);
-  v.experts = reinterpret_cast<int32_t*>(b + 16);
+  v.experts = reinterpret_cast<uint32_t*>(b + 16);
   v.weights = reinterpret_cast<float*>(b + 16 + 4 * kFewMaxRows);
   v.tokens = reinterpret_cast<uint32_t*>(b + 16 + 8 * kFewMaxRows);
   v.slot = reinterpret_cast<int16_t*>(b + 16 + 12 * kFewMaxRows);
   v.act = reinterpret_cast<float*>(b + kFewHeadBytes);
   v.pmax = v.act + R * I;
   v.partial = v.pmax + R * (I >> 4);
-  v.arrived = reinterpret_cast<uint32_t*>(v.partial + kFewDownMaxGrid * 2 * T * 16);
+  v.arrived = reinterpret_cast<uint32_t*>(v.partial + kFewDownMaxGrid * 2 * T * 32);
   return v;
 }
 
@@ -440,22 +439,22 @@ __global__ __launch_bounds__(kFewThreads, GW <= 6 ? 4 : 2) void few_gate_up_kern
                     w_out ? w_out + t * k : nullptr);
     if (f == 0) *ws.count = D;
     if (f < D) {
-      uint32_t set = 0;
-      int fa = 0;
+      uint32_t set = 0, fa = 0, fb = 0;
       for (int t = T - 1; t >= 0; --t) {
         const int v = slot[f][t];
         if (v >= 0) {
           set |= 1u << t;
-          fa = v;
+          fb = fa;
+          fa = (uint32_t)v;
         }
       }
-      ws.experts[f] = experts[f] | fa << 16;
+      ws.experts[f] = (uint32_t)experts[f] | fa << 10 | fb << 18;
       ws.tokens[f] = set;
     }
     if (f < R && ids_out) ids_out[f] = ids[f];
     for (int i = threadIdx.x; i < D * kFewMaxTokens / 2; i += kFewThreads)
       reinterpret_cast<int*>(ws.slot)[i] = reinterpret_cast<const int*>(slot)[i];
-    for (int i = threadIdx.x; i < (int)(H >> 4); i += kFewThreads) ws.arrived[i] = 0u;
+    for (int i = threadIdx.x; i < (int)(H >> 5); i += kFewThreads) ws.arrived[i] = 0u;
   }
   __syncthreads();
 
@@ -547,26 +546,42 @@ __global__ __launch_bounds__(kFewThreads, GW <= 6 ? 4 : 2) void few_gate_up_kern
 }
 
 // ---- kernel 2: requantization, down, the routing-weighted sum ----------------
-// The work is a row of pieces: for each block of 16 columns of y, the (distinct expert, K
-// chunk of up to 8 groups) products that its columns sum.  The workgroups take equal
-// ranges of that row (H/16 blocks are rarely a multiple of the CUs: whole blocks would
-// leave half the CUs with half the work of the others), so a workgroup has pieces of at
-// most two blocks, and a block is summed by several workgroups (one to five at
-// H 2048 and more).  Each of them leaves
-// its sums in memory and counts itself on the block's counter; the one that arrives last
-// adds them in workgroup order (the same bits whichever that is) and writes y.  Nothing
-// waits on a counter.
+// The work is a row of pieces: for each block of 16 NB columns of y, the (distinct expert, K
+// chunk of up to 8 / NB groups) products that its columns sum; a piece is 8 KB of weights.
+// The workgroups take equal ranges of that row, of whole rounds of their 8 waves (H/32
+// blocks are rarely a multiple of the CUs), so a workgroup has pieces of at most two
+// blocks.  It leaves its sums of a block that it shares in memory and counts itself on the
+// block's counter; the one that arrives last adds them in workgroup order (the same bits
+// whichever that is) and writes y.  Nothing waits on a counter.  Where that saves no more
+// than a round, a workgroup takes a whole block (few_down_range).
 //
 // A wave takes pieces in turn: it requantizes the act of the expert's tokens over those K
-// elements into LDS of its own, up to 2 tokens at a time as rows 0 and 1 of the A operand
-// (an expert has one or two of the few tokens as a rule; the weights stay in registers for
-// the next 2), multiplies, and adds the rows with the factors w[t, j] sa[f] to its own sums
-// in LDS.  The next piece's weights, and the act of its first token, are loaded meanwhile.
-//  Besides HBM the instructions bound this kernel (53 for a K group's product,
-// about 250 for a piece): so a piece is long, and the FP8 codes are held as the bf16 values
-// they stand for, converted once per token and piece instead of once per operand read.
-template <int kForm>
-__global__ __launch_bounds__(kFewThreads, 4) void few_down_kernel(int T, int64_t H, int k,
+// elements into LDS of its own, up to 4 tokens at a time as rows 0 to 3 of the A operand (an
+// expert has one or two of the few tokens as a rule; for more than 4 the weights stay in
+// registers), multiplies, and adds the rows with the factors w[t, j] sa[f] to its own sums
+// in LDS.  The next piece's weights, and the act of its first two tokens, are loaded
+// meanwhile.  The FP8 codes are held as the bf16 values they stand for, converted once per
+// token and piece.
+//
+// NB = 2: codes, their operands and the -8 products serve two tiles, and the scales of a
+// group are a whole line of memory.  One workgroup of 8 waves on a CU, with the registers
+// for it, reads no slower than two with half of them.
+__device__ __forceinline__ void store_y(void* y, int y_bf16, int64_t at, float v) {
+  if (y_bf16) static_cast<uint16_t*>(y)[at] = __builtin_bit_cast(uint16_t, (__bf16)v);
+  else static_cast<float*>(y)[at] = v;
+}
+template <int NB>
+struct FewDownShape {
+  static constexpr int kCols = 16 * NB;
+  static constexpr int kGroups = 8 / NB;
+};
+// pieces of a workgroup: total in all, M of a block.  A shared block costs about a round.
+__host__ __device__ inline int few_down_range(int total, int M) {
+  const int per = (total + kFewDownMaxGrid * kFewWaves - 1) / (kFewDownMaxGrid * kFewWaves) * kFewWaves;
+  return M <= per + kFewWaves ? M : per;
+}
+template <int kForm, int NB>
+__global__ __launch_bounds__(kFewThreads, 2) void few_down_kernel(int T, int64_t H, int k,
                                                                   const uint8_t* __restrict__ w2,
                                                                   const uint8_t* __restrict__ s2, int64_t I,
                                                                   void* __restrict__ workspace, void* __restrict__ y,
@@ -575,23 +590,25 @@ __global__ __launch_bounds__(kFewThreads, 4) void few_down_kernel(int T, int64_t
   using Acc = typename P::Acc;
   constexpr bool kInt8 = P::kInt8;
   constexpr int W = kFewWaves;
-  constexpr int CG = kFewDownGroups;
-  constexpr int SW = (CG + 3) / 4;                                       // scale words per lane
-  constexpr int kRows = 2;                                               // rows of A in use
+  constexpr int CG = FewDownShape<NB>::kGroups;
+  constexpr int kDownCols = FewDownShape<NB>::kCols;
+  constexpr int kRows = 4;                                               // rows of A in use
+  constexpr int SW = (CG + 3) / 4;                                       // scale words per lane and tile
   constexpr int kQuads = CG * kGroup / 4 / 64;                           // float4 of act per lane, token and piece
   // the wave's A rows: FP8 forms [CG][4 products][4 lane groups][rows][16 bytes], INT8 form [CG][4][rows][32 bytes]
   __shared__ __attribute__((aligned(16))) uint8_t a_sm[W][CG * kGroup * kRows * (kInt8 ? 1 : 2)];
+  __shared__ int last_sm[2];
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];   // few_down_smem bytes
 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 15, kq = lane >> 4;
-  const int G = (int)(I >> 7), R = T * k, cols = (int)(H >> 4);
+  const int G = (int)(I >> 7), R = T * k, cols = (int)(H / kDownCols);
   float4* row_sm = reinterpret_cast<float4*>(smem);                      // [R] of routed index f: sa and 1 / sa to divide by, w sa, `by`
   int16_t(*slot)[kFewMaxTokens] = reinterpret_cast<int16_t(*)[kFewMaxTokens]>(row_sm + R);   // [R]
-  int* experts = reinterpret_cast<int*>(slot + R);                       // [R] expert | first routed index << 16
-  uint32_t* routed = reinterpret_cast<uint32_t*>(experts + R);           // [R] bit t: token t picked the expert
-  float* y_sm = reinterpret_cast<float*>(routed + R);                    // [W][2 blocks][T][16]
+  uint32_t* experts = reinterpret_cast<uint32_t*>(slot + R);             // [R] as in the workspace
+  uint32_t* routed = experts + R;                                        // [R] bit t: token t picked the expert
+  float* y_sm = reinterpret_cast<float*>(routed + R);                    // [W][2 blocks][T][kDownCols]
   const int nch = (G + CG - 1) / CG, cg = (G + nch - 1) / nch;           // K chunks of an expert, groups of a chunk
   const FewWorkspace ws = few_workspace(workspace, T, R, I);
 
@@ -611,11 +628,10 @@ __global__ __launch_bounds__(kFewThreads, 4) void few_down_kernel(int T, int64_t
 
   // every distinct expert's words, lane l holding numbers l, l + 64, ..: with the count they are one round trip to
   // memory before the first weights (words past the count are not used)
-  int pe[kFewMaxRows / 64];
-  uint32_t pt[kFewMaxRows / 64];
+  uint32_t pe[kFewMaxRows / 64], pt[kFewMaxRows / 64];
 #pragma unroll
   for (int i = 0; i < kFewMaxRows / 64; ++i) {
-    pe[i] = lane + 64 * i < R ? ws.experts[lane + 64 * i] : 0;
+    pe[i] = lane + 64 * i < R ? ws.experts[lane + 64 * i] : 0u;
     pt[i] = lane + 64 * i < R ? ws.tokens[lane + 64 * i] : 0u;
   }
 
@@ -623,24 +639,22 @@ __global__ __launch_bounds__(kFewThreads, 4) void few_down_kernel(int T, int64_t
   // `second` are of block c0, the others of c0 + 1 (a range is at most M long)
   const int D = __builtin_amdgcn_readfirstlane(*ws.count);
   const int M = D * nch, total = cols * M;
-  const int wgs = min((int)gridDim.x, total);                            // every one of them has a piece
-  const int wg0 = wgs == (int)gridDim.x ? xcd_order() : (int)blockIdx.x; // the workgroup's number
-  if (wg0 >= wgs) return;
-  auto range_start = [&](int wg) { return (int)((int64_t)total * wg / wgs); };
-  const int lo = range_start(wg0), hi = range_start(wg0 + 1);
+  const int per = NB == 1 ? M : few_down_range(total, M);                // pieces of a workgroup
+  const int lo = (NB == 1 ? xcd_order() : (int)blockIdx.x) * per, hi = min(lo + per, total);
+  if (lo >= total) return;
   const int c0 = lo / M, second = (c0 + 1) * M;
 
-  // The weights of a piece, and the act of one of its tokens.  Loads past the last piece,
+  // The weights of a piece, and the act of its first two tokens.  Loads past the last piece,
   // or of a token that is not there, read nothing.
   struct Piece {
     int d, g0, ng, block;  // ng = 0: none
     uint32_t tokens;       // bit t: token t picked the expert
-    int f;                 // routed index of the first, -1: none
+    int fa, fb;            // routed indices of the first two, -1: none
   };
-  i32x4 w[CG];
-  uint32_t s[SW];
-  float4 av[kQuads];
-  __amdgpu_buffer_rsrc_t rw, rs;
+  i32x4 w[NB][CG];
+  uint32_t s[NB][SW];
+  float4 av[2][kQuads];
+  __amdgpu_buffer_rsrc_t rw[NB], rs;
   auto piece_at = [&](int it) {
     Piece p;
     const bool on = it < hi;
@@ -651,41 +665,56 @@ __global__ __launch_bounds__(kFewThreads, 4) void few_down_kernel(int T, int64_t
     p.ng = on ? min(cg, G - p.g0) : 0;
     return p;
   };
+  auto set_tokens = [&](Piece& p, uint32_t expert, uint32_t tokens) {
+    p.tokens = tokens;
+    p.fa = p.ng ? (int)(expert >> 10 & 0xffu) : -1;
+    p.fb = p.ng && (tokens & (tokens - 1)) ? (int)(expert >> 18 & 0xffu) : -1;
+  };
   auto point = [&](int64_t e, const Piece& p) {
     const int cb = c0 + p.block;
-    rw = buffer_of(w2 + ((e * (H >> 4) + cb) * G + p.g0) * 1024, p.ng * 1024);
-    if constexpr (!kInt8)
-      rs = buffer_of(s2 + ((e * G + p.g0) * H + 16 * cb) * 4, p.ng ? ((int)H * p.ng - 16 * cb) * 4 : 0);
-  };
-  auto load = [&](int i) { w[i] = buffer_load16_nt(rw, col * 64 + kq * 16 + i * 1024); };
-  auto load_scales = [&]() {                                             // (before the weights)
-    if constexpr (!kInt8) {
 #pragma unroll
-      for (int j = 0; j < SW; ++j) s[j] = buffer_load4(rs, (uint32_t)((4 * j + kq) * (int)H + col) * 4);
+    for (int j = 0; j < NB; ++j)
+      rw[j] = buffer_of(w2 + ((e * (H >> 4) + NB * cb + j) * G + p.g0) * 1024, p.ng * 1024);
+    if constexpr (kInt8) rs = buffer_of(s2 + (e * H + kDownCols * cb) * 4, p.ng ? kDownCols * 4 : 0);
+    else rs = buffer_of(s2 + ((e * G + p.g0) * H + kDownCols * cb) * 4, p.ng ? ((int)H * p.ng - kDownCols * cb) * 4 : 0);
+  };
+  auto load = [&](int i) {
+#pragma unroll
+    for (int j = 0; j < NB; ++j) w[j][i] = buffer_load16_nt(rw[j], col * 64 + kq * 16 + i * 1024);
+  };
+  // before the weights.  INT8 form: the scale of the column that the lane adds up (add_rows)
+  auto load_scales = [&]() {
+    if constexpr (kInt8) {
+      s[0][0] = buffer_load4(rs, (lane & (kDownCols - 1)) * 4);
+    } else {
+#pragma unroll
+      for (int m = 0; m < SW; ++m)
+#pragma unroll
+        for (int j = 0; j < NB; ++j) s[j][m] = buffer_load4(rs, (uint32_t)((4 * m + kq) * (int)H + 16 * j + col) * 4);
     }
   };
-  auto load_act = [&](int f, int g0, int ng) {                           // f < 0: nothing
-    const __amdgpu_buffer_rsrc_t ra = buffer_of(ws.act + (int64_t)max(f, 0) * I + g0 * kGroup,
-                                                f >= 0 ? ng * kGroup * 4 : 0);
+  auto load_act = [&](int a, int f, const Piece& p) {                    // f < 0: nothing
+    const __amdgpu_buffer_rsrc_t ra = buffer_of(ws.act + (int64_t)max(f, 0) * I + p.g0 * kGroup,
+                                                f >= 0 ? p.ng * kGroup * 4 : 0);
 #pragma unroll
     for (int q = 0; q < kQuads; ++q)
-      av[q] = __builtin_bit_cast(float4, buffer_load16(ra, (lane + 64 * q) * 16));
+      av[a][q] = __builtin_bit_cast(float4, buffer_load16(ra, (lane + 64 * q) * 16));
   };
   // the first piece of the wave, from what the first kernel left in memory
   Piece cur = piece_at(lo + wave);
   {
-    int e = 0;
-    cur.tokens = 0;
+    uint32_t e = 0, set = 0;
 #pragma unroll
     for (int i = 0; i < kFewMaxRows / 64; ++i) {
       if (cur.d >> 6 == i) {
-        e = __builtin_amdgcn_readlane(pe[i], cur.d & 63);
-        cur.tokens = __builtin_amdgcn_readlane((int)pt[i], cur.d & 63);
+        e = (uint32_t)__builtin_amdgcn_readlane((int)pe[i], cur.d & 63);
+        set = (uint32_t)__builtin_amdgcn_readlane((int)pt[i], cur.d & 63);
       }
     }
-    cur.f = cur.ng ? e >> 16 : -1;
-    load_act(cur.f, cur.g0, cur.ng);
-    point(e & 0xffff, cur);
+    set_tokens(cur, e, set);
+    load_act(0, cur.fa, cur);
+    load_act(1, cur.fb, cur);
+    point(e & 0x3ffu, cur);
     load_scales();
 #pragma unroll
     for (int i = 0; i < CG; ++i) load(i);
@@ -724,7 +753,7 @@ __global__ __launch_bounds__(kFewThreads, 4) void few_down_kernel(int T, int64_t
   }
   for (int i = threadIdx.x; i < D * kFewMaxTokens / 2; i += kFewThreads)
     reinterpret_cast<int*>(slot)[i] = reinterpret_cast<const int*>(ws.slot)[i];
-  for (int i = threadIdx.x; i < W * 2 * T * 16; i += kFewThreads) y_sm[i] = 0.0f;
+  for (int i = threadIdx.x; i < W * 2 * T * kDownCols; i += kFewThreads) y_sm[i] = 0.0f;
   __syncthreads();
 
   uint8_t* mine = a_sm[wave];
@@ -733,19 +762,21 @@ __global__ __launch_bounds__(kFewThreads, 4) void few_down_kernel(int T, int64_t
   uint8_t* put_at = mine + (kInt8 ? (lane >> 3) * kRows * 32 + 4 * (lane & 7)
                                   : (((lane >> 5) * 4 + ((lane & 7) >> 1)) * 4 + ((lane >> 3) & 3)) * kRows * 16 + 8 * (lane & 1));
   constexpr int kPutStep = kInt8 ? 8 * kRows * 32 : 2 * 16 * kRows * 16;  // two groups on
-  float fac[kRows];                                                      // w sa of the rows
-  auto put = [&](int row, int f) {                                       // one token's codes of a piece, from av
+  const int r0 = NB == 2 ? 2 * (lane >> 5) : kq;                         // see add_rows
+  float fac[NB];                                                         // w sa of the rows r0 and (NB = 2) r0 + 1
+  auto put = [&](int row, int a, int f) {                                // one token's codes of a piece, from av[a]
     const float4 r4 = row_sm[f];
-    fac[row] = r4.z;
+    fac[row % NB] = row < NB || r0 == row / NB * NB ? r4.z : fac[row % NB];
     if (rescaled(r4.w)) {                                                // (a subnormal sa can be too small by half: clamped)
       const float top = (kInt8 ? 127.0f : kFp8Max) * r4.x;
-      auto in = [&](float a) { return fminf(fmaxf(a * r4.w, -top), top); };
+      auto in = [&](float v) { return fminf(fmaxf(v * r4.w, -top), top); };
 #pragma unroll
-      for (int i = 0; i < kQuads; ++i) av[i] = make_float4(in(av[i].x), in(av[i].y), in(av[i].z), in(av[i].w));
+      for (int i = 0; i < kQuads; ++i)
+        av[a][i] = make_float4(in(av[a][i].x), in(av[a][i].y), in(av[a][i].z), in(av[a][i].w));
     }
 #pragma unroll
     for (int i = 0; i < kQuads; ++i) {
-      const uint32_t c4 = codes4<kInt8>(av[i].x, av[i].y, av[i].z, av[i].w, r4.x, r4.y);
+      const uint32_t c4 = codes4<kInt8>(av[a][i].x, av[a][i].y, av[a][i].z, av[a][i].w, r4.x, r4.y);
       if constexpr (kInt8) {
         *reinterpret_cast<uint32_t*>(put_at + i * kPutStep + row * 32) = c4;
       } else {
@@ -756,91 +787,111 @@ __global__ __launch_bounds__(kFewThreads, 4) void few_down_kernel(int T, int64_t
       }
     }
   };
-  uint32_t s4[SW][4];
-  auto product = [&](int i, Acc& acc, int row) {                         // row: the lane's row of A
+  uint32_t s4[NB][SW][4];
+  auto product = [&](int i, Acc (&acc)[NB]) {                             // lane row col of A is row col % 4 of LDS
     P p;
     if constexpr (kInt8) {
-      p.set_codes(*reinterpret_cast<const v8i*>(mine + ((i * 4 + kq) * kRows + row) * 32));
+      p.set_codes(*reinterpret_cast<const v8i*>(mine + ((i * 4 + kq) * kRows + (col & 3)) * 32));
     } else {
 #pragma unroll
       for (int c = 0; c < 4; ++c)
-        p.ab[c] = *reinterpret_cast<const i32x4*>(mine + (((i * 4 + c) * 4 + kq) * kRows + row) * 16);
+        p.ab[c] = *reinterpret_cast<const i32x4*>(mine + (((i * 4 + c) * 4 + kq) * kRows + (col & 3)) * 16);
       p.set_bias();
     }
-    uint32_t fs = 0;
-    if constexpr (!kInt8) fs = kForm == kFormMx ? (s4[i >> 2][i & 3] >> (8 * kq)) & 0xffu : s4[i >> 2][i & 3];
-    p.add(w[i], fs, acc);
+#pragma unroll
+    for (int j = 0; j < NB; ++j) {
+      uint32_t fs = 0;
+      if constexpr (!kInt8) fs = kForm == kFormMx ? (s4[j][i >> 2][i & 3] >> (8 * kq)) & 0xffu : s4[j][i >> 2][i & 3];
+      p.add(w[j][i], fs, acc[j]);
+    }
   };
-  // rows 0 and 1 of the tile (lanes 0..15) to the sums of the first two tokens of `set`
-  auto add_rows = [&](const Acc& acc, uint32_t set) {
-    float ws_n = 1.0f;
-    if constexpr (kInt8)
-      ws_n = reinterpret_cast<const float*>(s2)[(int64_t)(experts[cur.d] & 0xffff) * H + 16 * (c0 + cur.block) + col];
-    float* base = y_sm + ((size_t)(wave * 2 + cur.block) * T) * 16 + col;
-    if (lane < 16) {
-      float* at = base + __builtin_ctz(set) * 16;
-      *at = fmaf(fac[0], kInt8 ? (float)acc[0] * ws_n : (float)acc[0], *at);
-      set &= set - 1;
-      if (set) {
-        at = base + __builtin_ctz(set) * 16;
-        *at = fmaf(fac[1], kInt8 ? (float)acc[1] * ws_n : (float)acc[1], *at);
+  // Rows 0 to 3 to the sums of the first four tokens of `set`.  A row stands in every lane group's tiles
+  // (register r: row r).  NB = 2: lane group q takes tile q % 2 and the rows r0 = 2 (q / 2) and r0 + 1; NB = 1: row q.
+  auto add_rows = [&](const Acc (&acc)[NB], uint32_t set) {
+    const uint32_t set1 = set & (set - 1), set2 = set1 & (set1 - 1), set3 = set2 & (set2 - 1);
+    float* base = y_sm + ((size_t)(wave * 2 + cur.block) * T) * kDownCols + (lane & (kDownCols - 1));
+    auto add = [&](uint32_t from, float f, float v) {                    // to the lowest token of `from`
+      if constexpr (kInt8) v *= __uint_as_float(s4[0][0][0]);
+      if (from) {
+        float* at = base + (__builtin_ctz(from | 0x80000000u) & 15) * kDownCols;
+        *at = fmaf(f, v, *at);
       }
+    };
+    if constexpr (NB == 2) {
+      const bool odd = kq & 1;
+      const auto a0 = odd ? acc[1][0] : acc[0][0], a1 = odd ? acc[1][1] : acc[0][1];
+      const auto a2 = odd ? acc[1][2] : acc[0][2], a3 = odd ? acc[1][3] : acc[0][3];
+      add(r0 ? set2 : set, fac[0], (float)(r0 ? a2 : a0));
+      add(r0 ? set3 : set1, fac[1], (float)(r0 ? a3 : a1));
+    } else {
+      const auto a01 = kq & 1 ? acc[0][1] : acc[0][0], a23 = kq & 1 ? acc[0][3] : acc[0][2];
+      const uint32_t s01 = kq & 1 ? set1 : set, s23 = kq & 1 ? set3 : set2;
+      add(kq & 2 ? s23 : s01, fac[0], (float)(kq & 2 ? a23 : a01));
     }
   };
   for (int it = lo + wave; it < hi; it += W) {
-    if constexpr (!kInt8) {
+    if constexpr (kInt8) {
+      s4[0][0][0] = s[0][0];
+    } else {
 #pragma unroll
-      for (int j = 0; j < SW; ++j) spread4(s[j], s4[j]);
+      for (int m = 0; m < SW; ++m)
+#pragma unroll
+        for (int j = 0; j < NB; ++j) spread4(s[j][m], s4[j][m]);
     }
-    uint32_t tokens = cur.tokens, next = tokens & (tokens - 1);          // at least one bit
-    put(0, cur.f);
-    auto take = [&]() {                                                  // the routed index of the next token
-      const int f = __builtin_amdgcn_readfirstlane((int)slot[cur.d][__builtin_ctz(next)]);
+    uint32_t tokens = cur.tokens, next = tokens;                         // at least one bit
+    int fa = cur.fa, fb = cur.fb;                                        // the tokens whose act av holds
+    auto take = [&]() {                                                  // the routed index of the next token, -1: none
+      const int f = next ? __builtin_amdgcn_readfirstlane((int)slot[cur.d][__builtin_ctz(next | 0x80000000u) & 15]) : -1;
       next &= next - 1;
       return f;
     };
-    if (next) {
-      const int f = take();
-      load_act(f, cur.g0, cur.ng);
-      put(1, f);
-    }
-    while (next) {                                                       // more than 2 tokens: the same weights again
+    next &= next - 1;
+    next &= next - 1;
+    for (;;) {
+      put(0, 0, fa);
+      if (fb >= 0) put(1, 1, fb);
+      if (next) {
+        const int fc = take(), fd = take();
+        load_act(0, fc, cur);
+        load_act(1, fd, cur);
+        put(2, 0, fc);
+        if (fd >= 0) put(3, 1, fd);
+      }
+      wave_lds_fence();
+      if (!next) break;
+      // more than 4 tokens: the same weights again
       // (opaque here: hoisted out of the loop, the unpacked weights would take a third more registers)
 #pragma unroll
-      for (int i = 0; i < CG; ++i) asm volatile("" : "+v"(w[i]));
-      const uint32_t set = next;
-      const int fa = take();
-      load_act(fa, cur.g0, cur.ng);
-      wave_lds_fence();
-      Acc acc = Acc{0, 0, 0, 0};
+      for (int i = 0; i < CG; ++i)
+#pragma unroll
+        for (int j = 0; j < NB; ++j) asm volatile("" : "+v"(w[j][i]));
+      const uint32_t rest = next;
+      fa = take();
+      fb = take();
+      load_act(0, fa, cur);
+      load_act(1, fb, cur);
+      Acc acc[NB] = {};
 #pragma unroll
       for (int i = 0; i < CG; ++i)
-        if (i < cur.ng) product(i, acc, col & 1);
+        if (i < cur.ng) product(i, acc);
       add_rows(acc, tokens);
       wave_lds_fence();
-      tokens = set;
-      put(0, fa);
-      if (next) {
-        const int fb = take();
-        load_act(fb, cur.g0, cur.ng);
-        put(1, fb);
-      }
+      tokens = rest;
     }
-    const int ng = cur.ng, row = tokens & (tokens - 1) ? col & 1 : 0;
-    wave_lds_fence();
+    const int ng = cur.ng;
     Piece nx = piece_at(it + W);
     {
-      nx.tokens = __builtin_amdgcn_readfirstlane(routed[nx.d]);
-      const int e = __builtin_amdgcn_readfirstlane(experts[nx.d]);
-      nx.f = nx.ng ? e >> 16 : -1;
-      load_act(nx.f, nx.g0, nx.ng);
-      point(e & 0xffff, nx);
-      load_scales();
+      const uint32_t e = (uint32_t)__builtin_amdgcn_readfirstlane((int)experts[nx.d]);
+      set_tokens(nx, e, (uint32_t)__builtin_amdgcn_readfirstlane((int)routed[nx.d]));
+      load_act(0, nx.fa, nx);
+      load_act(1, nx.fb, nx);
+      point(e & 0x3ffu, nx);
     }
-    Acc acc = Acc{0, 0, 0, 0};
+    load_scales();
+    Acc acc[NB] = {};
 #pragma unroll
     for (int i = 0; i < CG; ++i) {
-      if (i < ng) product(i, acc, row);
+      if (i < ng) product(i, acc);
       load(i);
     }
     add_rows(acc, tokens);
@@ -849,63 +900,79 @@ __global__ __launch_bounds__(kFewThreads, 4) void few_down_kernel(int T, int64_t
   }
   __syncthreads();
 
-  // The block's sums: threads 0 .. 255 take block c0, the others c0 + 1; one per (token, column).
-  const int b = threadIdx.x >> 8, t = (threadIdx.x >> 4) & 15, c = threadIdx.x & 15;
-  const int cb = c0 + b;
-  const int first = cb * M, end = first + M;                             // the block's pieces
-  const bool here = b == 0 || hi > second;                               // some are this workgroup's
-  const bool whole = here && lo <= first && end <= hi;
-  const bool sums = here && t < T;
-  float sum = 0.0f;
-  if (sums) {
+  // The blocks' sums: a thread per (token, column) of each.
+  const int t = threadIdx.x / kDownCols, c = threadIdx.x % kDownCols;
+  if constexpr (NB == 1) {
+    if (t < T) {
+      float sum = 0.0f;
 #pragma unroll
-    for (int v = 0; v < W; ++v) sum += y_sm[((size_t)(v * 2 + b) * T + t) * 16 + c];
+      for (int v = 0; v < W; ++v) sum += y_sm[((size_t)(v * 2) * T + t) * kDownCols + c];
+      store_y(y, y_bf16, (int64_t)t * H + kDownCols * c0 + c, sum);
+    }
+    return;
   }
-  bool writes = sums && whole;
-  if (lo > c0 * M || hi < second || hi > second) {                       // (the same for every thread) a block is shared
-    __shared__ int last_sm[2];
-    // The workgroups before and after: piece p is in number ((p + 1) wgs - 1) / total.
-    const int from = (int)(((int64_t)(first + 1) * wgs - 1) / total), to = (int)(((int64_t)end * wgs - 1) / total);
+  float sum[2] = {0.0f, 0.0f};
+  bool here[2], whole[2], writes[2];                                     // the workgroup has some of the block, all of it
+#pragma unroll
+  for (int b = 0; b < 2; ++b) {
+    here[b] = b == 0 || hi > second;
+    whole[b] = here[b] && lo <= second - M + b * M && hi >= second + b * M;
+    writes[b] = t < T && whole[b];
+    if (t < T && here[b]) {
+#pragma unroll
+      for (int v = 0; v < W; ++v) sum[b] += y_sm[((size_t)(v * 2 + b) * T + t) * kDownCols + c];
+    }
+  }
+  if (!whole[0] || here[1]) {                                            // (the same for every thread) a block is shared
     // The sums go to and come from the point where all XCDs' caches meet (device-scope accesses, which no cache
     // holds back), so the order "sums, then the count" needs the stores to be done and no cache to be written
     // back or dropped: a device-scope fence in its place took 170 us of a 50 us launch.
-    if (sums && !whole)
-      __hip_atomic_store(&ws.partial[((int64_t)(wg0 * 2 + b) * T + t) * 16 + c], sum, __ATOMIC_RELAXED,
-                         __HIP_MEMORY_SCOPE_AGENT);
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+      if (t < T && here[b] && !whole[b])
+        __hip_atomic_store(&ws.partial[((int64_t)(blockIdx.x * 2 + b) * T + t) * kDownCols + c], sum[b], __ATOMIC_RELAXED,
+                           __HIP_MEMORY_SCOPE_AGENT);
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
-    if ((threadIdx.x & 255) == 0)
-      last_sm[b] = here && !whole &&
-                   __hip_atomic_fetch_add(&ws.arrived[cb], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
-                       (uint32_t)(to - from);
+    if (threadIdx.x < 2) {
+      const int b = threadIdx.x, first = second - M + b * M;
+      const bool shared = b ? here[1] && !whole[1] : !whole[0];
+      // the workgroups with pieces of the block: first / per .. (first + M - 1) / per
+      last_sm[b] = shared && __hip_atomic_fetch_add(&ws.arrived[c0 + b], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
+                                 (uint32_t)((first + M - 1) / per - first / per);
+    }
     __syncthreads();
-    if (sums && !whole && last_sm[b]) {
-      writes = true;
-      sum = 0.0f;
-      for (int wg = from; wg <= to; ++wg) {                              // (block c is the second one of a range that starts before it)
-        const int half = range_start(wg) < first ? 1 : 0;
-        sum += __hip_atomic_load(&ws.partial[((int64_t)(wg * 2 + half) * T + t) * 16 + c], __ATOMIC_RELAXED,
-                                 __HIP_MEMORY_SCOPE_AGENT);
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      if (t < T && here[b] && !whole[b] && last_sm[b]) {
+        const int first = second - M + b * M;
+        writes[b] = true;
+        sum[b] = 0.0f;
+        for (int wg = first / per; wg <= (first + M - 1) / per; ++wg) {  // (the block is the second one of a range that starts before it)
+          const int half = wg * per < first ? 1 : 0;
+          sum[b] += __hip_atomic_load(&ws.partial[((int64_t)(wg * 2 + half) * T + t) * kDownCols + c], __ATOMIC_RELAXED,
+                                      __HIP_MEMORY_SCOPE_AGENT);
+        }
       }
     }
   }
-  if (writes) {
-    const int64_t at = (int64_t)t * H + 16 * cb + c;
-    if (y_bf16) static_cast<uint16_t*>(y)[at] = __builtin_bit_cast(uint16_t, (__bf16)sum);
-    else static_cast<float*>(y)[at] = sum;
-  }
+#pragma unroll
+  for (int b = 0; b < 2; ++b)
+    if (writes[b]) store_y(y, y_bf16, (int64_t)t * H + kDownCols * (c0 + b) + c, sum[b]);
 }
 
 // ---- launches ------------------------------------------------------------------
-// dynamic LDS of the second kernel: per routed row its scales, slots, expert and token set, then the waves' sums
-static size_t few_down_smem(int64_t R, int64_t T) { return (size_t)(56 * R + kFewWaves * 2 * T * 64); }
+// Whole blocks of 32 columns fill too few CUs below this many: then blocks of 16.
+constexpr int64_t kFewMinBlocks = 128;
 
-// From 48 pieces per column block (6 per wave) on, 512 workgroups take equal ranges; below,
-// a workgroup takes a whole block, which saves the exchange of sums.  Measured, equal ranges
-// against whole blocks (I 2048, 384 blocks, group 128): 1 token (16 pieces) 17.8 against 17.2
-// us, 3 tokens (48) 33.9 against 37.2, 16 tokens (256) 139 against 162; 128 blocks, MXFP4:
-// 32 pieces 13.7 against 12.5 us, 128 pieces 25.1 against 30.9.
-constexpr int64_t kFewSplitPieces = 48;
+template <int kForm, int NB>
+static void launch_few_down(const FewArgs& a, unsigned grid, hipStream_t stream) {
+  const int64_t R = a.T * a.k;
+  // dynamic LDS: per routed row its scales, slots, expert and token set, then the waves' sums
+  const size_t smem = (size_t)(56 * R + kFewWaves * 2 * a.T * FewDownShape<NB>::kCols * 4);
+  hipLaunchKernelGGL((few_down_kernel<kForm, NB>), dim3(grid), dim3(kFewThreads), smem, stream, (int)a.T, a.H, a.k,
+                     static_cast<const uint8_t*>(a.w2), static_cast<const uint8_t*>(a.s2), a.I, a.workspace, a.y, a.y_bf16);
+}
 
 template <int kForm, int GW, int S>
 static hipError_t launch_few_form(const FewArgs& a, hipStream_t stream) {
@@ -918,13 +985,16 @@ static hipError_t launch_few_form(const FewArgs& a, hipStream_t stream) {
                      a.ld, a.logits, a.E, a.k, a.renormalize, static_cast<const uint8_t*>(a.w13),
                      static_cast<const uint8_t*>(a.s13), a.I, a.ids, a.w, a.workspace);
   if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
-  const int64_t nch = (a.I / kGroup + kFewDownGroups - 1) / kFewDownGroups;
-  const int64_t pieces = (R < a.E ? R : a.E) * nch;                      // of a column block, at most
-  const unsigned cols = (unsigned)(a.H >> 4);
-  const unsigned nw = pieces >= kFewSplitPieces ? (unsigned)kFewDownMaxGrid : cols;
-  hipLaunchKernelGGL((few_down_kernel<kForm>), dim3(nw), dim3(kFewThreads),
-                     few_down_smem(R, a.T), stream, (int)a.T, a.H, a.k, static_cast<const uint8_t*>(a.w2),
-                     static_cast<const uint8_t*>(a.s2), a.I, a.workspace, a.y, a.y_bf16);
+  // at most M pieces of each of `cols` blocks of 32 columns
+  const int64_t groups = FewDownShape<2>::kGroups, nch = (a.I / kGroup + groups - 1) / groups;
+  const int64_t M = (R < a.E ? R : a.E) * nch, cols = a.H / FewDownShape<2>::kCols;
+  if (cols < kFewMinBlocks && few_down_range((int)(cols * M), (int)M) == M) {
+    launch_few_down<kForm, 1>(a, (unsigned)(a.H / 16), stream);
+  } else {
+    // whatever the number of distinct experts, ranges are whole blocks or whole rounds of the waves
+    const int64_t rounds = (cols * M + kFewWaves - 1) / kFewWaves, wgs = rounds > cols ? rounds : cols;
+    launch_few_down<kForm, 2>(a, (unsigned)(wgs < kFewDownMaxGrid ? wgs : kFewDownMaxGrid), stream);
+  }
   return hipGetLastError();
 }
 

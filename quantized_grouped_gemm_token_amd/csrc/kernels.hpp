@@ -109,12 +109,12 @@ constexpr int64_t kFewMaxH = 8192;       // 8 K groups for each of a workgroup's
 // bytes of activation codes a workgroup holds in LDS (T H), next to 32 KB of partial
 // tiles and 13 KB of routing
 constexpr int64_t kFewMaxCodes = 112 << 10;
-constexpr int kFewDownMaxGrid = 512;     // workgroups of the second kernel (at least H/16)
+constexpr int kFewDownMaxGrid = 256;     // workgroups of the second kernel (at least H/32)
 // the workspace: the routing (count, experts, weights, token sets, slots), act [R][I] and its block maxima [R][I/16], the second
-// kernel's shared sums [kFewDownMaxGrid][2][T][16] and arrival counts [kFewMaxH/16]
+// kernel's shared sums [kFewDownMaxGrid][2][T][32] and arrival counts [kFewMaxH/32]
 constexpr int64_t kFewHeadBytes = 16 + 12 * kFewMaxRows + 2 * kFewMaxRows * kFewMaxTokens;
 constexpr int64_t few_workspace_bytes(int64_t T, int64_t k, int64_t I) {
-  return kFewHeadBytes + 4 * (T * k * (I + I / 16) + kFewDownMaxGrid * 2 * T * 16 + kFewMaxH / 16);
+  return kFewHeadBytes + 4 * (T * k * (I + I / 16) + kFewDownMaxGrid * 2 * T * 32 + kFewMaxH / 32);
 }
 // dynamic LDS of the first kernel: the codes, then two buffers of partial tiles
 constexpr int64_t few_gate_up_smem(int64_t T, int64_t H) { return T * H + 2048 * T; }

@@ -34,6 +34,9 @@ SHAPES = [
     (16, 512, 256, 300, 16),         # the most routed rows (256), more than 256 experts
     (1, 128, 128, 1024, 64),         # one group each, the most experts
     (14, 8192, 128, 8, 2),           # the longest rows, the most codes in LDS
+    (3, 8192, 128, 64, 8),           # the most column blocks, 17 to 24 pieces in each
+    (2, 8192, 640, 16, 8),           # .. and a range of pieces that is nearly a block
+    (16, 384, 2176, 5, 2),           # 12 column blocks shared by many workgroups
     (9, 2304, 1280, 20, 3),          # two rows of work per wave in the quantizer's second pass
 ]
 
