@@ -201,15 +201,17 @@ __global__ __launch_bounds__(kMvThreads) void matvec_kernel(const uint16_t* __re
   }
 }
 
+constexpr int64_t kMvGrid = 256;             // one workgroup on each CU
+
 template <int kForm, bool kRM, int GW, bool kParts = false>
 static void launch_matvec_steps(const MatvecArgs& a, hipStream_t stream) {
   auto go = [&](auto kernel, int ns) {
-    const int64_t steps = (a.N + 16 * ns - 1) / (16 * ns), wgs = GW <= 2 ? 512 : 256;
+    const int64_t steps = (a.N + 16 * ns - 1) / (16 * ns), wgs = kMvGrid;
     hipLaunchKernelGGL(kernel, dim3((unsigned)(steps < wgs ? steps : wgs)), dim3(kMvThreads),
                        (size_t)(kMvWaves * a.T * 272), stream, a.x, (int)a.T, a.K, a.ld, static_cast<const uint8_t*>(a.w), static_cast<const uint8_t*>(a.s), a.N,
                        a.y, a.y_bf16);
   };
-  if (a.N >= 32 * 512) go(matvec_kernel<kForm, kRM, GW, 2, kParts>, 2);
+  if (a.N >= (kParts ? 32 : 64) * kMvGrid) go(matvec_kernel<kForm, kRM, GW, 2, kParts>, 2);
   else go(matvec_kernel<kForm, kRM, GW, 1, kParts>, 1);
 }
 
