@@ -604,6 +604,9 @@ int w4a8_moe_grouped_gemm_swiglu_mxfp4_prepacked(const uint8_t* a, const float* 
  *               take the seven calls.
  *   Logits of -infinity rank last and get weight zero.  Whatever the logits hold,
  *   every id written is in [0, E) and no memory outside the arrays is touched.
+ *   x is finite: a token with a NaN or an infinity has a row of y without meaning
+ *   (NaN in the FP8 forms); the other tokens' rows are what they are without it.
+ *   The same inputs give the same bits at every call.
  */
 
 /* Bytes of device workspace the _few calls need, or -1 on sizes outside their rules. */

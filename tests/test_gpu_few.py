@@ -278,6 +278,25 @@ def test_few_rows_of_tiny_values(form, T, H):
             check(form, x_bits, logits, low, k, y, torch.float32, what=f"tiny act {shift}")
 
 
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("T,H", [(4, 512), (16, 512), (12, 2304)])
+def test_few_a_token_that_is_not_finite_keeps_to_itself(form, T, H):
+    """NaN or infinities in one token's row: the other tokens' results are the same bits."""
+    I, E, k = 640, 6, 3
+    x_bits, logits, weights = make(form, T, H, I, E, k, seed=23)
+    say(f"few {form} T={T} H={H} with a NaN and an infinity in x")
+    x, lg, packed = bf16_to_dev(x_bits), to_dev(logits), prepack(form, weights)
+    want = CALL[form](x, lg, k, *packed)
+    assert torch.isfinite(want).all()
+    bad = x.clone()
+    bad[1, 7], bad[T - 1, :] = float("nan"), float("-inf")
+    got = CALL[form](bad, lg, k, *packed)
+    rest = [t for t in range(T) if t not in (1, T - 1)]
+    assert torch.equal(got[rest], want[rest])
+    if form != "channel":                                    # (an INT8 code has no value for them)
+        assert not torch.isfinite(got[[1, T - 1]]).any()
+
+
 def test_few_strided_rows_and_neighbours_untouched():
     form, T, H, I, E, k = "g128", 6, 512, 256, 10, 3
     x_bits, logits, weights = make(form, T, H, I, E, k, seed=31)

@@ -30,6 +30,8 @@ SHAPES = [
     (9, 33, 16512),                  # 129 groups
     (8, 6144, 2048), (4, 2049, 1024),
     (1, 8208, 640), (16, 8192, 384),
+    (16, 16400, 256),                # steps of 32 columns, the last of 16
+    (3, 8208, 6272),                 # .. and K in parts
 ]
 
 
@@ -103,6 +105,20 @@ def test_matvec_against_64_bits(form, T, N, K, rng):
         assert torch.equal(blk, y)                          # the same values in the same order
     for t in {0, T - 1}:                                    # a row's result does not depend on the others
         assert torch.equal(STORED[form](x[t:t + 1], wd, sd), y[t:t + 1])
+
+
+@pytest.mark.parametrize("form", FORMS)
+def test_matvec_a_row_that_is_not_finite_keeps_to_itself(form, rng):
+    T, N, K = 6, 48, 1152
+    x_bits, w, s = make(form, T, N, K, rng)
+    say(f"matvec {form} with NaN and infinities in x")
+    x, wd, sd = bf16_to_dev(x_bits), to_dev(w), to_dev(s)
+    want = STORED[form](x, wd, sd)
+    bad = x.clone()
+    bad[2, 5], bad[5, :] = float("nan"), float("inf")
+    got = STORED[form](bad, wd, sd)
+    assert torch.equal(got[[0, 1, 3, 4]], want[[0, 1, 3, 4]])
+    assert not torch.isfinite(got[[2, 5]]).any()
 
 
 @pytest.mark.parametrize("K", [32, 96, 160, 2912, 4064])
