@@ -21,6 +21,15 @@
 //     tiles meet in LDS and are summed in wave order: the same bits at every run.
 // The products run on the bf16 matrix cores (w4_bf16.hpp; INT8 form: the INT8 ones,
 // exact), so act and y carry fp32 rounding only.
+//
+// Measured (H 6144, I 2048, 256 experts, 8 picks; kernel times, weights and scales read):
+//             gate/up                  down
+//   1 token   24.5 us (107 MB, 4.4 TB/s)  16.0 us (54 MB, 3.3 TB/s)   group 128
+//   4 tokens  71 us (408 MB, 5.7 TB/s)    40 us (204 MB, 5.1 TB/s)    MXFP4
+//   16 tokens 227 us (1.36 GB, 6.0 TB/s)  130 us (0.68 GB, 5.2 TB/s)  group 128
+// against about 6.5 TB/s that a long read reaches.  With one token the start bounds both:
+// about 7 us of the first kernel (launch, logits and x, the picks at 0.2 us each, then the
+// first weights) and 5 us of the second, during which HBM has little to do.
 #include "kernels.hpp"
 #include "w4_bf16.hpp"
 
@@ -164,12 +173,13 @@ __device__ __forceinline__ void route_weights(const uint32_t* keys, const float*
 }
 
 // ---- what the first kernel leaves for the second ------------------------------
-// Views into the caller's workspace (16-byte aligned): the number of distinct
-// experts; of each, the expert (10 bits), the routed indices of its first two tokens (8 bits
-// each; one: the second counts nothing) and the set of its tokens; the routed index of (expert, token) or -1; the routing weights, act [R][I] and the maxima of |act| over its 16-column blocks [R][I/16]; then
-// what the second kernel's workgroups leave for each other: their sums of a column block
-// that they share, [workgroup][2][T][32], and a count of arrivals for each of the H/32
-// column blocks (set to zero by the first kernel).
+// Views into the caller's workspace (16-byte aligned): the number of distinct experts; of
+// each, the expert (10 bits), the routed indices of its first two tokens (8 bits each; one:
+// the second counts nothing) and the set of its tokens; the routed index of (expert, token)
+// or -1; the routing weights, act [R][I] and the maxima of |act| over its 16-column blocks
+// [R][I/16]; then what the second kernel's workgroups leave for each other: their sums of a
+// column block that they share, [workgroup][2][T][32], and a count of arrivals for each of
+// the H/32 column blocks (set to zero by the first kernel).
 struct FewWorkspace {
   int32_t* count;
   uint32_t* experts;      // [kFewMaxRows] expert | first routed index << 10 | second << 18
@@ -232,13 +242,13 @@ struct FewProduct {
 };
 
 // ---- kernel 1: routing, quantization, gate/up, SwiGLU -----------------------
-// A task is 16 columns of act for one distinct expert: 16 gate and 16 up rows of
-// w13, K split over the 8 waves.  The workgroups walk the tasks; a wave refills each
-// weight register with the next task's as it uses it up.  (Tasks of 32 columns, which use
-// an operand four times: 16 tokens 3 % faster at most, 1 token 24.6 -> 26.7 us, as the first
-// product waits for twice the weights and the last ends later.)
+// A task is 16 NC columns of act for one distinct expert: NC tiles of 16 gate rows of w13
+// and NC of up rows, K split over the 8 waves.  The workgroups walk the tasks; a wave
+// refills each weight register with the next task's as it uses it up.
+// NC = 2 uses an operand and its -8 products four times, and reads whole lines of scales,
+// but the first product waits for twice the weights and the last ends later.
 // GW: the most K groups of a wave (H <= 1024 GW).  S: logits per lane (E <= 64 S).
-template <int kForm, int GW, int S>
+template <int kForm, int GW, int S, int NC>
 __global__ __launch_bounds__(kFewThreads, 2) void few_gate_up_kernel(const uint16_t* __restrict__ x, int T, int64_t H,
                                                                   int64_t ld, const float* __restrict__ logits, int E,
                                                                   int k, int renormalize,
@@ -261,8 +271,8 @@ __global__ __launch_bounds__(kFewThreads, 2) void few_gate_up_kernel(const uint1
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 15, kq = lane >> 4;
   const int G = (int)(H >> 7), R = T * k;
-  uint8_t* codes = smem;                                          // [G][4][T][32]
-  float* red = reinterpret_cast<float*>(smem + (size_t)T * H);    // [2][waves][2][T][16]; int32 for INT8
+  uint8_t* codes = smem;                                          // [G][4][2][T][16]
+  float* red = reinterpret_cast<float*>(smem + (size_t)T * H);    // NC = 1: [2][waves][gate, up][T][16], NC = 2: [waves][gate, up][T][32]; int32 for INT8
 
   // The waves share the first 8 rows of x, wpr waves to a row, and wave v takes row v + 8.
   // A part of a row that is short enough stays in registers until the weights are on
@@ -300,7 +310,8 @@ __global__ __launch_bounds__(kFewThreads, 2) void few_gate_up_kernel(const uint1
     return m;
   };
   // the codes of chunk c of row t, in operand order: elements 8 c .. +7 are group c / 16, lane group
-  // (c / 4) % 4, bytes 8 (c % 4) .. +7 of its 32
+  // (c / 4) % 4, bytes 8 (c % 4) .. +7 of its 32, which are kept in two halves (16 lanes then read 256
+  // bytes side by side)
   auto times2 = [](uint32_t v, float by) {                        // both bf16 of a word times a power of two (exact)
     return (__float_as_uint(bf16_hi(v) * by) & 0xffff0000u) | __float_as_uint(bf16_lo(v) * by) >> 16;
   };
@@ -309,7 +320,7 @@ __global__ __launch_bounds__(kFewThreads, 2) void few_gate_up_kernel(const uint1
     uint2 o;
     o.x = codes4<kInt8>(bf16_lo(v.x), bf16_hi(v.x), bf16_lo(v.y), bf16_hi(v.y), d.s, d.r);
     o.y = codes4<kInt8>(bf16_lo(v.z), bf16_hi(v.z), bf16_lo(v.w), bf16_hi(v.w), d.s, d.r);
-    *reinterpret_cast<uint2*>(codes + ((size_t)(c >> 2) * T + t) * 32 + 8 * (c & 3)) = o;
+    *reinterpret_cast<uint2*>(codes + ((size_t)(c >> 1) * T + t) * 16 + 8 * (c & 1)) = o;
   };
   __syncthreads();                                                // picked and slot are set
   if (routes) pick_experts<S>(lg, E, k, ids + wave * k, keys + wave * k, picked);
@@ -378,31 +389,35 @@ __global__ __launch_bounds__(kFewThreads, 2) void few_gate_up_kernel(const uint1
   __syncthreads();
 
   const FewWorkspace ws = few_workspace(workspace, T, R, I);
-  const int blocks = (int)(I >> 4);                               // column blocks of act
+  constexpr int kCols = 16 * NC, NT = 2 * NC;                     // tiles: gate, then up
+  const int blocks = (int)(I / kCols);                            // column blocks of act
   const int ntasks = D * blocks;
   const int gpw = (G + kFewWaves - 1) / kFewWaves;                // <= GW
   const int g0 = wave * gpw, ng = max(0, min(gpw, G - g0));
   constexpr int SW = (GW + 3) / 4;                                // scale words: one for four groups
-  i32x4 wg[GW], wu[GW];
-  uint32_t sg[SW], su[SW];
-  __amdgpu_buffer_rsrc_t rg = buffer_of(w13, 0), ru = rg, rs = buffer_of(s13, 0);
+  i32x4 w[GW][NT];
+  uint32_t sc[SW][NT];
+  __amdgpu_buffer_rsrc_t rw[NT], rs;
   auto point = [&](int task) {                                    // the task's weights of this wave; none past the last task
     const bool on = task < ntasks && ng > 0;
     const int d = on ? task / blocks : 0, cb = on ? task - d * blocks : 0;
     const int64_t e = __builtin_amdgcn_readfirstlane(experts[d]);
-    const uint8_t* p = w13 + ((e * (I >> 3) + cb) * G + g0) * 1024;
-    rg = buffer_of(p, on ? ng * 1024 : 0);
-    ru = buffer_of(p + (I >> 4) * G * 1024, on ? ng * 1024 : 0);
-    if constexpr (!kInt8) rs = buffer_of(s13 + (((e * G + g0) * 2 * I) + 16 * cb) * 4, on ? ((int64_t)ng * 2 * I - 16 * cb) * 4 : 0);
+    const uint8_t* p = w13 + ((e * (I >> 3) + NC * cb) * G + g0) * 1024;
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+      rw[n] = buffer_of(p + (n % NC + n / NC * (I >> 4)) * G * 1024, on ? ng * 1024 : 0);
+    rs = buffer_of(s13 + (((e * G + g0) * 2 * I) + kCols * cb) * 4,
+                   !kInt8 && on ? ((int64_t)ng * 2 * I - kCols * cb) * 4 : 0);
   };
   auto load = [&](int i) {
-    wg[i] = buffer_load16_nt(rg, col * 64 + kq * 16 + i * 1024);
-    wu[i] = buffer_load16_nt(ru, col * 64 + kq * 16 + i * 1024);
+#pragma unroll
+    for (int n = 0; n < NT; ++n) w[i][n] = buffer_load16_nt(rw[n], col * 64 + kq * 16 + i * 1024);
   };
   auto load_scales = [&](int j) {                                 // of the groups 4 j .. 4 j + 3; before their weights
     if constexpr (!kInt8) {
-      sg[j] = buffer_load4(rs, (uint32_t)((4 * j + kq) * 2 * I + col) * 4);
-      su[j] = buffer_load4(rs, (uint32_t)((4 * j + kq) * 2 * I + I + col) * 4);
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+        sc[j][n] = buffer_load4(rs, (uint32_t)((4 * j + kq) * 2 * I + n / NC * I + 16 * (n % NC) + col) * 4);
     }
   };
   int task = xcd_order(), buf = 0;
@@ -419,7 +434,7 @@ __global__ __launch_bounds__(kFewThreads, 2) void few_gate_up_kernel(const uint1
     for (int i = 0; i < XC; ++i) m = amax8(m, xv[i]);
     m = wave_max(m);
     if (has_row && lane == 0) wave_amax[row][part] = m;           // (wave v's own row otherwise, below)
-    // (opaque: the fp32 values of the maxima are not kept for the codes, they would take twice the registers)
+      // (opaque: the fp32 values of the maxima are not kept for the codes, they would take twice the registers)
 #pragma unroll
     for (int i = 0; i < XC; ++i) asm volatile("" : "+v"(xv[i].x), "+v"(xv[i].y), "+v"(xv[i].z), "+v"(xv[i].w));
   }
@@ -460,70 +475,72 @@ __global__ __launch_bounds__(kFewThreads, 2) void few_gate_up_kernel(const uint1
   }
   __syncthreads();
 
-  const uint8_t* arow = codes + ((size_t)(4 * g0 + kq) * T + min(col, T - 1)) * 32;
+  const uint8_t* arow = codes + ((size_t)(8 * g0 + 2 * kq) * T + min(col, T - 1)) * 16;
   const size_t astep = (size_t)128 * T;
-  // this thread's token scale (threads below 16 T finish the tiles: token threadIdx.x / 16)
+  // this thread's token scale (threads below 16 NC T finish the tiles: token ft, column fc)
+  const int ft = threadIdx.x / kCols, fc = threadIdx.x % kCols;
   float sx = 1.0f;
-  if ((int)threadIdx.x < 16 * T) {
+  if (ft < T) {
     float amax = 0.0f;
-    for (int p = 0; p < wpr; ++p) amax = fmaxf(amax, wave_amax[threadIdx.x >> 4][p]);
+    for (int p = 0; p < wpr; ++p) amax = fmaxf(amax, wave_amax[ft][p]);
     sx = row_scale<kInt8>(amax);
   }
   for (; task < ntasks; task += gridDim.x, buf ^= 1) {
     point(task + (int)gridDim.x);
-    Acc ag = Acc{0, 0, 0, 0}, au = Acc{0, 0, 0, 0};
-    uint32_t g4[4], u4[4];
+    Acc acc[NT] = {};
+    uint32_t s4[NT][4];
 #pragma unroll
     for (int i = 0; i < GW; ++i) {
       if (!kInt8 && (i & 3) == 0) {
-        spread4(sg[i >> 2], g4);
-        spread4(su[i >> 2], u4);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) spread4(sc[i >> 2][n], s4[n]);
         load_scales(i >> 2);
       }
       if (i < ng) {
         P p;
-        p.set_codes(*reinterpret_cast<const v8i*>(arow + i * astep));
-        uint32_t fg = 0, fu = 0;
-        if constexpr (!kInt8) {
-          fg = kForm == kFormMx ? (g4[i & 3] >> (8 * kq)) & 0xffu : g4[i & 3];
-          fu = kForm == kFormMx ? (u4[i & 3] >> (8 * kq)) & 0xffu : u4[i & 3];
+        v8i a;
+        a.lo = *reinterpret_cast<const i32x4*>(arow + i * astep);
+        a.hi = *reinterpret_cast<const i32x4*>(arow + i * astep + 16 * T);
+        p.set_codes(a);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          uint32_t f = 0;
+          if constexpr (!kInt8) f = kForm == kFormMx ? (s4[n][i & 3] >> (8 * kq)) & 0xffu : s4[n][i & 3];
+          p.add(w[i][n], f, acc[n]);
         }
-        p.add(wg[i], fg, ag);
-        p.add(wu[i], fu, au);
       }
       load(i);
     }
-    // the partial tiles: red[buf][wave][gate, up][t][col]
-    float* rb = red + (size_t)buf * kFewWaves * 2 * T * 16;
+    // the partial tiles: one barrier per task where there are two buffers (the other's readers passed the last one)
+    const size_t step = (size_t)T * kCols;                        // gate to up, up to the next wave's gate
+    float* rb = red + (NC == 1 ? buf * kFewWaves * 2 * step : 0);
+    if constexpr (NC > 1) __syncthreads();
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const int t = 4 * kq + r;
       if (t < T) {
-        float* at = rb + ((size_t)wave * 2 * T + t) * 16 + col;
-        if constexpr (kInt8) {
-          at[0] = __int_as_float(ag[r]);
-          at[T * 16] = __int_as_float(au[r]);
-        } else {
-          at[0] = ag[r];
-          at[T * 16] = au[r];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          float* at = rb + (wave * 2 + n / NC) * step + t * kCols + 16 * (n % NC) + col;
+          if constexpr (kInt8) *at = __int_as_float(acc[n][r]);
+          else *at = acc[n][r];
         }
       }
     }
-    __syncthreads();       // one per task: the other buffer's readers passed the last one
-    if ((int)threadIdx.x < 16 * T) {
-      const int t = threadIdx.x >> 4, c = threadIdx.x & 15;
+    __syncthreads();
+    if (ft < T) {
       const int d = task / blocks, cb = task - d * blocks;
-      const int fr = slot[d][t];
+      const int fr = slot[d][ft];
       float gate, up;
-      const float* at = rb + (size_t)t * 16 + c;
+      const float* at = rb + (size_t)ft * kCols + fc;
       if constexpr (kInt8) {
         int ig = 0, iu = 0;
 #pragma unroll
         for (int v = 0; v < kFewWaves; ++v) {
-          ig += __float_as_int(at[(size_t)v * 2 * T * 16]);
-          iu += __float_as_int(at[(size_t)(v * 2 + 1) * T * 16]);
+          ig += __float_as_int(at[2 * v * step]);
+          iu += __float_as_int(at[(2 * v + 1) * step]);
         }
-        const float* sw = reinterpret_cast<const float*>(s13) + (int64_t)experts[d] * 2 * I + 16 * cb + c;
+        const float* sw = reinterpret_cast<const float*>(s13) + (int64_t)experts[d] * 2 * I + kCols * cb + fc;
         gate = (float)ig * sx * sw[0];
         up = (float)iu * sx * sw[I];
       } else {
@@ -531,8 +548,8 @@ __global__ __launch_bounds__(kFewThreads, 2) void few_gate_up_kernel(const uint1
         up = 0.0f;
 #pragma unroll
         for (int v = 0; v < kFewWaves; ++v) {
-          gate += at[(size_t)v * 2 * T * 16];
-          up += at[(size_t)(v * 2 + 1) * T * 16];
+          gate += at[2 * v * step];
+          up += at[(2 * v + 1) * step];
         }
         gate *= sx;
         up *= sx;
@@ -540,8 +557,8 @@ __global__ __launch_bounds__(kFewThreads, 2) void few_gate_up_kernel(const uint1
       const float a = silu_mul(gate, up);
       const float m = max16(fabsf(a));
       if (fr >= 0) {
-        ws.act[(int64_t)fr * I + 16 * cb + c] = a;
-        if (c == 0) ws.pmax[(int64_t)fr * blocks + cb] = m;
+        ws.act[(int64_t)fr * I + kCols * cb + fc] = a;
+        if ((fc & 15) == 0) ws.pmax[(int64_t)fr * NC * blocks + NC * cb + (fc >> 4)] = m;
       }
     }
   }
@@ -566,8 +583,10 @@ __global__ __launch_bounds__(kFewThreads, 2) void few_gate_up_kernel(const uint1
 // token and piece.
 //
 // NB = 2: codes, their operands and the -8 products serve two tiles, and the scales of a
-// group are a whole line of memory.  One workgroup of 8 waves on a CU, with the registers
-// for it, reads no slower than two with half of them.
+// group are a whole line of memory (NB = 1 at H 6144: 17.1 against 16.0 us for 1 token).
+// Whole blocks of 32 columns fill too few CUs where there are few of them: NB = 1 (H 2048, I
+// 768, 8 MXFP4 experts: 128 blocks of 16 7.5 us, 64 of 32 8.5 us).  One workgroup of 8 waves
+// on a CU, with the registers for it, reads no slower than two with half of them.
 __device__ __forceinline__ void store_y(void* y, int y_bf16, int64_t at, float v) {
   if (y_bf16) static_cast<uint16_t*>(y)[at] = __builtin_bit_cast(uint16_t, (__bf16)v);
   else static_cast<float*>(y)[at] = v;
@@ -577,7 +596,9 @@ struct FewDownShape {
   static constexpr int kCols = 16 * NB;
   static constexpr int kGroups = 8 / NB;
 };
-// pieces of a workgroup: total in all, M of a block.  A shared block costs about a round.
+// Pieces of a workgroup: total in all, M of a block.  A shared block costs about a round, so
+// whole blocks where equal ranges save no more: 192 blocks of 32 pieces 16.0 against 16.6 us,
+// 64 of 16 8.5 against 8.6; 64 of 28 to 32 (4 rounds or 1) 11.9 against 10.0.
 __host__ __device__ inline int few_down_range(int total, int M) {
   const int per = (total + kFewDownMaxGrid * kFewWaves - 1) / (kFewDownMaxGrid * kFewWaves) * kFewWaves;
   return M <= per + kFewWaves ? M : per;
@@ -964,7 +985,7 @@ __global__ __launch_bounds__(kFewThreads, 2) void few_down_kernel(int T, int64_t
 }
 
 // ---- launches ------------------------------------------------------------------
-// Whole blocks of 32 columns fill too few CUs below this many: then blocks of 16.
+// Fewer whole blocks of 32 columns than this: blocks of 16 (see FewDownShape).
 constexpr int64_t kFewMinBlocks = 128;
 
 template <int kForm, int NB>
@@ -981,15 +1002,26 @@ static void launch_few_down(const FewArgs& a, unsigned grid, hipStream_t stream)
 // experts) 28.5 against 32.4, 16 tokens 243 against 259; 4 tokens MXFP4 71.3 against 69.9.
 constexpr int64_t kFewGrid = 256;
 
+// From this many tokens on, tasks of 32 columns.  Gate/up, 32 against 16: 16 tokens (H 6144, I 2048, group
+// 128) 227 against 246 us, 12 tokens 185 against 199, 12 tokens MXFP4 177 against 179, 16 tokens (H 4096,
+// I 1024, 64 experts) 46.5 against 44.8; 8 tokens 132 against 136, (H 4096, I 1024) 32.0 against 29.4; 1 token 26.7
+// against 24.6.
+constexpr int64_t kFewWideTokens = 9;
+
+template <int kForm, int GW, int S, int NC>
+static void launch_few_gate_up(const FewArgs& a, hipStream_t stream) {
+  const int64_t R = a.T * a.k, tasks = (R < a.E ? R : a.E) * (a.I / (16 * NC));   // at most
+  hipLaunchKernelGGL((few_gate_up_kernel<kForm, GW, S, NC>), dim3((unsigned)(tasks < kFewGrid ? tasks : kFewGrid)),
+                     dim3(kFewThreads), (size_t)few_gate_up_smem(a.T, a.H), stream, a.x, (int)a.T, a.H, a.ld, a.logits,
+                     a.E, a.k, a.renormalize, static_cast<const uint8_t*>(a.w13), static_cast<const uint8_t*>(a.s13),
+                     a.I, a.ids, a.w, a.workspace);
+}
+
 template <int kForm, int GW, int S>
 static hipError_t launch_few_form(const FewArgs& a, hipStream_t stream) {
   const int64_t R = a.T * a.k;
-  const int64_t tasks = (R < a.E ? R : a.E) * (a.I >> 4);                // at most
-  const size_t smem = (size_t)few_gate_up_smem(a.T, a.H);
-  const unsigned grid = (unsigned)(tasks < kFewGrid ? tasks : kFewGrid);
-  hipLaunchKernelGGL((few_gate_up_kernel<kForm, GW, S>), dim3(grid), dim3(kFewThreads), smem, stream, a.x, (int)a.T, a.H,
-                     a.ld, a.logits, a.E, a.k, a.renormalize, static_cast<const uint8_t*>(a.w13),
-                     static_cast<const uint8_t*>(a.s13), a.I, a.ids, a.w, a.workspace);
+  if (a.T < kFewWideTokens) launch_few_gate_up<kForm, GW, S, 1>(a, stream);
+  else launch_few_gate_up<kForm, GW, S, 2>(a, stream);
   if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
   // at most M pieces of each of `cols` blocks of 32 columns
   const int64_t groups = FewDownShape<2>::kGroups, nch = (a.I / kGroup + groups - 1) / groups;

@@ -116,7 +116,7 @@ constexpr int64_t kFewHeadBytes = 16 + 12 * kFewMaxRows + 2 * kFewMaxRows * kFew
 constexpr int64_t few_workspace_bytes(int64_t T, int64_t k, int64_t I) {
   return kFewHeadBytes + 4 * (T * k * (I + I / 16) + kFewDownMaxGrid * 2 * T * 32 + kFewMaxH / 32);
 }
-// dynamic LDS of the first kernel: the codes, then two buffers of partial tiles
+// dynamic LDS of the first kernel: the codes, then the waves' partial tiles
 constexpr int64_t few_gate_up_smem(int64_t T, int64_t H) { return T * H + 2048 * T; }
 constexpr int64_t kFewMaxI = 65536;      // byte offsets of an expert's scales stay below 2^31
 struct FewArgs {

@@ -10,6 +10,12 @@
 // in flight while the one before is multiplied and summed.  The eight partial 16x16
 // tiles meet in LDS and are summed in wave order (fp32; the same bits at every run).
 // Rows of A past T repeat row T - 1; their products are never stored.
+//
+// Measured (group 128, GEMM storage; kernel times): 1 x 131072 x 6144 67 us (428 MB, 6.4
+// TB/s), 16 x 65536 x 6144 40.5 us (5.3 TB/s), 1 x 12288 x 6144 11.8 us (40 MB, 3.4 TB/s),
+// 1 x 4096 x 6144 7.1 us, 1 x 2048 x 2048 4.1 us: up to some 20 MB the start bounds it (the
+// launch, one trip to memory for the weights, the exchange in LDS).  A call from the host
+// takes about 8 us, so the smallest are bound by that.
 #include "kernels.hpp"
 #include "w4_bf16.hpp"
 
@@ -17,6 +23,7 @@ namespace w4a8 {
 
 constexpr int kMvWaves = 8;
 constexpr int kMvThreads = 64 * kMvWaves;
+constexpr int kMvPitch = 272;                // bytes of a row of activations on its way to operand order
 
 // kParts: K is longer than the 8 GW groups held at once; a step then goes over parts of
 // K and fetches each part's activations again (a path of its own: their loads would
@@ -30,7 +37,7 @@ __global__ __launch_bounds__(kMvThreads) void matvec_kernel(const uint16_t* __re
   __shared__ float red[2][kMvWaves][NS][16][16];
   // The wave's activations of one group on their way to operand order, T rows of 256 bytes.  A row is 16 bytes
   // longer so that the 16 rows an operand read covers start in different banks.
-  constexpr int kPitch = 272;
+  constexpr int kPitch = kMvPitch;
   extern __shared__ __attribute__((aligned(16))) unsigned char a_sm[];   // [waves][T][kPitch]
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -201,16 +208,21 @@ __global__ __launch_bounds__(kMvThreads) void matvec_kernel(const uint16_t* __re
   }
 }
 
-constexpr int64_t kMvGrid = 256;             // one workgroup on each CU
+// One workgroup on each CU: 256 against 512 at 16 x 12288 x 6144 13.7 against 20.1 us, 1 x
+// 131072 x 6144 67.5 against 69.9; the same where K is 2048.
+constexpr int64_t kMvGrid = 256;
 
 template <int kForm, bool kRM, int GW, bool kParts = false>
 static void launch_matvec_steps(const MatvecArgs& a, hipStream_t stream) {
   auto go = [&](auto kernel, int ns) {
-    const int64_t steps = (a.N + 16 * ns - 1) / (16 * ns), wgs = kMvGrid;
-    hipLaunchKernelGGL(kernel, dim3((unsigned)(steps < wgs ? steps : wgs)), dim3(kMvThreads),
-                       (size_t)(kMvWaves * a.T * 272), stream, a.x, (int)a.T, a.K, a.ld, static_cast<const uint8_t*>(a.w), static_cast<const uint8_t*>(a.s), a.N,
-                       a.y, a.y_bf16);
+    const int64_t steps = (a.N + 16 * ns - 1) / (16 * ns);
+    hipLaunchKernelGGL(kernel, dim3((unsigned)(steps < kMvGrid ? steps : kMvGrid)), dim3(kMvThreads),
+                       (size_t)(kMvWaves * a.T * kMvPitch), stream, a.x, (int)a.T, a.K, a.ld,
+                       static_cast<const uint8_t*>(a.w), static_cast<const uint8_t*>(a.s), a.N, a.y, a.y_bf16);
   };
+  // Steps of 32 outputs (whole lines of scales, half the exchanges) from two steps of them per workgroup on: K
+  // 4096, N 32768 15.1 against 16.3 us, N 4096 7.0 against 6.3.  With K in parts from one on, as each step fetches
+  // the activations again: 8192 x 16384 21.6 against 26.7 us.
   if (a.N >= (kParts ? 32 : 64) * kMvGrid) go(matvec_kernel<kForm, kRM, GW, 2, kParts>, 2);
   else go(matvec_kernel<kForm, kRM, GW, 1, kParts>, 1);
 }
