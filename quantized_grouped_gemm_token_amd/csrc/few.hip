@@ -1002,7 +1002,8 @@ static void launch_few_down(const FewArgs& a, unsigned grid, hipStream_t stream)
 // experts) 28.5 against 32.4, 16 tokens 243 against 259; 4 tokens MXFP4 71.3 against 69.9.
 constexpr int64_t kFewGrid = 256;
 
-// From this many tokens on, tasks of 32 columns.  Gate/up, 32 against 16: 16 tokens (H 6144, I 2048, group
+// From this many tokens on, tasks of 32 columns where every workgroup has one (16 tokens, 8 experts of I 128:
+// 32 tasks 10.1 us, 64 of 16 columns 9.9).  Gate/up, 32 against 16: 16 tokens (H 6144, I 2048, group
 // 128) 227 against 246 us, 12 tokens 185 against 199, 12 tokens MXFP4 177 against 179, 16 tokens (H 4096,
 // I 1024, 64 experts) 46.5 against 44.8; 8 tokens 132 against 136, (H 4096, I 1024) 32.0 against 29.4; 1 token 26.7
 // against 24.6.
@@ -1020,7 +1021,8 @@ static void launch_few_gate_up(const FewArgs& a, hipStream_t stream) {
 template <int kForm, int GW, int S>
 static hipError_t launch_few_form(const FewArgs& a, hipStream_t stream) {
   const int64_t R = a.T * a.k;
-  if (a.T < kFewWideTokens) launch_few_gate_up<kForm, GW, S, 1>(a, stream);
+  const bool wide = a.T >= kFewWideTokens && (R < a.E ? R : a.E) * (a.I >> 5) >= kFewGrid;
+  if (!wide) launch_few_gate_up<kForm, GW, S, 1>(a, stream);
   else launch_few_gate_up<kForm, GW, S, 2>(a, stream);
   if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
   // at most M pieces of each of `cols` blocks of 32 columns

@@ -33,6 +33,9 @@ SHAPES = [
     (7, 896, 128, 1, 1),             # one expert
     (16, 512, 256, 300, 16),         # the most routed rows (256), more than 256 experts
     (1, 128, 128, 1024, 64),         # one group each, the most experts
+    (10, 4352, 512, 24, 3),          # gate/up tasks of 32 columns, rows of up to 6144
+    (9, 6400, 512, 24, 3),           # .. and of more
+    (2, 256, 128, 300, 128),         # more picks than a wave has lanes
     (14, 8192, 128, 8, 2),           # the longest rows, the most codes in LDS
     (3, 8192, 128, 64, 8),           # the most column blocks, 17 to 24 pieces in each
     (2, 8192, 640, 16, 8),           # .. and a range of pieces that is nearly a block
