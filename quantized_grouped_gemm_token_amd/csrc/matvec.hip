@@ -15,7 +15,7 @@
 // TB/s), 16 x 65536 x 6144 40.5 us (5.3 TB/s), 1 x 12288 x 6144 11.8 us (40 MB, 3.4 TB/s),
 // 1 x 4096 x 6144 7.1 us, 1 x 2048 x 2048 4.1 us: up to some 20 MB the start bounds it (the
 // launch, one trip to memory for the weights, the exchange in LDS).  A call from the host
-// takes about 8 us, so the smallest are bound by that.
+// takes about 7 us, so the smallest are bound by that.
 #include "kernels.hpp"
 #include "w4_bf16.hpp"
 

@@ -948,13 +948,14 @@ def _ld(x: torch.Tensor, T: int, K: int) -> int:
     return x.stride(0) if T > 1 else K
 
 
-def _y(y, y_dtype, T: int, N: int, dev):
+def _y(y, y_dtype, T: int, N: int, x: torch.Tensor, dev):
+    """y or a new one next to x (bf16, like y_dtype as a rule: the cheapest allocation), and its type's code."""
     if y is None:
         if y_dtype is _BF16:
-            return torch.empty((T, N), dtype=_BF16, device=dev), W4A8_Y_BF16
+            return x.new_empty((T, N)), W4A8_Y_BF16
         if y_dtype is not _F32:
             raise TypeError("y must be float32 or bfloat16")
-        return torch.empty((T, N), dtype=_F32, device=dev), W4A8_Y_F32
+        return x.new_empty((T, N), dtype=_F32), W4A8_Y_F32
     if not isinstance(y, torch.Tensor) or y.dtype not in (_F32, _BF16):
         raise TypeError("y must be a float32 or bfloat16 tensor")
     _is(y, "y", y.dtype, (T, N), dev)
@@ -963,6 +964,7 @@ def _y(y, y_dtype, T: int, N: int, dev):
 
 _functions: dict = {}
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)   # (dev is a GPU: it is initialised)
 
 
 def _call_on(dev: torch.device, name: str, *args) -> None:
@@ -971,7 +973,7 @@ def _call_on(dev: torch.device, name: str, *args) -> None:
     if f is None:
         f = _functions[name] = getattr(lib(), name)
     i = dev.index
-    if i == torch.cuda.current_device():
+    if i == _current_device():
         status = f(*args, _raw_stream(i) if _raw_stream else _stream(dev))
     else:
         with torch.cuda.device(dev):
@@ -1022,7 +1024,7 @@ def _few(form, x, logits, k, w13, s13, w2, s2, renormalize, y, y_dtype, ids, w, 
     else:
         _is(s13, "s13", _U8, (E, G13, 2 * I, 4), dev)
         _is(s2, "s2", _U8, (E, G2, H, 4), dev)
-    y, code = _y(y, y_dtype, T, H, dev)
+    y, code = _y(y, y_dtype, T, H, x, dev)
     if ids is not None:
         _is(ids, "ids", _I32, (T, k), dev)
     if w is not None:
@@ -1091,7 +1093,7 @@ def _matvec(name, form, prepacked, x, w, s, y, y_dtype):
         _is(w, "w", _U8 if mx else _I32, (N, K // 2 if mx else K // 8), dev)
         want = (N,) if form == "channel" else (N, K // 32) if mx else (N, K // 128)
     _is(s, "s", _U8 if mx else _F32, want, dev)
-    y, code = _y(y, y_dtype, T, N, dev)
+    y, code = _y(y, y_dtype, T, N, x, dev)
     _call_on(dev, name, x.data_ptr(), T, K, _ld(x, T, K), w.data_ptr(), s.data_ptr(), N, y.data_ptr(), code)
     return y
 
