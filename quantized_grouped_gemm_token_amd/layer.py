@@ -102,7 +102,7 @@ class W4A8MoE:
 
     def uses_few(self, T: int) -> bool:
         """Whether a forward over T tokens is the one call for a few tokens."""
-        return self.few and T > 0 and ops.w4a8_moe_few_fits(T, self.H, self.k)
+        return self.few and T > 0 and self.I <= ops.FEW_MAX_I and ops.w4a8_moe_few_fits(T, self.H, self.k)
 
     def _forward_few(self, x, logits, y, y_dtype, events):
         # the call allocates its workspace: forwards on several streams, or captured

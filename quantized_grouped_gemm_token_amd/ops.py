@@ -913,6 +913,7 @@ def w4a8_moe_grouped_gemm_swiglu_mxfp4_prepacked(a: torch.Tensor, a_scale: torch
 
 # ------------------------------------------------- a few tokens: the whole layer, and matrix-vector products
 FEW_MAX_TOKENS = 16
+FEW_MAX_I = 65536
 
 
 # These calls are short (a matrix-vector product runs in a few microseconds), so the

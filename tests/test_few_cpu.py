@@ -71,6 +71,17 @@ def test_few_workspace_bytes(L):
             ops.w4a8_moe_few_workspace_bytes(*bad)
 
 
+def test_few_layers_of_larger_experts_take_the_steps():
+    from quantized_grouped_gemm_token_amd.layer import W4A8MoE
+    moe = W4A8MoE.__new__(W4A8MoE)
+    moe.few, moe.H, moe.k, moe.I = True, 128, 1, ops.FEW_MAX_I
+    assert moe.uses_few(1) and not moe.uses_few(17)
+    moe.I += 128
+    assert not moe.uses_few(1)
+    with pytest.raises(ValueError):
+        ops.w4a8_moe_few_workspace_bytes(1, 1, moe.I)
+
+
 def test_few_fits_is_the_rule(L):
     for T, H, k in [(1, 8192, 8), (14, 8192, 8), (15, 8192, 8), (16, 7168, 8), (16, 7296, 8), (17, 128, 1),
                     (16, 128, 16), (16, 128, 17), (1, 8320, 1), (1, 128, 256), (1, 128, 257)]:

@@ -35,6 +35,8 @@ SHAPES = [
     (1, 128, 128, 1024, 64),         # one group each, the most experts
     (10, 4352, 512, 24, 3),          # gate/up tasks of 32 columns, rows of up to 6144
     (9, 6400, 512, 24, 3),           # .. and of more
+    (1, 128, 65536, 2, 1),           # the longest act rows
+    (5, 256, 4224, 3, 2),            # .. and ones whose maxima take more than one pass
     (2, 256, 128, 300, 128),         # more picks than a wave has lanes
     (14, 8192, 128, 8, 2),           # the longest rows, the most codes in LDS
     (3, 8192, 128, 64, 8),           # the most column blocks, 17 to 24 pieces in each
@@ -370,6 +372,44 @@ def test_few_graph_replays_follow_the_inputs(form):
         other = CALL[form](*sets[(i + 1) % 3], k, *packed)   # eager work between replays
         torch.cuda.synchronize()
         assert torch.equal(other, want[(i + 1) % 3])
+
+
+def test_few_two_graphs_replayed_in_turn_and_at_once():
+    """Two captured layers with matrix-vector products behind them, each with workspaces of its own."""
+    T, H, I, E, k = 6, 512, 384, 24, 3
+    x_bits, logits, weights = make("mxfp4", T, H, I, E, k, seed=71)
+    packed = prepack("mxfp4", weights)
+    x, lg = [bf16_to_dev(x_bits) * f for f in (1, 3)], [to_dev(logits), -to_dev(logits)]
+    w = torch.randint(0, 256, (300, H // 2), dtype=torch.uint8, device="cuda:0")
+    s = torch.randint(118, 124, (300, H // 32), dtype=torch.uint8, device="cuda:0")
+
+    def step(i):
+        h = ops.w4a8_moe_few_mxfp4_prepacked(x[i], lg[i], k, *packed, y_dtype=torch.bfloat16)
+        return h, ops.w4a8_moe_matvec_mxfp4(h, w, s)
+
+    say("few: two graphs")
+    want = [step(i) for i in range(2)]
+    torch.cuda.synchronize()
+    graphs, got = [], []
+    for i in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            got.append(step(i))
+        graphs.append(g)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for at_once in (False, True, False, True):
+        for h, y in got:
+            h.zero_()
+            y.zero_()
+        torch.cuda.synchronize()
+        for _ in range(5):
+            for i in range(2):
+                with torch.cuda.stream(streams[i if at_once else 0]):
+                    graphs[i].replay()
+        torch.cuda.synchronize()
+        for i in range(2):
+            assert all(torch.equal(a, b) for a, b in zip(got[i], want[i]))
+        assert all(torch.equal(a, b) for i in range(2) for a, b in zip(step(i), want[i]))   # eager work between
 
 
 def test_few_on_two_streams_at_once():
