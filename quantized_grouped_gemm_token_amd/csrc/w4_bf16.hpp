@@ -84,7 +84,9 @@ __device__ __forceinline__ void wave_lds_fence() {
 // size reads as zero without touching memory, so a load of nothing (a wave's missing
 // group, the step after the last) is the same instruction as any other, and a loop
 // that refills registers as it uses them up needs no branch around its loads.  (With
-// a branch, the compiler waits for each load at the branch's end.)
+// a branch, the compiler waits for each load at the branch's end.)  Weights are read
+// once: without the hint (nt) the output head takes 75 instead of 67.5 us, gate/up of 16
+// tokens 251 instead of 228; on scales, whose lines two blocks share, it only costs.
 constexpr uint32_t kNowhere = 0x80000000u;                     // past every resource
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void* base, int64_t bytes) {
   const int n = (int)(bytes < 0 ? 0 : bytes < 0x7fffffff ? bytes : 0x7fffffff);
