@@ -52,7 +52,8 @@
  *     library holds per GPU.
  *   - Data preconditions that are NOT checked (undefined if violated):
  *     expert ids in [0, E); offsets monotone with offsets[E] == M_total;
- *     gather rows in range; no NaN/Inf in activations, logits or scales.
+ *     gather rows in range; no NaN/Inf in activations, logits or scales where a
+ *     call does not say what it makes of them.
  *   - Every result is deterministic: the same inputs give bit-identical
  *     outputs from run to run.
  */
@@ -581,7 +582,7 @@ int w4a8_moe_grouped_gemm_swiglu_mxfp4_prepacked(const uint8_t* a, const float* 
  * calls above spend five launches and as many trips through memory on a step that
  * reads little more than the touched experts' weights.  (One decode step of the
  * layer: "GLM-5.3-W4A8" card, sections 量化方式 and 性能.)
- *   ids, w as w4a8_moe_route (the same bits); qx, sx by the rule of
+ *   ids, w as w4a8_moe_route (the same bits, masks apart: below); qx, sx by the rule of
  *   w4a8_moe_quant_act (_i8 form: w4a8_moe_quant_act_i8); for every f = t*k + j:
  *   act[f, :] = silu(gate) * up of expert ids[f], sa[f] and the codes qa[f, :] by the
  *   rule of w4a8_moe_requant (_i8); y[t, :] = sum_j w[t, j] * sa[f] * (qa[f, :] x w2).
@@ -602,8 +603,14 @@ int w4a8_moe_grouped_gemm_swiglu_mxfp4_prepacked(const uint8_t* a, const float* 
  *   Rules     : 0 <= T <= 16, 1 <= k <= E <= 1024, T*k <= 256, H > 0, H % 128 == 0,
  *               H <= 8192, T*H <= 114688, 0 < I <= 65536, I % 128 == 0.  Larger batches
  *               take the seven calls.
- *   Logits of -infinity rank last and get weight zero.  Whatever the logits hold,
- *   every id written is in [0, E) and no memory outside the arrays is touched.
+ *   A logit of -infinity or NaN masks its expert for that token: it ranks last (NaN
+ *   below -infinity, equal ones by the lower expert), gets weight zero and is not
+ *   routed, so what the expert holds does not reach y; a token with nothing but masks
+ *   has a row of y that is zero.  (w4a8_moe_route writes ids outside [0, E) for such
+ *   picks, which the calls after it skip: the same y.  Without renormalize a NaN
+ *   leaves the sum over all logits, and with it the row, without meaning.)  Whatever
+ *   the logits hold, every id written here is in [0, E) and no memory outside the
+ *   arrays is touched.
  *   x is finite: a token with a NaN or an infinity has a row of y without meaning
  *   (NaN in the FP8 forms); the other tokens' rows are what they are without it.
  *   The same inputs give the same bits at every call.

@@ -89,12 +89,16 @@ __device__ __forceinline__ RowDivisor row_divisor(float scale) {
 __device__ __forceinline__ bool rescaled(float by) { return __builtin_amdgcn_readfirstlane(__float_as_int(by)) != 0x3f800000; }
 
 // ---- routing of one token by one wave ---------------------------------------
-// fp32 -> uint32 with the order of the values (-0 as +0); 0 is below every value
+// fp32 -> uint32 with the order of the values (-0 as +0); NaN is below -infinity, 0 below both
 __device__ __forceinline__ uint32_t order_key(float v) {
   const uint32_t b = __float_as_uint(v + 0.0f);
   const uint32_t k = (b & 0x80000000u) ? ~b : b | 0x80000000u;
-  return k > 1u ? k : 1u;
+  return v == v ? k : 1u;
 }
+// The key of -infinity.  An expert whose key is not above it is masked: it can be picked (where fewer
+// than k are not masked), with weight 0, and is not routed, as in the separate steps, so nothing of
+// it reaches y.
+constexpr uint32_t kMaskedKey = 0x007fffffu;
 __device__ __forceinline__ float key_value(uint32_t k) {
   return __uint_as_float((k & 0x80000000u) ? k & 0x7fffffffu : ~k);
 }
@@ -114,7 +118,7 @@ constexpr int kRouteSlots = 16;                // 1024 experts
 // The k experts of a logits row in descending order, equal logits by the lower expert
 // (the order of w4a8_moe_route): slot s of lane l is expert l + 64 s, v its logit.  Every
 // id written is in [0, E), whatever the logits hold.  keys: the picks' order keys;
-// picked: a bit for each expert.  A round is one DPP maximum of the wave, then the
+// picked: a bit for each expert that is routed to.  A round is one DPP maximum of the wave, then the
 // lowest slot and lane that hold it; picks stay in registers (lane j holds pick j) and
 // reach LDS 64 at a time.
 template <int S>
@@ -147,34 +151,34 @@ __device__ __forceinline__ void pick_experts(const float (&v)[kRouteSlots], int 
     if (lane < n) {
       ids[j0 + lane] = my_id;
       keys[j0 + lane] = my_key;
-      atomicOr(&picked[my_id >> 5], 1u << (my_id & 31));
+      if (my_key > kMaskedKey) atomicOr(&picked[my_id >> 5], 1u << (my_id & 31));
     }
   }
 }
 
 // The routing weights of one row from its picks' logits, by one wave, with the sums of
-// w4a8_moe_route (the same bits).  lr: the logits row.
+// w4a8_moe_route (the same bits); 0 for a masked expert.  lr: the logits row.
 __device__ __forceinline__ void route_weights(const uint32_t* keys, const float* __restrict__ lr, int E, int k,
                                               int renormalize, float* __restrict__ w, float* __restrict__ w_out) {
   const int lane = threadIdx.x & 63;
   const float m = key_value(keys[0]);
   float denom = 0.0f;
   if (renormalize) {
-    for (int j = lane; j < k; j += kWave) denom += expf(key_value(keys[j]) - m);
+    for (int j = lane; j < k; j += kWave) denom += keys[j] > kMaskedKey ? expf(key_value(keys[j]) - m) : 0.0f;
   } else {
     for (int e = lane; e < E; e += kWave) denom += expf(lr[e] - m);
   }
   denom = wave_sum(denom);
   for (int j = lane; j < k; j += kWave) {
-    const float p = expf(key_value(keys[j]) - m) / denom;
+    const float p = keys[j] > kMaskedKey ? expf(key_value(keys[j]) - m) / denom : 0.0f;
     w[j] = p;
     if (w_out) w_out[j] = p;
   }
 }
 
 // ---- what the first kernel leaves for the second ------------------------------
-// Views into the caller's workspace (16-byte aligned): the number of distinct experts; of
-// each, the expert (10 bits), the routed indices of its first two tokens (8 bits each; one:
+// Views into the caller's workspace (16-byte aligned): the number of distinct experts (0: every
+// logit is masked); of each, the expert (10 bits), the routed indices of its first two tokens (8 bits each; one:
 // the second counts nothing) and the set of its tokens; the routed index of (expert, token)
 // or -1; the routing weights, act [R][I] and the maxima of |act| over its 16-column blocks
 // [R][I/16]; then what the second kernel's workgroups leave for each other: their sums of a
@@ -381,7 +385,7 @@ __global__ __launch_bounds__(kFewThreads, 2) void few_gate_up_kernel(const uint1
     const int e = f < R ? ids[f] : 0;
     const uint32_t we = (uint32_t)__shfl((int)word, e >> 5, kWave);
     const int number = __shfl(below, e >> 5, kWave) + __builtin_popcount(we & ((1u << (e & 31)) - 1u));
-    if (f < R) {
+    if (f < R && keys[f] > kMaskedKey) {
       slot[number][f / k] = (int16_t)f;
       experts[number] = e;                                        // the same value from every token that picked it
     }
@@ -661,6 +665,11 @@ __global__ __launch_bounds__(kFewThreads, 2) void few_down_kernel(int T, int64_t
   // the workgroup's pieces: lo .. hi - 1 of block * M + (expert number * nch + chunk); those below
   // `second` are of block c0, the others of c0 + 1 (a range is at most M long)
   const int D = __builtin_amdgcn_readfirstlane(*ws.count);
+  if (D == 0) {                                                          // nothing is routed: y is zero
+    for (int i = (int)(blockIdx.x * kFewThreads + threadIdx.x); i < T * (int)H; i += (int)gridDim.x * kFewThreads)
+      store_y(y, y_bf16, i, 0.0f);
+    return;
+  }
   const int M = D * nch, total = cols * M;
   const int per = NB == 1 ? M : few_down_range(total, M);                // pieces of a workgroup
   const int lo = (NB == 1 ? xcd_order() : (int)blockIdx.x) * per, hi = min(lo + per, total);

@@ -1052,7 +1052,8 @@ def w4a8_moe_few_prepacked(x: torch.Tensor, logits: torch.Tensor, k: int, w13: t
     router logits fp32 [T, E], experts in the GEMM storage (w13 int32 [E, 2I/16, H/128, 16, 16], s13 fp32
     [E, H/128, 2I], w2 int32 [E, H/16, I/128, 16, 16], s2 fp32 [E, I/128, H]) -> y [T, H] (fp32 or bf16).
 
-    ids int32 [T, k] and w fp32 [T, k], if given, receive the routing.  workspace: uint8
+    ids int32 [T, k] and w fp32 [T, k], if given, receive the routing.  A logit of -infinity or NaN masks its
+    expert: weight 0 and not routed; a token with nothing but masks has a row of y that is zero.  workspace: uint8
     [w4a8_moe_few_workspace_bytes(T, k, I)], allocated here if not given."""
     return _few("g128", x, logits, k, w13, s13, w2, s2, renormalize, y, y_dtype, ids, w, workspace)
 
