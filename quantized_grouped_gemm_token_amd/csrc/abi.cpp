@@ -12,14 +12,6 @@
 
 #include "kernels.hpp"
 
-// The newest launchers are weak references here, so that a host-only build of this
-// file (its argument checks without the kernels) also links and loads; the device
-// check keeps such a build from reaching them.
-namespace w4a8 {
-hipError_t launch_few(const FewArgs& f, hipStream_t stream) __attribute__((weak));
-hipError_t launch_matvec(const MatvecArgs& a, hipStream_t stream) __attribute__((weak));
-}  // namespace w4a8
-
 namespace {
 
 thread_local std::string g_last_error;

@@ -59,6 +59,8 @@ hipError_t launch_requant_i8(const float*, const float*, int64_t, int64_t, int8_
   return absent();
 }
 hipError_t launch_front(const FrontArgs&, bool, hipStream_t) { return absent(); }
+hipError_t launch_few(const FewArgs&, hipStream_t) { return absent(); }
+hipError_t launch_matvec(const MatvecArgs&, hipStream_t) { return absent(); }
 hipError_t launch_unpermute(const float*, const int32_t*, const float*, int64_t, int, int64_t, void*, int,
                             hipStream_t) {
   return absent();

@@ -71,3 +71,21 @@ def test_abi_checks_under_sanitizers(sanitized_lib):
     tail = (r.stdout + r.stderr)[-3000:]
     assert r.returncode == 0, tail
     assert "AddressSanitizer" not in tail and "runtime error" not in tail, tail
+
+
+def test_few_and_matvec_checks_under_sanitizers(sanitized_lib):
+    """tests/test_few_cpu.py (the few-token layer and the matrix-vector products) against the same library."""
+    r = subprocess.run([sys.executable, "-m", "pytest", "-q", "-s", "-p", "no:cacheprovider",
+                        os.path.join(ROOT, "tests", "test_few_cpu.py")],
+                       env=sanitized_lib, capture_output=True, text=True, cwd=ROOT, timeout=300)
+    tail = (r.stdout + r.stderr)[-3000:]
+    assert r.returncode == 0, tail
+    assert "AddressSanitizer" not in tail and "runtime error" not in tail, tail
+
+
+def test_every_launcher_is_linked(sanitized_lib):
+    """No launcher may be missing from a library that links: a weak reference to one would be a jump to null."""
+    nm = subprocess.run(["nm", "-C", OUT], capture_output=True, text=True, check=True).stdout.splitlines()
+    ours = [line.split(maxsplit=2) if line[0] != " " else ["", *line.split(maxsplit=1)] for line in nm if "w4a8::" in line]
+    assert any("launch_few" in name for _, _, name in ours) and any("launch_matvec" in name for _, _, name in ours)
+    assert not [name for _, kind, name in ours if kind in "wU"]
