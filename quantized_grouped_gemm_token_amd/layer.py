@@ -22,15 +22,17 @@ W4A8MoEChannel is the per-channel INT4 x per-token INT8 variant: fp32 [E][N]
 scales, INT8 activations.  W4A8MoEMxfp4 holds MXFP4 group-32 experts (E2M1
 codes uint8 [E][N][K/2], E8M0 scales uint8 [E][N][K/32]) and uses the same
 FP8 activations.
-With few=True a forward of at most 16 tokens runs as one call of two kernels
-(w4a8_moe_few_prepacked and its forms) instead of the steps; larger batches, and
-sizes outside that call's rules, take the steps as before.  Its results differ from
-the steps' by rounding.
 Intermediate buffers are allocated once per token count and reused, so a
 forward pass enqueues kernels only: no allocation, no host synchronisation.
 That also makes a step capturable: capture() records one forward into a HIP
 graph, whose replay re-runs the whole step on the current contents of the
 same x, logits and y tensors with a single launch.
+
+With few=True a forward of at most 16 tokens runs as one call of two kernels
+(w4a8_moe_few_prepacked and its forms) instead of the steps; larger batches,
+sizes outside that call's rules, and forwards that ask for a GEMM kernel (algo) take
+the steps as before (uses_few).  front, fused and scatter are about the steps only.
+Its results differ from the steps' by rounding.
 """
 from __future__ import annotations
 
@@ -100,9 +102,10 @@ class W4A8MoE:
         """Whether a forward over T tokens folds the routing weights into the down GEMM."""
         return self.scatter if self.scatter is not None else T * self.k >= self.SCATTER_MIN_ROWS
 
-    def uses_few(self, T: int) -> bool:
-        """Whether a forward over T tokens is the one call for a few tokens."""
-        return self.few and T > 0 and self.I <= ops.FEW_MAX_I and ops.w4a8_moe_few_fits(T, self.H, self.k)
+    def uses_few(self, T: int, algo: int = ops.W4A8_GG_AUTO) -> bool:
+        """Whether a forward over T tokens is the one call for a few tokens (which has no GEMM of an algo)."""
+        return (self.few and algo == ops.W4A8_GG_AUTO and T > 0 and self.I <= ops.FEW_MAX_I
+                and ops.w4a8_moe_few_fits(T, self.H, self.k))
 
     def _forward_few(self, x, logits, y, y_dtype, events):
         # the call allocates its workspace: forwards on several streams, or captured
@@ -125,7 +128,7 @@ class W4A8MoE:
         current stream around each step.
         """
         T = x.shape[0]
-        if self.uses_few(T):
+        if self.uses_few(T, algo):
             return self._forward_few(x, logits, y, y_dtype, events)
         b = self.buffers(T)
         R = T * self.k
@@ -209,7 +212,7 @@ class W4A8MoEChannel(W4A8MoE):
                 y_dtype: torch.dtype = torch.float32, algo: int = ops.W4A8_GG_AUTO,
                 events: dict | None = None) -> torch.Tensor:
         T = x.shape[0]
-        if self.uses_few(T):
+        if self.uses_few(T, algo):
             return self._forward_few(x, logits, y, y_dtype, events)
         b = self.buffers(T)
         R = T * self.k
