@@ -22,7 +22,7 @@ W4A8MoEChannel is the per-channel INT4 x per-token INT8 variant: fp32 [E][N]
 scales, INT8 activations.  W4A8MoEMxfp4 holds MXFP4 group-32 experts (E2M1
 codes uint8 [E][N][K/2], E8M0 scales uint8 [E][N][K/32]) and uses the same
 FP8 activations.
-Intermediate buffers are allocated once per token count and reused, so a
+The steps' intermediate buffers are allocated once per token count and reused, so a
 forward pass enqueues kernels only: no allocation, no host synchronisation.
 That also makes a step capturable: capture() records one forward into a HIP
 graph, whose replay re-runs the whole step on the current contents of the
@@ -32,7 +32,9 @@ With few=True a forward of at most 16 tokens runs as one call of two kernels
 (w4a8_moe_few_prepacked and its forms) instead of the steps; larger batches,
 sizes outside that call's rules, and forwards that ask for a GEMM kernel (algo) take
 the steps as before (uses_few).  front, fused and scatter are about the steps only.
-Its results differ from the steps' by rounding.
+The call's results differ from the steps' by rounding; it fills none of buffers(T),
+and takes its workspace from torch's allocator at every forward (from the graph's
+pool in a captured one).
 """
 from __future__ import annotations
 
@@ -107,10 +109,16 @@ class W4A8MoE:
         return (self.few and algo == ops.W4A8_GG_AUTO and T > 0 and self.I <= ops.FEW_MAX_I
                 and ops.w4a8_moe_few_fits(T, self.H, self.k))
 
+    def steps_for(self, T: int, algo: int = ops.W4A8_GG_AUTO) -> tuple:
+        """The step names of a forward over T tokens, as its events are keyed: ("few",) or self.steps."""
+        return ("few",) if self.uses_few(T, algo) else self.steps
+
     def _forward_few(self, x, logits, y, y_dtype, events):
         # the call allocates its workspace: forwards on several streams, or captured
         # into several graphs, share none
         ev = events.get("few") if events else None
+        if events and not ev:
+            raise ValueError(f"this forward's one step is 'few' (steps_for), not {sorted(events)}")
         if ev:
             ev[0].record()
         y = self.FEW(x, logits, self.k, self.w13, self.s13, self.w2, self.s2, self.renormalize, y, y_dtype)
@@ -123,9 +131,8 @@ class W4A8MoE:
                 events: dict | None = None) -> torch.Tensor:
         """x bf16 [T, H], router logits fp32 [T, E] -> y [T, H].
 
-        events, if given, maps step names (self.steps, or "few" for a forward that
-        is that one call) to (start, end) CUDA events that are recorded on the
-        current stream around each step.
+        events, if given, maps step names (of steps_for(T, algo)) to (start, end) CUDA
+        events that are recorded on the current stream around each step.
         """
         T = x.shape[0]
         if self.uses_few(T, algo):

@@ -1,4 +1,4 @@
-"""A layer with few=True whose caller asks for a GEMM kernel."""
+"""A layer with few=True whose caller asks for a GEMM kernel or for the times of steps."""
 import pytest
 import torch
 
@@ -38,3 +38,22 @@ def test_layer_few_with_a_kernel_asked_for(form):
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(y, ref)
+
+
+@pytest.mark.parametrize("form", FORMS)
+def test_layer_few_events(form):
+    """Events keyed by steps_for are recorded whichever path a forward takes; others are refused."""
+    T, H, I, E, k = 6, 512, 256, 16, 4
+    x_bits, logits, weights = make(form, T, H, I, E, k, seed=92)
+    x, lg = bf16_to_dev(x_bits), to_dev(logits)
+    few = LAYER[form](*(to_dev(a) for a in weights), k=k, few=True)
+    for algo in (ops.W4A8_GG_AUTO, ops.W4A8_GG_STREAM, ops.W4A8_GG_TILED):
+        say(f"layer {form} few=True, algo={algo}, events")
+        ev = {n: (torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True))
+              for n in few.steps_for(T, algo)}
+        want = few(x, lg, algo=algo)
+        assert torch.equal(few(x, lg, algo=algo, events=ev), want)
+        torch.cuda.synchronize()
+        assert all(a.elapsed_time(b) >= 0 for a, b in ev.values())
+    with pytest.raises(ValueError):
+        few(x, lg, events={n: None for n in few.steps})
