@@ -613,6 +613,8 @@ int w4a8_moe_grouped_gemm_swiglu_mxfp4_prepacked(const uint8_t* a, const float* 
  *   arrays is touched.
  *   x is finite: a token with a NaN or an infinity has a row of y without meaning
  *   (NaN in the FP8 forms); the other tokens' rows are what they are without it.
+ *   MXFP4: a scale byte of 255 is NaN; a weight of 2^128 or more (bytes 253 and 254, no
+ *   fp32 value) counts as an infinity.
  *   The same inputs give the same bits at every call.
  */
 
@@ -657,6 +659,8 @@ int w4a8_moe_few_mxfp4_prepacked(const uint16_t* x_bf16, int64_t T, int64_t H, i
  *   Rules   : 0 <= T <= 16; 0 < K <= 2^22, K % 128 == 0 (stored MXFP4: K % 32 == 0);
  *             0 < N <= 2^24, _prepacked: N % 16 == 0.  Larger batches take the grouped
  *             GEMMs.
+ *   MXFP4: a scale byte of 255 is NaN; a weight of 2^128 or more (bytes 253 and 254, no
+ *   fp32 value) counts as an infinity; smaller ones are exact, subnormals included.
  */
 int w4a8_moe_matvec(const uint16_t* x_bf16, int64_t T, int64_t K, int64_t ld_x, const int32_t* w_packed,
                     const float* w_scale, int64_t N, void* y, int32_t y_dtype, void* stream);

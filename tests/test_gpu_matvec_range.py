@@ -1,0 +1,64 @@
+"""Products with MXFP4 weights at the ends of the E8M0 scales."""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from gpu_util import bf16_to_dev, say, to_dev
+from oracle import mxfp4_oracle as mx
+from quantized_grouped_gemm_token_amd import ops
+from test_gpu_few import CALL, make as make_layer, prepack as prepack_layer
+from test_gpu_matvec import BLK, STORED, prepack
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    assert torch.cuda.is_available(), "GPU tests need a GPU"
+    assert ops.w4a8_moe_device_supported(), "the current device is not a gfx950"
+    yield
+    torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("prepacked", [False, True])
+@pytest.mark.parametrize("byte", [0, 1, 2, 3, 127, 251, 252, 253, 254, 255])
+def test_matvec_mxfp4_every_code_at_the_ends_of_the_scales(byte, prepacked):
+    """One weight per output, one activation: the value itself, a subnormal one included; an infinity from 2^128 on
+    (no fp32 value), NaN for byte 255."""
+    K, N = 128, 16
+    w = np.zeros((N, K // 2), np.uint8)
+    w[:, 35] = np.arange(16)                                 # code n at k = 70, in the third block
+    s = np.full((N, K // 32), 127, np.uint8)
+    s[:, 2] = byte
+    say(f"matvec mxfp4 scale byte {byte}, prepacked={prepacked}")
+    wd, sd = prepack("mxfp4", w, s) if prepacked else (to_dev(w), to_dev(s))
+    call = (BLK if prepacked else STORED)["mxfp4"]
+    code = mx.e2m1_decode(np.arange(16, dtype=np.uint8)).astype(np.float64)
+    # activations whose products are the smallest fp32 values that hold a code, ordinary and near the largest: exact
+    for e in (-14, 0, 100) if byte < 4 else (-100, -14, 0):
+        x = np.zeros((1, K), np.float32)
+        x[0, 70] = 2.0 ** e
+        y = call(bf16_to_dev(oracle.f32_to_bf16_bits(x)), wd, sd).double().cpu().numpy()[0]
+        if byte == 255:
+            assert np.isnan(y).all()
+            continue
+        weight = code * 2.0 ** (byte - 127)
+        want = np.where(np.abs(weight) < 2.0 ** 128, weight * 2.0 ** e, np.copysign(np.inf, weight))
+        assert np.array_equal(y, want), (e, y, want)
+
+
+def test_few_mxfp4_scale_of_nan():
+    """Scale byte 255 in one row of w2: that column of y is NaN for the tokens that take the expert, nothing else."""
+    T, H, I, E, k = 4, 256, 128, 4, 1
+    x_bits, logits, weights = make_layer("mxfp4", T, H, I, E, k, seed=13)
+    logits[:] = -5.0
+    logits[np.arange(T), [0, 2, 2, 3]] = 1.0
+    x, lg = bf16_to_dev(x_bits), to_dev(logits)
+    say("few mxfp4 scale byte 255")
+    want = CALL["mxfp4"](x, lg, k, *prepack_layer("mxfp4", weights))
+    weights[3][2, 37, 1] = 255
+    y = CALL["mxfp4"](x, lg, k, *prepack_layer("mxfp4", weights))
+    bad = torch.zeros_like(y, dtype=torch.bool)
+    bad[1:3, 37] = True
+    assert torch.isnan(y[bad]).all() and torch.equal(y[~bad], want[~bad])
