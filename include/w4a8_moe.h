@@ -659,6 +659,10 @@ int w4a8_moe_few_mxfp4_prepacked(const uint16_t* x_bf16, int64_t T, int64_t H, i
  *   Rules   : 0 <= T <= 16; 0 < K <= 2^22, K % 128 == 0 (stored MXFP4: K % 32 == 0);
  *             0 < N <= 2^24, _prepacked: N % 16 == 0.  Larger batches take the grouped
  *             GEMMs.
+ *   x is finite and, in the INT4 forms, at most 2^116 in magnitude (a group's sums of
+ *   x (q + 8) and of -8 x stay finite); a row of x that is not has a row of y without
+ *   meaning (INT4 forms: NaN where x is infinite or NaN), the other rows are what they
+ *   are without it.
  *   MXFP4: a scale byte of 255 is NaN; a weight of 2^128 or more (bytes 253 and 254, no
  *   fp32 value) counts as an infinity; smaller ones are exact, subnormals included.
  */

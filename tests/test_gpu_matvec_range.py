@@ -1,4 +1,4 @@
-"""Products with MXFP4 weights at the ends of the E8M0 scales."""
+"""Matrix-vector products at the ends of their numbers: E8M0 scales, large activations."""
 import numpy as np
 import pytest
 import torch
@@ -8,7 +8,7 @@ from gpu_util import bf16_to_dev, say, to_dev
 from oracle import mxfp4_oracle as mx
 from quantized_grouped_gemm_token_amd import ops
 from test_gpu_few import CALL, make as make_layer, prepack as prepack_layer
-from test_gpu_matvec import BLK, STORED, prepack
+from test_gpu_matvec import BLK, STORED, check, exact, make, prepack
 
 pytestmark = pytest.mark.gpu
 
@@ -46,6 +46,35 @@ def test_matvec_mxfp4_every_code_at_the_ends_of_the_scales(byte, prepacked):
         weight = code * 2.0 ** (byte - 127)
         want = np.where(np.abs(weight) < 2.0 ** 128, weight * 2.0 ** e, np.copysign(np.inf, weight))
         assert np.array_equal(y, want), (e, y, want)
+
+
+@pytest.mark.parametrize("form", ["g128", "channel"])
+def test_matvec_int4_largest_activations(form, rng):
+    """Activations of up to 2^116: a group's sums of x (q + 8) and of -8 x stay finite."""
+    T, N, K = 4, 48, 1152
+    x_bits, w, s = make(form, T, N, K, rng)
+    x = oracle.bf16_bits_to_f32(x_bits)
+    x = np.sign(x) * np.exp2(rng.integers(100, 117, size=x.shape)).astype(np.float32)
+    x[1] = 2.0 ** 116                                        # every element of one sign
+    x_bits, s = oracle.f32_to_bf16_bits(x), (s * np.float32(2.0 ** -20)).astype(np.float32)
+    want, tol = exact(form, x_bits, w, s)
+    say(f"matvec {form} largest activations")
+    xd = bf16_to_dev(x_bits)
+    y = STORED[form](xd, to_dev(w), to_dev(s))
+    assert torch.isfinite(y).all()
+    check(y, want, tol, "stored")
+    blk = BLK[form](xd, *prepack(form, w, s))
+    assert torch.equal(blk, y)
+
+
+@pytest.mark.parametrize("form", ["g128", "channel"])
+def test_matvec_int4_infinite_activations_give_nan(form, rng):
+    x_bits, w, s = make(form, 3, 32, 256, rng)
+    x = bf16_to_dev(x_bits)
+    x[1, 77], x[2, 3] = float("inf"), float("-inf")
+    say(f"matvec {form} infinities in x")
+    y = STORED[form](x, to_dev(w), to_dev(s))
+    assert torch.isfinite(y[0]).all() and torch.isnan(y[1:]).all()
 
 
 def test_few_mxfp4_scale_of_nan():
