@@ -660,7 +660,8 @@ int w4a8_moe_few_mxfp4_prepacked(const uint16_t* x_bf16, int64_t T, int64_t H, i
  *             0 < N <= 2^24, _prepacked: N % 16 == 0.  Larger batches take the grouped
  *             GEMMs.
  *   x is finite and, in the INT4 forms, at most 2^116 in magnitude (a group's sums of
- *   x (q + 8) and of -8 x stay finite); a row of x that is not has a row of y without
+ *   x (q + 8) and of -8 x stay finite; per channel the sum of x q over all k, which the
+ *   scale follows, has to as well); a row of x that is not has a row of y without
  *   meaning (INT4 forms: NaN where x is infinite or NaN), the other rows are what they
  *   are without it.
  *   MXFP4: a scale byte of 255 is NaN; a weight of 2^128 or more (bytes 253 and 254, no
