@@ -596,7 +596,8 @@ int w4a8_moe_grouped_gemm_swiglu_mxfp4_prepacked(const uint8_t* a, const float* 
  *               the _prepacked GEMMs of the same form (_i8 : fp32 [E][2I] and [E][H]).
  *   ids, w    : int32 [T][k] and fp32 [T][k], written; either may be NULL.
  *   y         : [T][H], fp32 or bf16 (y_dtype, as in w4a8_moe_unpermute; bf16 rounded
- *               to nearest even), aligned to its elements.
+ *               to nearest even), aligned to its elements.  It may be x's memory or
+ *               the logits' (the second kernel, which writes it, reads neither).
  *   workspace : device memory of w4a8_moe_few_workspace_bytes(T, k, I) bytes, 16-byte
  *               aligned (contents need no initialisation; calls that overlap must not
  *               share one).
@@ -655,7 +656,8 @@ int w4a8_moe_few_mxfp4_prepacked(const uint16_t* x_bf16, int64_t T, int64_t H, i
  *             (the E = 1 case of the grouped GEMMs' arrays): weights 16-byte aligned,
  *             fp32 scales and the GEMM storage's E8M0 words 4-byte aligned.
  *   y       : [T][N], fp32 or bf16 (y_dtype; rounded to nearest even), aligned to its
- *             elements.
+ *             elements; no overlap with the inputs (not checked here: workgroups write
+ *             y while others still read x).
  *   Rules   : 0 <= T <= 16; 0 < K <= 2^22, K % 128 == 0 (stored MXFP4: K % 32 == 0);
  *             0 < N <= 2^24, _prepacked: N % 16 == 0.  Larger batches take the grouped
  *             GEMMs.

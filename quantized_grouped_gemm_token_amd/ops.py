@@ -963,6 +963,16 @@ def _y(y, y_dtype, T: int, N: int, x: torch.Tensor, dev):
     return y, W4A8_Y_F32 if y.dtype is _F32 else W4A8_Y_BF16
 
 
+def _apart(y: torch.Tensor, x: torch.Tensor, T: int, K: int) -> None:
+    """y shares no memory with the rows of x (it may lie between them)."""
+    lo, hi = y.data_ptr(), y.data_ptr() + y.numel() * y.element_size()
+    x0, step = x.data_ptr(), 2 * _ld(x, T, K)
+    if step >= 2 * K > 0 and lo < x0 + (T - 1) * step + 2 * K and x0 < hi:      # (other strides are refused below)
+        for r in range(x0, x0 + T * step, step):
+            if lo < r + 2 * K and r < hi:
+                raise ValueError("y must not overlap x, which is read while y is written")
+
+
 _functions: dict = {}
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)   # (dev is a GPU: it is initialised)
@@ -1095,7 +1105,10 @@ def _matvec(name, form, prepacked, x, w, s, y, y_dtype):
         _is(w, "w", _U8 if mx else _I32, (N, K // 2 if mx else K // 8), dev)
         want = (N,) if form == "channel" else (N, K // 32) if mx else (N, K // 128)
     _is(s, "s", _U8 if mx else _F32, want, dev)
+    given = y
     y, code = _y(y, y_dtype, T, N, x, dev)
+    if given is not None and T:
+        _apart(y, x, T, K)
     _call_on(dev, name, x.data_ptr(), T, K, _ld(x, T, K), w.data_ptr(), s.data_ptr(), N, y.data_ptr(), code)
     return y
 
