@@ -2,13 +2,17 @@
 // (few.hip) and the matrix-vector product (matvec.hip).
 //
 // Both read every weight once for at most 16 activation rows, so they are bound
-// by HBM and can afford the bf16 matrix cores, whose sums are fp32: measured over
-// K = 128 (test_one_group_on_the_bf16_matrix_cores), 16x16x32 products and sums
-// of normally distributed activations stay within 9.7e-9 of sum |products| (rms
-// 7.8e-10; a serial fp32 sum: 5.5e-9, 3.5e-10), of ones spread over 24 binades within
-// 2.4e-7 (rms 3.1e-8; a serial sum: 3.2e-7, 4.8e-8), against 7.5e-6 for the FP8
-// form that the grouped GEMMs use.  Every operand is exact in bf16: an FP8 or bf16
-// activation, an INT4 value u = q + 8 (0..15), an E2M1 code times a power of two.
+// by HBM and can afford the bf16 matrix cores, whose sums are fp32.  Largest and rms
+// error over K = 128 in units of sum |products| (16 x 4096 outputs,
+// test_one_group_on_the_bf16_matrix_cores), against a serial fp32 sum of the same:
+//   activations                 INT4 (u and -8)           E2M1
+//   normally distributed        9.7e-9, 6.2e-10           3.0e-8, 1.2e-9
+//     a serial sum              9.7e-9, 4.9e-10           3.0e-8, 1.4e-9
+//   spread over 24 binades      2.0e-7, 1.9e-8            1.8e-7, 2.9e-8
+//     a serial sum              3.1e-7, 3.6e-8            4.5e-7, 4.9e-8
+// The FP8 form that the grouped GEMMs use is off by up to 7.5e-6.  Every operand is
+// exact in bf16: an FP8 or bf16 activation, an INT4 value u = q + 8 (0..15), an E2M1
+// code times a power of two (below 2^128).
 //
 // The conversions are one instruction per two values at the rate of an FMA:
 //   * INT4: two masks and a shift give the bytes u of a word; u read as E4M3 is

@@ -56,22 +56,25 @@ def test_few_act_and_y_to_fp32_rounding(form, T, H, I, E, k):
     assert rms_y <= 1 and top_y <= 8, "y"
 
 
+@pytest.mark.parametrize("binades", [0, 24])
 @pytest.mark.parametrize("form", ["g128", "mxfp4"])
-def test_one_group_on_the_bf16_matrix_cores(form, rng):
+def test_one_group_on_the_bf16_matrix_cores(form, binades):
     """K = 128, scale 1: the products and sums of one group, eight (MXFP4: four) instructions in a row.
 
     An instruction's order of adding is its own, so what holds for any is all that bounds an element: an fp32 sum of
     n terms takes n - 1 additions, each off by at most U of a partial sum <= sum |products|.  In the mean square the
     instructions are as good as if each rounded its result once."""
     T, N, K = 16, 4096, 128
+    rng = np.random.Generator(np.random.PCG64(binades))
     _, w, s = make_mv(form, T, N, K, rng)
     s = np.full_like(s, 127 if form == "mxfp4" else 1)
-    # (over 24 binades: ordinary ones hardly round at all in one group)
-    x_bits = oracle.f32_to_bf16_bits((rng.standard_normal((T, K)) * np.exp2(rng.uniform(-12, 12, (T, K)))).astype(np.float32))
+    # (normally distributed, and spread over 24 binades: the former hardly round at all in one group)
+    x = rng.standard_normal((T, K)) * np.exp2(rng.uniform(-binades / 2, binades / 2, (T, K)))
+    x_bits = oracle.f32_to_bf16_bits(x.astype(np.float32))
     want, _ = exact(form, x_bits, w, s)
     x = oracle.bf16_bits_to_f32(x_bits).astype(np.float64)
     B = np.abs(x) @ scaled(form, w, s)[1].T
-    say(f"one group {form}")
+    say(f"one group {form}, {binades} binades")
     err = (host(STORED[form](bf16_to_dev(x_bits), to_dev(w), to_dev(s))).astype(np.float64) - want) / B
     top, rms = float(np.abs(err).max()), float(np.sqrt(np.mean(err ** 2)))
     say(f"  largest {top:.2e}, rms {rms:.2e} of sum |products|")
