@@ -24,12 +24,13 @@
 //
 // Measured (H 6144, I 2048, 256 experts, 8 picks; kernel times, weights and scales read):
 //             gate/up                  down
-//   1 token   24.5 us (107 MB, 4.4 TB/s)  16.0 us (54 MB, 3.3 TB/s)   group 128
-//   4 tokens  71 us (408 MB, 5.7 TB/s)    40 us (204 MB, 5.1 TB/s)    MXFP4
-//   16 tokens 227 us (1.36 GB, 6.0 TB/s)  130 us (0.68 GB, 5.2 TB/s)  group 128
-// against about 6.5 TB/s that a long read reaches.  With one token the start bounds both:
-// about 7 us of the first kernel (launch, logits and x, the picks at 0.2 us each, then the
-// first weights) and 5 us of the second, during which HBM has little to do.
+//   1 token   23.6 us (107 MB, 4.5 TB/s)  16.0 us (54 MB, 3.3 TB/s)   group 128
+//   4 tokens  70 us (408 MB, 5.8 TB/s)    40 us (204 MB, 5.1 TB/s)    MXFP4
+//   16 tokens 226 us (1.36 GB, 6.0 TB/s)  131 us (0.68 GB, 5.2 TB/s)  group 128
+// against about 6.5 TB/s that a long read reaches.  With one token the start bounds both
+// (launch; logits and x, then the picks one after the other, then the first weights; count,
+// act, then weights): a layer with next to no bytes takes 9.3 and 8.7 us (16 tokens, 8
+// experts of I 128).
 #include "kernels.hpp"
 #include "w4_bf16.hpp"
 
@@ -1016,7 +1017,8 @@ constexpr int64_t kFewGrid = 256;
 // 32 tasks 10.1 us, 64 of 16 columns 9.9).  Gate/up, 32 against 16: 16 tokens (H 6144, I 2048, group
 // 128) 227 against 246 us, 12 tokens 185 against 199, 12 tokens MXFP4 177 against 179, 16 tokens (H 4096,
 // I 1024, 64 experts) 46.5 against 44.8; 8 tokens 132 against 136, (H 4096, I 1024) 32.0 against 29.4; 1 token 26.7
-// against 24.6.
+// against 24.6.  So the rule takes the slower form, by 3 to 4 %, at 16 tokens of the smaller layer and at 8 of
+// the larger: what decides may be the tasks per workgroup rather than the tokens.
 constexpr int64_t kFewWideTokens = 9;
 
 template <int kForm, int GW, int S, int NC>

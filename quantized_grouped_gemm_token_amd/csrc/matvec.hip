@@ -12,9 +12,11 @@
 // Rows of A past T repeat row T - 1; their products are never stored.
 //
 // Measured (group 128, GEMM storage; kernel times): 1 x 131072 x 6144 67 us (428 MB, 6.4
-// TB/s), 16 x 65536 x 6144 40.5 us (5.3 TB/s), 1 x 12288 x 6144 11.8 us (40 MB, 3.4 TB/s),
-// 1 x 4096 x 6144 7.1 us, 1 x 2048 x 2048 4.1 us: up to some 20 MB the start bounds it (the
-// launch, one trip to memory for the weights, the exchange in LDS).  A call from the host
+// TB/s), 16 x 65536 x 6144 40.5 us (5.3 TB/s), 16 x 12288 x 6144 13.8 us (41 MB, 3.0 TB/s; 13.4
+// with the weights of three matrices in turn, which the 256 MB last-level cache holds),
+// 1 x 4096 x 6144 8.3 us (7.3 from the cache), 1 x 2048 x 2048 4.1 us (from the cache): up to
+// some 20 MB the start bounds it (the launch, one trip to memory for the weights, which the
+// turn of x waits for as they are issued first, the exchange in LDS).  A call from the host
 // takes about 7 us, so the smallest are bound by that.
 #include "kernels.hpp"
 #include "w4_bf16.hpp"
@@ -222,11 +224,15 @@ static void launch_matvec_steps(const MatvecArgs& a, hipStream_t stream) {
   };
   // Steps of 32 outputs (whole lines of scales, half the exchanges) from two steps of them per workgroup on: K
   // 4096, N 32768 15.1 against 16.3 us, N 4096 7.0 against 6.3.  With K in parts from one on, as each step fetches
-  // the activations again: 8192 x 16384 21.6 against 26.7 us.
+  // the activations again: 8192 x 16384 21.6 against 26.7 us (group 128).
   if (a.N >= (kParts ? 32 : 64) * kMvGrid) go(matvec_kernel<kForm, kRM, GW, 2, kParts>, 2);
   else go(matvec_kernel<kForm, kRM, GW, 1, kParts>, 1);
 }
 
+// K above 6144 goes in parts, at a cost: a part's activations are fetched behind its weights, and waiting for them
+// drains the prefetch; the MXFP4 form also spills registers (10 to 12 of 256 in steps of 16 outputs, 103 to 125 in
+// steps of 32).  1 / 16 rows of 8192 x 8192: group 128 14.9 / 18.7 us, per channel 14.9 / 17.5, MXFP4 30.4 / 42.9; of
+// 6144 x 12288: 19.7 / 27.6, 19.6 / 27.1 and 28.2 / 45.1, against 13.8 for 16 rows of 12288 x 6144.
 template <int kForm, bool kRM>
 static void launch_matvec_form(const MatvecArgs& a, hipStream_t stream) {
   const int64_t gpw = ((a.K + kGroup - 1) / kGroup + kMvWaves - 1) / kMvWaves;   // K groups per wave
