@@ -1,4 +1,5 @@
 """y in memory that the call also reads: refused by the matrix-vector products, allowed by the few-token layer."""
+import numpy as np
 import pytest
 import torch
 
@@ -8,6 +9,11 @@ from test_gpu_few import CALL, FORMS, make as make_layer, prepack as prepack_lay
 from test_gpu_matvec import BLK, STORED, make, prepack
 
 pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture
+def rng():
+    return np.random.Generator(np.random.PCG64(7))
 
 
 @pytest.fixture(scope="module", autouse=True)

@@ -13,6 +13,11 @@ from test_gpu_matvec import BLK, STORED, check, exact, make, prepack
 pytestmark = pytest.mark.gpu
 
 
+@pytest.fixture
+def rng():
+    return np.random.Generator(np.random.PCG64(7))
+
+
 @pytest.fixture(scope="module", autouse=True)
 def _gpu():
     assert torch.cuda.is_available(), "GPU tests need a GPU"
