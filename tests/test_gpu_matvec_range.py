@@ -96,3 +96,18 @@ def test_few_mxfp4_scale_of_nan():
     bad = torch.zeros_like(y, dtype=torch.bool)
     bad[1:3, 37] = True
     assert torch.isnan(y[bad]).all() and torch.equal(y[~bad], want[~bad])
+
+
+@pytest.mark.parametrize("T,N", [(3, 37), (16, 8200), (1, 1)])
+@pytest.mark.parametrize("K", [6176, 6240, 12352, 18464])
+def test_matvec_mxfp4_long_rows_that_end_inside_a_group(K, T, N, rng):
+    """Stored rows of several parts whose last group is not whole; what follows a row of x is NaN."""
+    x_bits, w, s = make("mxfp4", T, N, K, rng)
+    want, tol = exact("mxfp4", x_bits, w, s)
+    say(f"matvec mxfp4 T={T} N={N} K={K}")
+    wide = torch.full((T, K + 8), float("nan"), dtype=torch.bfloat16, device="cuda:0")
+    wide[:, :K] = bf16_to_dev(x_bits)
+    wd, sd = to_dev(w), to_dev(s)
+    y = STORED["mxfp4"](wide[:, :K], wd, sd)
+    check(y, want, tol, "strided")
+    assert torch.equal(STORED["mxfp4"](bf16_to_dev(x_bits), wd, sd), y)
