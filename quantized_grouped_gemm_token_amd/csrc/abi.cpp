@@ -10,11 +10,15 @@
 #include <cstring>
 #include <string>
 
+#include "abi_common.hpp"
 #include "kernels.hpp"
 
-namespace {
+namespace w4a8 {
+namespace abi {
 
+namespace {
 thread_local std::string g_last_error;
+}  // namespace
 
 int fail(int status, const char* fmt, ...) {
   char buf[512];
@@ -31,10 +35,10 @@ int ok() {
   return W4A8_OK;
 }
 
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
+namespace {
 constexpr int kMaxDevices = 64;
 std::atomic<int> g_device_ok[kMaxDevices];   // 0 unknown, 1 gfx950, 2 other
+}  // namespace
 
 // 1 if the current device is a gfx950; fills the error detail otherwise.
 int check_device() {
@@ -67,11 +71,10 @@ int launched(hipError_t e, const char* what) {
   return ok();
 }
 
-hipStream_t as_stream(void* s) { return reinterpret_cast<hipStream_t>(s); }
+}  // namespace abi
+}  // namespace w4a8
 
-constexpr int64_t kMaxRows = (int64_t)1 << 31;   // row indices are int32
-
-}  // namespace
+using namespace w4a8::abi;
 
 extern "C" {
 

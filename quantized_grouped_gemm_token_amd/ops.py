@@ -93,6 +93,23 @@ _SIGNATURES = {
     "w4a8_moe_device_supported": (ctypes.c_int, []),
 }
 
+# include/w4a8_block.h: the operators around the experts (bound at their first call)
+_DENSE = [_c_p, _c_p, _i64, _i64, _i64, _c_p, _c_p]
+_NORM = [_c_p, _i32, _i64, _i64, _i64, _c_p, ctypes.c_float]
+_RESIDUAL = [_c_p, _i32, _i64, _c_p, _i32, _i64, _i64, _i64, _c_p, _c_p, _c_p, ctypes.c_float, ctypes.c_float, _c_p,
+             _i64]
+_BLOCK_SIGNATURES = {
+    "w4a8_moe_dense_i8_workspace_bytes": (ctypes.c_int64, [_i64, _i64, _i64]),
+    "w4a8_moe_dense_i8": (ctypes.c_int, _DENSE + [_c_p, _i64, _c_p, _c_p, _i32, _c_p, _i64, _c_p]),
+    "w4a8_moe_mlp_i8_workspace_bytes": (ctypes.c_int64, [_i64, _i64, _i64]),
+    "w4a8_moe_mlp_i8": (ctypes.c_int, _DENSE + [_c_p, _c_p, _i64, _c_p, _c_p, _i32, _c_p, _i64, _c_p]),
+    "w4a8_moe_norm_quant": (ctypes.c_int, _NORM + [_c_p, _c_p, _c_p, _c_p]),
+    "w4a8_moe_norm_quant_i8": (ctypes.c_int, _NORM + [_c_p, _c_p, _c_p, _c_p, _c_p]),
+    "w4a8_moe_residual_norm": (ctypes.c_int, _RESIDUAL + [_c_p]),
+    "w4a8_moe_residual_norm_quant": (ctypes.c_int, _RESIDUAL + [_c_p, _c_p, _c_p, _c_p, _c_p]),
+    "w4a8_moe_residual_norm_quant_i8": (ctypes.c_int, _RESIDUAL + [_c_p, _c_p, _c_p, _c_p, _c_p, _c_p]),
+}
+
 
 class W4A8Error(RuntimeError):
     """A nonzero status from the library."""
@@ -978,11 +995,18 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)   # (dev is a GPU: it is initialised)
 
 
+def _function(name: str):
+    f = getattr(lib(), name)
+    if name in _BLOCK_SIGNATURES:
+        f.restype, f.argtypes = _BLOCK_SIGNATURES[name]
+    return f
+
+
 def _call_on(dev: torch.device, name: str, *args) -> None:
     """The library call on dev's current stream, with dev the current device."""
     f = _functions.get(name)
     if f is None:
-        f = _functions[name] = getattr(lib(), name)
+        f = _functions[name] = _function(name)
     i = dev.index
     if i == _current_device():
         status = f(*args, _raw_stream(i) if _raw_stream else _stream(dev))
@@ -1149,3 +1173,280 @@ def w4a8_moe_matvec_mxfp4_prepacked(x: torch.Tensor, w: torch.Tensor, s: torch.T
                                     y: torch.Tensor | None = None, y_dtype: torch.dtype = torch.float32):
     """The same on the GEMM storage (w uint8 [N/16, K/128, 16, 64], s uint8 [K/128, N, 4])."""
     return _matvec("w4a8_moe_matvec_mxfp4_prepacked", "mxfp4", True, x, w, s, y, y_dtype)
+
+
+# ------------------------------------------------- around the experts: dense products, the gated block, norms
+_I8 = torch.int8
+
+
+def _rows(t, name: str, dtypes: tuple, quantum: int) -> tuple[int, int, int]:
+    """(T, H, elements between two rows) of a GPU tensor [T, H] with contiguous rows whose distance is a whole
+    number of 16 bytes (quantum elements; the library checks it)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have 2 dims, got shape {tuple(t.shape)}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor")
+    T, H = t.shape
+    if H > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    # a single row has no distance to the next: any that the library admits
+    return T, H, t.stride(0) if T > 1 else -(-H // quantum) * quantum
+
+
+def _span(t: torch.Tensor) -> tuple[int, int]:
+    """The addresses from a tensor's first byte to behind its last (rows and columns of positive stride)."""
+    lo = t.data_ptr()
+    return lo, lo + (sum((n - 1) * s for n, s in zip(t.shape, t.stride())) + 1) * t.element_size()
+
+
+def _between(a: torch.Tensor, b: torch.Tensor) -> bool:
+    """Whether the rows of b lie between those of a (both [T, H], the same distance from row to row)."""
+    if a.dim() != 2 or b.dim() != 2 or a.shape[0] < 2 or b.shape[0] < 2:
+        return False
+    step, other = a.stride(0) * a.element_size(), b.stride(0) * b.element_size()
+    ra, rb = a.shape[1] * a.element_size(), b.shape[1] * b.element_size()
+    d = (b.data_ptr() - a.data_ptr()) % step if step > 0 else 0
+    return step == other and d >= ra and d + rb <= step
+
+
+def _no_overlap(out, name: str, *inputs) -> None:
+    """A result given by the caller shares no memory with what is read while it is written."""
+    lo, hi = _span(out)
+    for other, t in inputs:
+        if t is not None and t.numel():
+            a, b = _span(t)
+            if lo < b and a < hi and not _between(out, t):
+                raise ValueError(f"{name} must not overlap {other}")
+
+
+def _dense_out(y, y_dtype, M: int, N: int, add, dev, x: torch.Tensor, inputs: tuple):
+    """y (given, or allocated) with its type's code; add has its type and shape, and is y or apart from it."""
+    if y is None:
+        if add is not None and isinstance(add, torch.Tensor) and add.dtype is not y_dtype:
+            raise TypeError(f"add must have y's type {y_dtype}")
+        if y_dtype is not _BF16 and y_dtype is not _F32:
+            raise TypeError("y must be float32 or bfloat16")
+        y = x.new_empty((M, N), dtype=y_dtype)
+    else:
+        if not isinstance(y, torch.Tensor) or y.dtype not in (_F32, _BF16):
+            raise TypeError("y must be a float32 or bfloat16 tensor")
+        _is(y, "y", y.dtype, (M, N), dev)
+        if M and N:
+            apart = () if add is None or (isinstance(add, torch.Tensor) and add.data_ptr() == y.data_ptr()) else \
+                (("add", add),)
+            _no_overlap(y, "y", *inputs, *apart)
+    if add is not None:
+        _is(add, "add", y.dtype, (M, N), dev)
+    return y, W4A8_Y_F32 if y.dtype is _F32 else W4A8_Y_BF16
+
+
+def w4a8_moe_dense_i8_workspace_bytes(M: int, N: int, K: int) -> int:
+    n = _function("w4a8_moe_dense_i8_workspace_bytes")(M, N, K)
+    if n < 0:
+        raise ValueError(f"sizes outside the rules of the dense product: M={M} N={N} K={K}")
+    return n
+
+
+def _workspace(given, name: str, dev, *sizes):
+    """(pointer, bytes, tensor) of the workspace of a call: given, or allocated where it needs one."""
+    if given is not None:
+        _need(given, "workspace", _U8, 1, dev)
+        return given.data_ptr(), given.numel(), given
+    f = _functions.get(name)
+    if f is None:
+        f = _functions[name] = _function(name)
+    n = f(*sizes)                                            # (-1 on sizes that the call refuses)
+    if n <= 0:
+        return None, 0, None
+    t = torch.empty((n,), dtype=_U8, device=dev)
+    return t.data_ptr(), n, t
+
+
+def w4a8_moe_dense_i8(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor,
+                      bias: torch.Tensor | None = None, add: torch.Tensor | None = None,
+                      y: torch.Tensor | None = None, y_dtype: torch.dtype = torch.float32,
+                      workspace: torch.Tensor | None = None):
+    """int8 activation codes a [M, K] (rows any multiple of 16 elements apart) with scales fp32 [M] times int8
+    weights w [N, K] with scales fp32 [N], plus bias fp32 [N] and add [M, N] (y's type; it may be y) -> y [M, N]
+    (fp32 or bf16).  The integer sums are exact."""
+    M, K, ld = _rows(a, "a", (_I8,), 16)
+    dev = a.device
+    if not isinstance(w, torch.Tensor) or w.dim() != 2:
+        raise ValueError("w must be an int8 matrix [N, K]")
+    N = w.shape[0]
+    _is(w, "w", _I8, (N, K), dev)
+    _is(a_scale, "a_scale", _F32, (M,), dev)
+    _is(w_scale, "w_scale", _F32, (N,), dev)
+    if bias is not None:
+        _is(bias, "bias", _F32, (N,), dev)
+    y, code = _dense_out(y, y_dtype, M, N, add, dev, a,
+                         (("a", a), ("a_scale", a_scale), ("w", w), ("w_scale", w_scale), ("bias", bias)))
+    ws, nbytes, held = _workspace(workspace, "w4a8_moe_dense_i8_workspace_bytes", dev, M, N, K)
+    _call_on(dev, "w4a8_moe_dense_i8", a.data_ptr(), a_scale.data_ptr(), M, K, ld, w.data_ptr(), w_scale.data_ptr(),
+             _p(bias), N, _p(add), y.data_ptr(), code, ws, nbytes)
+    return y
+
+
+def w4a8_moe_mlp_i8_workspace_bytes(M: int, H: int, I: int) -> int:
+    n = _function("w4a8_moe_mlp_i8_workspace_bytes")(M, H, I)
+    if n < 0:
+        raise ValueError(f"sizes outside the rules of the gated block: M={M} H={H} I={I}")
+    return n
+
+
+def w4a8_moe_mlp_i8(a: torch.Tensor, a_scale: torch.Tensor, w13: torch.Tensor, s13: torch.Tensor, w2: torch.Tensor,
+                    s2: torch.Tensor, add: torch.Tensor | None = None, y: torch.Tensor | None = None,
+                    y_dtype: torch.dtype = torch.float32, workspace: torch.Tensor | None = None):
+    """The gated feed-forward block on int8 weights: codes a [M, H] (rows any multiple of 16 elements apart) with
+    scales fp32 [M], w13 int8 [2I, H] (gate rows, then up rows) with s13 fp32 [2I], w2 int8 [H, I] with s2 fp32 [H],
+    plus add [M, H] (y's type; it may be y) -> y [M, H] (fp32 or bf16).  act = silu(gate) * up is quantized to int8
+    per row in between.  workspace: uint8 [w4a8_moe_mlp_i8_workspace_bytes(M, H, I)], allocated here if not given."""
+    M, H, ld = _rows(a, "a", (_I8,), 16)
+    dev = a.device
+    if not isinstance(w2, torch.Tensor) or w2.dim() != 2:
+        raise ValueError("w2 must be an int8 matrix [H, I]")
+    I = w2.shape[1]
+    _is(w13, "w13", _I8, (2 * I, H), dev)
+    _is(w2, "w2", _I8, (H, I), dev)
+    _is(a_scale, "a_scale", _F32, (M,), dev)
+    _is(s13, "s13", _F32, (2 * I,), dev)
+    _is(s2, "s2", _F32, (H,), dev)
+    y, code = _dense_out(y, y_dtype, M, H, add, dev, a, (("a", a), ("a_scale", a_scale), ("w13", w13), ("s13", s13),
+                                                         ("w2", w2), ("s2", s2)))
+    ws, nbytes, held = _workspace(workspace, "w4a8_moe_mlp_i8_workspace_bytes", dev, M, H, I)
+    _call_on(dev, "w4a8_moe_mlp_i8", a.data_ptr(), a_scale.data_ptr(), M, H, ld, w13.data_ptr(), s13.data_ptr(),
+             w2.data_ptr(), s2.data_ptr(), I, _p(add), y.data_ptr(), code, ws, nbytes)
+    return y
+
+
+_FLOATS = (_BF16, _F32)
+
+
+def _code(t: torch.Tensor) -> int:
+    return W4A8_Y_BF16 if t.dtype is _BF16 else W4A8_Y_F32
+
+
+def _coded_rows(x: torch.Tensor, T: int, H: int, codes, xn, q, s, dev):
+    """The outputs of a norm before a block: given, or allocated."""
+    if xn is None:
+        xn = x.new_empty((T, H), dtype=_BF16)
+    else:
+        _is(xn, "xn", _BF16, (T, H), dev)
+    if q is None:
+        q = x.new_empty((T, H), dtype=codes)
+    else:
+        _is(q, "qx", codes, (T, H), dev)
+    if s is None:
+        s = x.new_empty((T,), dtype=_F32)
+    else:
+        _is(s, "sx", _F32, (T,), dev)
+    return xn, q, s
+
+
+def _norm_quant(name, codes, x, weight, eps, xn, qx, sx, rowsum):
+    T, H, ld = _rows(x, "x", _FLOATS, 8)
+    dev = x.device
+    _is(weight, "weight", _F32, (H,), dev)
+    given = [(n, t) for n, t in (("xn", xn), ("qx", qx), ("sx", sx), ("rowsum", rowsum)) if t is not None]
+    xn, qx, sx = _coded_rows(x, T, H, codes, xn, qx, sx, dev)
+    if rowsum is not None:
+        _is(rowsum, "rowsum", _I32, (T,), dev)
+    if T:
+        for i, (n, t) in enumerate(given):
+            _no_overlap(t, n, ("x", x), ("weight", weight), *given[:i])
+    tail = (_p(rowsum),) if codes is _I8 else ()
+    _call_on(dev, name, x.data_ptr(), _code(x), T, H, ld, weight.data_ptr(), eps, xn.data_ptr(), qx.data_ptr(),
+             sx.data_ptr(), *tail)
+    return xn, qx, sx
+
+
+def w4a8_moe_norm_quant(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, xn: torch.Tensor | None = None,
+                        qx: torch.Tensor | None = None, sx: torch.Tensor | None = None):
+    """RMS norm before a block: x [T, H] (fp32 or bf16, rows a whole number of 16 bytes apart), weight fp32 [H]
+    -> (xn bf16 [T, H], E4M3 codes uint8 [T, H], scales fp32 [T]); the codes are of the norm as it is before its
+    rounding to bf16."""
+    return _norm_quant("w4a8_moe_norm_quant", _U8, x, weight, eps, xn, qx, sx, None)
+
+
+def w4a8_moe_norm_quant_i8(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, xn: torch.Tensor | None = None,
+                           qx: torch.Tensor | None = None, sx: torch.Tensor | None = None,
+                           rowsum: torch.Tensor | None = None):
+    """The same with int8 codes [T, H]; rowsum int32 [T], if given, receives the sums of each row's codes (which the
+    INT4 x INT8 products need)."""
+    return _norm_quant("w4a8_moe_norm_quant_i8", _I8, x, weight, eps, xn, qx, sx, rowsum)
+
+
+def _residual(name, codes, y, r, next_weight, post_weight, gate, token_gate, r_scale, eps, out, xn, qx, sx, rowsum):
+    T, H, ld_y = _rows(y, "y", _FLOATS, 8)
+    dev = y.device
+    Tr, Hr, ld_r = _rows(r, "r", _FLOATS, 8)
+    if (Tr, Hr) != (T, H) or r.device != dev:
+        raise ValueError(f"r must be [{T}, {H}] on {dev} like y, got {list(r.shape)} on {r.device}")
+    for n, v, size in (("post_weight", post_weight, H), ("gate", gate, H), ("token_gate", token_gate, T)):
+        if v is not None:
+            _is(v, n, _F32, (size,), dev)
+    vectors = (("post_weight", post_weight), ("gate", gate), ("token_gate", token_gate))
+    if out is None:
+        out, ld_out = r.new_empty((T, H)), -(-H // 8) * 8
+    else:
+        To, Ho, ld_out = _rows(out, "out", (r.dtype,), 8)
+        if (To, Ho) != (T, H) or out.device != dev:
+            raise ValueError(f"out must be [{T}, {H}] on {dev}, got {list(out.shape)} on {out.device}")
+        if T:
+            # out may be r or y themselves: a row is read whole before it is written
+            same = lambda t, ld: t.data_ptr() == out.data_ptr() and t.dtype is out.dtype and ld == ld_out  # noqa: E731
+            _no_overlap(out, "out", *(() if same(r, ld_r) else (("r", r),)), *(() if same(y, ld_y) else (("y", y),)),
+                        *vectors)
+    args = (y.data_ptr(), _code(y), ld_y, r.data_ptr(), _code(r), ld_r, T, H, _p(post_weight), _p(gate),
+            _p(token_gate), r_scale, eps, out.data_ptr(), ld_out)
+    if codes is None:
+        _call_on(dev, name, *args)
+        return out
+    _is(next_weight, "next_weight", _F32, (H,), dev)
+    given = [(n, t) for n, t in (("xn", xn), ("qx", qx), ("sx", sx), ("rowsum", rowsum)) if t is not None]
+    xn, qx, sx = _coded_rows(y, T, H, codes, xn, qx, sx, dev)
+    if rowsum is not None:
+        _is(rowsum, "rowsum", _I32, (T,), dev)
+    if T:
+        _no_overlap(out, "out", ("next_weight", next_weight))
+        for i, (n, t) in enumerate(given):
+            _no_overlap(t, n, ("y", y), ("r", r), ("out", out), ("next_weight", next_weight), *vectors, *given[:i])
+    tail = (_p(rowsum),) if codes is _I8 else ()
+    _call_on(dev, name, *args, next_weight.data_ptr(), xn.data_ptr(), qx.data_ptr(), sx.data_ptr(), *tail)
+    return out, xn, qx, sx
+
+
+def w4a8_moe_residual_norm(y: torch.Tensor, r: torch.Tensor, post_weight: torch.Tensor | None = None,
+                           gate: torch.Tensor | None = None, token_gate: torch.Tensor | None = None,
+                           r_scale: float = 1.0, eps: float = 1e-6, out: torch.Tensor | None = None):
+    """After a block whose result is y [T, H]: out = r_scale r + token_gate gate norm(y), with the residual r [T, H]
+    (y, r fp32 or bf16, rows a whole number of 16 bytes apart), post_weight fp32 [H] (None: y as it is), gate fp32 [H]
+    and token_gate fp32 [T] (None: 1) -> out [T, H] of r's type (a given out may be r or y)."""
+    return _residual("w4a8_moe_residual_norm", None, y, r, None, post_weight, gate, token_gate, r_scale, eps, out,
+                     None, None, None, None)
+
+
+def w4a8_moe_residual_norm_quant(y: torch.Tensor, r: torch.Tensor, next_weight: torch.Tensor,
+                                 post_weight: torch.Tensor | None = None, gate: torch.Tensor | None = None,
+                                 token_gate: torch.Tensor | None = None, r_scale: float = 1.0, eps: float = 1e-6,
+                                 out: torch.Tensor | None = None, xn: torch.Tensor | None = None,
+                                 qx: torch.Tensor | None = None, sx: torch.Tensor | None = None):
+    """w4a8_moe_residual_norm and w4a8_moe_norm_quant of its result (before that is rounded to r's type) with
+    next_weight, in one pass -> (out, xn, qx, sx)."""
+    return _residual("w4a8_moe_residual_norm_quant", _U8, y, r, next_weight, post_weight, gate, token_gate, r_scale,
+                     eps, out, xn, qx, sx, None)
+
+
+def w4a8_moe_residual_norm_quant_i8(y: torch.Tensor, r: torch.Tensor, next_weight: torch.Tensor,
+                                    post_weight: torch.Tensor | None = None, gate: torch.Tensor | None = None,
+                                    token_gate: torch.Tensor | None = None, r_scale: float = 1.0, eps: float = 1e-6,
+                                    out: torch.Tensor | None = None, xn: torch.Tensor | None = None,
+                                    qx: torch.Tensor | None = None, sx: torch.Tensor | None = None,
+                                    rowsum: torch.Tensor | None = None):
+    """The same with int8 codes, as w4a8_moe_norm_quant_i8."""
+    return _residual("w4a8_moe_residual_norm_quant_i8", _I8, y, r, next_weight, post_weight, gate, token_gate, r_scale,
+                     eps, out, xn, qx, sx, rowsum)
