@@ -1,126 +1,296 @@
 // Dense products in 8-bit integers and the gated feed-forward block on them (w4a8_block.h).
 //
-// One workgroup of four waves computes a tile of 128 rows x 128 weight rows (output
-// columns), each wave 64 x 64 of it in 16x16x64 INT8 products with int32 sums.  K goes in
-// steps of 128 bytes through two LDS slots, filled by loads straight into LDS.
+// One workgroup of kWM x kWN waves computes a tile of kBM rows x kBN weight rows (output
+// columns), in 16x16x64 INT8 products with int32 sums.  K goes in steps of 128 bytes through
+// two LDS slots, filled by loads straight into LDS one step ahead.
 #include "block.hpp"
 #include "gemm_common.hpp"
 #include "lds_dma.hpp"
 #include "row_codes.hpp"
 
+#include <type_traits>
+
 namespace w4a8 {
 
 namespace {
 
-constexpr int kBM = 128, kBN = 128, kBK = 128;
+constexpr int kBK = 128;             // K bytes of a step
 
+// Row r of a slot keeps its 16-byte chunk c at 16 (c ^ swz(r)): the operand reads (lane l: row
+// l % 16, chunk 2 (l / 16) + h of half h) are then free of bank conflicts.  Which K elements a
+// half takes does not matter, as both operands take the same.
 __device__ __forceinline__ int swz(int r) { return (r & 7) ^ ((r >> 3) & 1); }
 
-// kGated: the tile's columns are 64 gate rows and the 64 up rows of the same act columns, by
-// 16 in turn, and the result is act = silu(gate) up, fp32 [M][I]; otherwise y.
-template <bool kGated>
-__global__ __launch_bounds__(256) void dense_i8_kernel(const DenseArgs d, int64_t I, float* __restrict__ act) {
-  __shared__ __attribute__((aligned(16))) uint8_t sm[2][(kBM + kBN) * kBK];
+// a buffer resource in scalar registers (64-bit comparisons leave uniform values in vector ones)
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t uniform_rsrc(const void* base, int bytes) {
+  const uint64_t p = (uint64_t)base;
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((int)(uint32_t)p);
+  const uint32_t hi = __builtin_amdgcn_readfirstlane((int)(uint32_t)(p >> 32));
+  return buffer_rsrc(reinterpret_cast<const void*>(((uint64_t)hi << 32) | lo), (uint32_t)__builtin_amdgcn_readfirstlane(bytes));
+}
+
+enum Out : int { kOutF32 = 0, kOutBf16 = 1, kOutAct = 2 };
+
+// kOutAct: the tile's columns are 16 gate rows and the 16 up rows of the same act columns in
+// turn, and the result is act = silu(gate) up, fp32 [M][I]; otherwise y, with an addend (kAdd).
+template <int kBM, int kBN, int kWM, int kWN, int kOut, bool kAdd>
+__global__ __launch_bounds__(64 * kWM * kWN) void dense_i8_kernel(const DenseArgs d, int64_t I,
+                                                                  float* __restrict__ act, int mblocks, int nblocks) {
+  constexpr bool kGated = kOut == kOutAct;
+  constexpr int kWaves = kWM * kWN;
+  constexpr int WM = kBM / kWM, WN = kBN / kWN, FM = WM / 16, FN = WN / 16;
+  constexpr int kSlot = (kBM + kBN) * kBK;
+  constexpr int kALoads = kBM / 8 / kWaves, kWLoads = kBN / 8 / kWaves;    // instructions of 8 rows per wave
+  constexpr int kScaleBytes = 4 * (2 * kBN + kBM);                         // w_scale, bias, a_scale of a tile
+  extern __shared__ __attribute__((aligned(16))) uint8_t sm[];             // two slots, two tiles' scales
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int lr = lane & 15, lq = lane >> 4;
-  const int64_t m0 = (int64_t)blockIdx.y * kBM, n0 = (int64_t)blockIdx.x * kBN;
-  const int K = (int)d.K;
-  const int rows = (int)min((int64_t)kBM, d.M - m0);
-  const int cols = (int)min((int64_t)kBN, d.N - n0);
-  const __amdgpu_buffer_rsrc_t ra = buffer_rsrc(d.a + m0 * d.ld_a, (uint32_t)((rows - 1) * d.ld_a + K));
-  // weight rows: 64 gate and 64 up rows, or 128 in a row
-  const int64_t c0 = kGated ? n0 / 2 : n0;
-  const int wrows = kGated ? cols / 2 : cols;
-  const __amdgpu_buffer_rsrc_t rg = buffer_rsrc(d.w + c0 * K, (uint32_t)(wrows * K));
-  const __amdgpu_buffer_rsrc_t ru = buffer_rsrc(d.w + ((kGated ? I : 0) + c0) * K, (uint32_t)(wrows * K));
+  const int K = (int)d.K, steps = (K + kBK - 1) / kBK;
+  const int total = mblocks * nblocks;
 
-  const int steps = (K + kBK - 1) / kBK;
-  // an instruction loads 8 rows of 128 bytes; wave w loads the rows 32 w .. +31 of each side.  A row or chunk
-  // past the operand is never read (its offset is past the resource) and never matters: rows past the end give
-  // outputs that are not stored, bytes past K are taken out of a below.
-  auto stage = [&](int s, int kt) {
+  // Loads of 8 rows of 128 bytes.  A row or chunk past the operand is never read (its offset is
+  // past the resource) and never matters: rows past the end give outputs that are not stored,
+  // bytes past K are taken out of a in the last step.
+  uint32_t aoff[kALoads], woff[kWLoads];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int r = 32 * wave + 8 * q + (lane >> 3);
-      const int c = (lane & 7) ^ swz(r);
-      dma16(ra, (uint32_t)(r * (int)d.ld_a + 16 * c), (uint32_t)(kt * kBK), &sm[s][(32 * wave + 8 * q) * kBK]);
-    }
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int r = 32 * wave + 8 * q + (lane >> 3);
-      const int c = (lane & 7) ^ swz(r);
-      const int wr = kGated ? 16 * (r >> 5) + (r & 15) : r;
-      if (kGated && ((2 * wave + (q >> 1)) & 1))
-        dma16(ru, (uint32_t)(wr * K + 16 * c), (uint32_t)(kt * kBK), &sm[s][(kBM + 32 * wave + 8 * q) * kBK]);
-      else
-        dma16(rg, (uint32_t)(wr * K + 16 * c), (uint32_t)(kt * kBK), &sm[s][(kBM + 32 * wave + 8 * q) * kBK]);
-    }
-  };
-  const int wm = 64 * (wave >> 1), wn = 64 * (wave & 1);
-  i32x4 acc[4][4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
-  stage(0, 0);
-  for (int kt = 0; kt < steps; ++kt) {
-    const int s = kt & 1;
-    __builtin_amdgcn_s_waitcnt(0x0F70);                      // vmcnt(0): this step's loads
-    barrier_loads_in_flight();
-    if (kt + 1 < steps) stage(s ^ 1, kt + 1);                // (its readers passed the barrier)
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      i32x4 a[4], b[4];
-      const uint32_t off = 16u * (uint32_t)((4 * h + lq) ^ swz(lr));
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        a[i] = lds_load<i32x4>(&sm[s][(wm + 16 * i + lr) * kBK + off]);
-        b[i] = lds_load<i32x4>(&sm[s][(kBM + wn + 16 * i + lr) * kBK + off]);
-      }
-      if (kt * kBK + 64 * h + 16 * lq >= K) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) a[i] = i32x4{0, 0, 0, 0};
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = mfma_i8_16x16x64(a[i], b[j], acc[i][j]);
-    }
-    __builtin_amdgcn_s_waitcnt(0xC07F);                      // lgkmcnt(0)
+  for (int q = 0; q < kALoads; ++q) {
+    const int r = 8 * (kALoads * wave + q) + (lane >> 3);
+    aoff[q] = (uint32_t)(r * (int)d.ld_a + 16 * ((lane & 7) ^ swz(r)));
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int q = 0; q < kWLoads; ++q) {
+    const int r = 8 * (kWLoads * wave + q) + (lane >> 3);
+    const int wr = kGated ? 16 * (r >> 5) + (r & 15) : r;
+    woff[q] = (uint32_t)(wr * K + 16 * ((lane & 7) ^ swz(r)));
+  }
+  static_assert(kWLoads % 4 == 0 || !kGated, "the wave's loads go two by two over gate and up rows");
+  __amdgpu_buffer_rsrc_t ra, rw0, rw1;
+  int64_t m0 = 0, n0 = 0;
+
+  // Tile t of the workgroups' order: workgroups go to the 8 XCDs in turn, and each XCD takes a
+  // window of neighbouring tiles.  The tiles go in groups of 4 row blocks that walk the column
+  // blocks side by side, so that 32 tiles of an XCD at a time share 4 row and 8 column blocks
+  // in its L2.
+  auto point = [&](int t, int par) {
+    const int per = 4 * nblocks, group = t / per, gm = min(4, mblocks - 4 * group), in = t - group * per;
+    m0 = (int64_t)(4 * group + in % gm) * kBM, n0 = (int64_t)(in / gm) * kBN;
+    const int rows = (int)min((int64_t)kBM, d.M - m0), cols = (int)min((int64_t)kBN, d.N - n0);
+    ra = uniform_rsrc(d.a + m0 * d.ld_a, (rows - 1) * (int)d.ld_a + K);
+    const int64_t c0 = kGated ? n0 / 2 : n0;
+    const int wrows = kGated ? cols / 2 : cols;
+    rw0 = uniform_rsrc(d.w + c0 * K, wrows * K);
+    if (kGated) rw1 = uniform_rsrc(d.w + (I + c0) * K, wrows * K);
+    // scales of the tile: 64 words to an instruction
+    uint8_t* sc = &sm[2 * kSlot + par * kScaleBytes];
+    for (int c = wave; c < kBN / 64; c += kWaves) {
+      // gated: the gate and up rows 32 c .. +31 of the tile's act columns, by 16
+      const uint32_t o = kGated ? (uint32_t)(32 * c + 16 * (lq >> 1) + lr + (lq & 1) * (int)I) * 4u
+                                : (uint32_t)(64 * c + lane) * 4u;
+      const int bytes = kGated ? (int)(I + wrows) * 4 : cols * 4;
+      dma4(uniform_rsrc(d.w_scale + c0, bytes), o, 0, sc + 256 * c);
+      if (!kGated && d.bias) dma4(uniform_rsrc(d.bias + n0, cols * 4), o, 0, sc + 4 * kBN + 256 * c);
+    }
+    for (int c = wave; c < kBM / 64; c += kWaves)
+      dma4(uniform_rsrc(d.a_scale + m0, rows * 4), (uint32_t)(64 * c + lane) * 4u, 0, sc + 8 * kBN + 256 * c);
+  };
+  constexpr int kLoads = kALoads + kWLoads;
+  auto load = [&](int s, int kt, int q) {                     // load q of the wave's kLoads of step kt
+    const uint32_t k = (uint32_t)(kt * kBK);
+    if (q < kALoads) {
+      dma16(ra, aoff[q], k, &sm[s * kSlot + 8 * (kALoads * wave + q) * kBK]);
+    } else {
+      const int u = q - kALoads;
+      uint8_t* to = &sm[s * kSlot + (kBM + 8 * (kWLoads * wave + u)) * kBK];
+      if (kGated && ((u >> 1) & 1)) dma16(rw1, woff[u], k, to);
+      else dma16(rw0, woff[u], k, to);
+    }
+  };
+  // the first loads of a tile: step 0's, and of step 1 those that a step issues for the step
+  // after the next one
+  constexpr int kAhead = 4, kPerRegion = (kLoads + 2 * kAhead - 1) / (2 * kAhead), kEarly = kAhead * kPerRegion;
+  auto begin = [&]() {
 #pragma unroll
-    for (int v = 0; v < 4; ++v) {
-      const int64_t m = m0 + wm + 16 * i + 4 * lq + v;
-      if (m >= d.M) continue;
-      const float sa = d.a_scale[m];
-      if constexpr (kGated) {
+    for (int q = 0; q < kLoads; ++q) load(0, 0, q);
+    if (steps > 1) {
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int64_t n = c0 + wn / 2 + 16 * j + lr;
-          if (n < I) {
-            const float g = (float)acc[i][2 * j][v] * sa * d.w_scale[n];
-            const float u = (float)acc[i][2 * j + 1][v] * sa * d.w_scale[I + n];
-            act[m * I + n] = silu_mul(g, u);
+      for (int q = 0; q < kEarly; ++q) load(1, 1, q);
+    }
+  };
+  const int wm = WM * (wave / kWN), wn = WN * (wave % kWN);
+  const int fs = swz(lr);
+
+  const int grid = gridDim.x;
+  const int window = (grid + 7) >> 3;
+  const int first = (blockIdx.x & 7) * window + (blockIdx.x >> 3);    // (grid % 8 == 0, or one round)
+  const int start = grid % 8 == 0 ? first : (int)blockIdx.x;
+  int par = 0;
+  if (!kGated && !d.bias) {                                    // a bias of zero
+    for (int c = tid; c < 2 * kBN; c += 64 * kWaves)
+      reinterpret_cast<float*>(&sm[2 * kSlot + (c / kBN) * kScaleBytes])[kBN + c % kBN] = 0.0f;
+    __builtin_amdgcn_s_waitcnt(0xC07F);                        // (read after the barriers of the first tile)
+  }
+  point(start, par);
+  begin();
+  for (int t = start; t < total; t += grid, par ^= 1) {
+    i32x4 acc[FM][FN];
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+      for (int j = 0; j < FN; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
+    // A step is 2 FM regions: the products of one block of 16 rows and half a step's K with the
+    // FN column blocks.  Region r reads the row block of region r + kAhead, and in the last
+    // kAhead regions of a half the column blocks of the next.  Before region kLast the wave's
+    // reads of the slot are done and the loads of the next step (in the other slot) have landed;
+    // one barrier, and from there on the next step's operands are read, at the pace of the
+    // others, and the slot is filled again.
+    constexpr int kRegions = 2 * FM, kLast = kRegions - kAhead, kPerA = (FN + kAhead - 1) / kAhead;
+    static_assert(FM % kAhead == 0 && kRegions % 8 == 0, "regions");
+    i32x4 a[8], b[2][FN];
+    auto read_a = [&](int s, int r) {
+      a[r & 7] = lds_load<i32x4>(&sm[s * kSlot + (wm + lr + 16 * (r % FM)) * kBK + 16 * ((2 * lq + r / FM) ^ fs)]);
+    };
+    auto read_b = [&](int s, int h, int j) {
+      b[h][j] = lds_load<i32x4>(&sm[s * kSlot + (kBM + wn + lr + 16 * j) * kBK + 16 * ((2 * lq + h) ^ fs)]);
+    };
+    __builtin_amdgcn_s_waitcnt(0x0F70);
+    barrier_loads_in_flight();
+#pragma unroll
+    for (int r = 0; r < kAhead; ++r) {
+      read_a(0, r);
+#pragma unroll
+      for (int j = 0; j < FN; ++j)
+        if (j / kPerA == r) read_b(0, 0, j);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    auto step = [&](auto Last_, int kt) {
+      constexpr bool kTail = decltype(Last_)::value;          // the last step: bytes past K are zeros
+      const int s = kt & 1;
+#pragma unroll
+      for (int r = 0; r < kRegions; ++r) {
+        const int h = r / FM, i = r % FM;
+        if (r == kLast) {
+          __builtin_amdgcn_s_waitcnt(kTail ? 0xC07F : 0x0070);  // lgkmcnt(0), and vmcnt(0)
+          barrier_loads_in_flight();
+          if (kTail && t + grid < total) {                    // the next tile's first loads
+            point(t + grid, par ^ 1);
+            begin();
           }
         }
-      } else {
+        // loads of the next step (regions 0 ..), and from the barrier on of the one after it
+        if constexpr (!kTail) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int64_t n = n0 + wn + 16 * j + lr;
-          if (n >= d.N) continue;
-          float y = (float)acc[i][j][v] * sa * d.w_scale[n];
-          if (d.bias) y += d.bias[n];
-          const int64_t o = m * d.N + n;
-          if (d.y_bf16) {
-            if (d.add) y += __uint_as_float((uint32_t)static_cast<const uint16_t*>(d.add)[o] << 16);
-            static_cast<uint16_t*>(d.y)[o] = __builtin_bit_cast(uint16_t, (__bf16)y);
-          } else {
-            if (d.add) y += static_cast<const float*>(d.add)[o];
-            static_cast<float*>(d.y)[o] = y;
+          for (int q = 0; q < kLoads; ++q) {
+            if (r < kLast && q >= kEarly && (q - kEarly) / kPerRegion == r) load(s ^ 1, kt + 1, q);
+            if (r >= kLast && q < kEarly && q / kPerRegion == r - kLast && kt + 2 < steps) load(s, kt + 2, q);
           }
         }
+        if (r < kLast) read_a(s, r + kAhead);
+        else if (!kTail) read_a(s ^ 1, r - kLast);
+#pragma unroll
+        for (int j = 0; j < FN; ++j) {
+          if (r >= FM - kAhead && r < FM && j / kPerA == r - (FM - kAhead)) read_b(s, 1, j);
+          if (!kTail && r >= kLast && j / kPerA == r - kLast) read_b(s ^ 1, 0, j);
+        }
+        if (kTail && kt * kBK + 16 * (2 * lq + h) >= K) a[r & 7] = i32x4{0, 0, 0, 0};
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int j = 0; j < FN; ++j) acc[i][j] = mfma_i8_16x16x64(b[h][j], a[r & 7], acc[i][j]);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    };
+    for (int kt = 0; kt + 1 < steps; ++kt) step(std::false_type{}, kt);
+    const int64_t tm0 = m0, tn0 = n0;
+    step(std::true_type{}, steps - 1);
+    // ---- epilogue: D lane holds row lr of its row block, outputs 4 lq .. +3 of its column block
+    // (lane roles taken afresh: addresses built from them are not kept through the products)
+    int lr = lane & 15, lq = lane >> 4;
+    asm volatile("" : "+v"(lr), "+v"(lq));
+    const float* sc = reinterpret_cast<const float*>(&sm[2 * kSlot + par * kScaleBytes]) + wn + 4 * lq;
+    const float* as = reinterpret_cast<const float*>(&sm[2 * kSlot + par * kScaleBytes]) + 2 * kBN + wm + lr;
+    const int mleft = (int)min(d.M - tm0 - wm, (int64_t)WM);  // rows of the wave
+    const int nleft = (int)min(d.N - tn0 - wn, (int64_t)WN);  // columns of the wave
+    const int64_t row0 = tm0 + wm + lr;
+    float sa[FM];
+#pragma unroll
+    for (int i = 0; i < FM; ++i) sa[i] = as[16 * i];
+#pragma unroll
+    for (int j = 0; j < FN; j += 2) {                          // two column blocks: gate and up, or 32 outputs
+      f32x4 ws[2], bs[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        ws[e] = lds_load<f32x4>(sc + 16 * (j + e));
+        if constexpr (!kGated) bs[e] = lds_load<f32x4>(sc + kBN + 16 * (j + e));
+      }
+      const bool whole = 16 * j + 32 <= nleft;                 // (the same for the whole wave)
+#pragma unroll
+      for (int i = 0; i < FM; ++i) {
+        const bool live = 16 * i + lr < mleft;
+        if constexpr (kGated) {
+          f32x4 o;
+#pragma unroll
+          for (int v = 0; v < 4; ++v)
+            o[v] = silu_mul((float)acc[i][j][v] * sa[i] * ws[0][v], (float)acc[i][j + 1][v] * sa[i] * ws[1][v]);
+          // (a block of 32 columns is all inside the 2 I, or none)
+          if (live && whole)
+            *reinterpret_cast<f32x4*>(act + (row0 + 16 * i) * I + (tn0 + wn) / 2 + 8 * j + 4 * lq) = o;
+        } else {
+          constexpr bool kBf16 = kOut == kOutBf16;
+          using E = std::conditional_t<kBf16, uint16_t, float>;
+          const int64_t at = (row0 + 16 * i) * d.N + tn0 + wn + 16 * j;
+          const E* add = static_cast<const E*>(d.add) + at;
+          E* y = static_cast<E*>(d.y) + at;
+          f32x4 o[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int v = 0; v < 4; ++v) o[e][v] = (float)acc[i][j + e][v] * sa[i] * ws[e][v] + bs[e][v];
+          if (whole) {
+            if (kAdd && live) {
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                if constexpr (kBf16) {
+                  uint2 w;
+                  __builtin_memcpy(&w, add + 16 * e + 4 * lq, 8);
+                  o[e][0] += bf16_lo(w.x), o[e][1] += bf16_hi(w.x), o[e][2] += bf16_lo(w.y), o[e][3] += bf16_hi(w.y);
+                } else {
+                  f32x4 w;
+                  __builtin_memcpy(&w, add + 16 * e + 4 * lq, 16);
+#pragma unroll
+                  for (int v = 0; v < 4; ++v) o[e][v] += w[v];
+                }
+              }
+            }
+            if constexpr (kBf16) {
+              // neighbouring groups of 16 lanes trade halves: 8 outputs of one block each
+              const auto s0 = __builtin_amdgcn_permlane16_swap(bf16_pair(o[0][0], o[0][1]), bf16_pair(o[1][0], o[1][1]),
+                                                               false, false);
+              const auto s1 = __builtin_amdgcn_permlane16_swap(bf16_pair(o[0][2], o[0][3]), bf16_pair(o[1][2], o[1][3]),
+                                                               false, false);
+              const uint4 v = make_uint4(s0[0], s1[0], s0[1], s1[1]);
+              if (live) __builtin_memcpy(y + 16 * (lq & 1) + 8 * (lq >> 1), &v, 16);
+            } else if (live) {
+#pragma unroll
+              for (int e = 0; e < 2; ++e) __builtin_memcpy(y + 16 * e + 4 * lq, &o[e], 16);
+            }
+          } else if (live) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+              for (int v = 0; v < 4; ++v) {
+                const int c = 16 * e + 4 * lq + v;
+                if (16 * j + c < nleft) {
+                  float r = o[e][v];
+                  if constexpr (kBf16) {
+                    if (kAdd) r += __uint_as_float((uint32_t)add[c] << 16);
+                    y[c] = __builtin_bit_cast(uint16_t, (__bf16)r);
+                  } else {
+                    y[c] = kAdd ? r + add[c] : r;
+                  }
+                }
+              }
+          }
+        }
+        __builtin_amdgcn_sched_barrier(0);                     // one row block at a time: few temporaries
       }
     }
   }
@@ -158,14 +328,39 @@ __global__ __launch_bounds__(256) void act_quant_kernel(const float* __restrict_
   if (threadIdx.x == 0) s[blockIdx.x] = scale;
 }
 
+template <int kBM, int kBN, int kWM, int kWN, int kOut, bool kAdd>
+hipError_t launch_tiles(const DenseArgs& d, int64_t I, float* act, int per_cu, hipStream_t stream) {
+  const int64_t mb = (d.M + kBM - 1) / kBM, nb = (d.N + kBN - 1) / kBN;
+  auto kernel = dense_i8_kernel<kBM, kBN, kWM, kWN, kOut, kAdd>;
+  constexpr int kLds = 2 * (kBM + kBN) * kBK + 2 * 4 * (2 * kBN + kBM);
+  if constexpr (kLds > 65536) {
+    static const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                                                    hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
+    if (e != hipSuccess) return e;
+  }
+  const int64_t slots = 256 * per_cu, tiles = mb * nb;
+  hipLaunchKernelGGL(kernel, dim3((unsigned)(tiles < slots ? tiles : slots)), dim3(64 * kWM * kWN), kLds, stream, d, I,
+                     act, (int)mb, (int)nb);
+  return hipGetLastError();
+}
+
+template <int kOut, bool kAdd>
+hipError_t launch_product(const DenseArgs& d, int64_t I, float* act, hipStream_t stream) {
+  const int64_t big = ((d.M + 255) / 256) * ((d.N + 255) / 256);
+  if (d.M > 128 && big >= 192) return launch_tiles<256, 256, 2, 4, kOut, kAdd>(d, I, act, 1, stream);
+  return launch_tiles<128, 128, 2, 2, kOut, kAdd>(d, I, act, 2, stream);
+}
+
 }  // namespace
 
 int64_t dense_i8_workspace_bytes(int64_t, int64_t, int64_t) { return 0; }
 
 hipError_t launch_dense_i8(const DenseArgs& d, hipStream_t stream) {
-  const dim3 grid((unsigned)((d.N + kBN - 1) / kBN), (unsigned)((d.M + kBM - 1) / kBM));
-  hipLaunchKernelGGL(dense_i8_kernel<false>, grid, dim3(256), 0, stream, d, (int64_t)0, (float*)nullptr);
-  return hipGetLastError();
+  if (d.y_bf16)
+    return d.add ? launch_product<kOutBf16, true>(d, 0, nullptr, stream)
+                 : launch_product<kOutBf16, false>(d, 0, nullptr, stream);
+  return d.add ? launch_product<kOutF32, true>(d, 0, nullptr, stream)
+               : launch_product<kOutF32, false>(d, 0, nullptr, stream);
 }
 
 // act fp32 [M][I], codes [M][I], scales [M]
@@ -175,9 +370,8 @@ hipError_t launch_mlp_i8(const MlpArgs& p, hipStream_t stream) {
   float* act = static_cast<float*>(p.workspace);
   uint8_t* q = reinterpret_cast<uint8_t*>(act + p.M * p.I);
   float* s = reinterpret_cast<float*>(q + p.M * p.I);
-  DenseArgs up{p.a, p.a_scale, p.M, p.H, p.ld_a, p.w13, p.s13, nullptr, 2 * p.I, nullptr, nullptr, 0, nullptr};
-  const dim3 grid((unsigned)((2 * p.I + kBN - 1) / kBN), (unsigned)((p.M + kBM - 1) / kBM));
-  hipLaunchKernelGGL(dense_i8_kernel<true>, grid, dim3(256), 0, stream, up, p.I, act);
+  const DenseArgs up{p.a, p.a_scale, p.M, p.H, p.ld_a, p.w13, p.s13, nullptr, 2 * p.I, nullptr, nullptr, 0, nullptr};
+  if (const hipError_t e = launch_product<kOutAct, false>(up, p.I, act, stream); e != hipSuccess) return e;
   hipLaunchKernelGGL(act_quant_kernel, dim3((unsigned)p.M), dim3(256), 0, stream, act, p.I, q, s);
   const DenseArgs down{reinterpret_cast<int8_t*>(q), s, p.M, p.I, p.I, p.w2, p.s2, nullptr, p.H, p.add, p.y, p.y_bf16,
                        nullptr};

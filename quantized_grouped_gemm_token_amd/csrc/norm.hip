@@ -70,9 +70,6 @@ __device__ __forceinline__ void load_vector(const float* v, int chunk, float (&f
   const float4 a = reinterpret_cast<const float4*>(v)[2 * chunk], b = reinterpret_cast<const float4*>(v)[2 * chunk + 1];
   f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
 }
-__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
-  return (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)lo) | ((uint32_t)__builtin_bit_cast(uint16_t, (__bf16)hi) << 16);
-}
 __device__ __forceinline__ uint4 bf16x8(const float (&f)[8]) {
   return make_uint4(bf16_pair(f[0], f[1]), bf16_pair(f[2], f[3]), bf16_pair(f[4], f[5]), bf16_pair(f[6], f[7]));
 }
