@@ -46,6 +46,14 @@ struct MlpArgs {
 int64_t mlp_i8_workspace_bytes(int64_t M, int64_t H, int64_t I);
 hipError_t launch_mlp_i8(const MlpArgs& m, hipStream_t stream);
 
+// the same for 1 to 16 rows (dense_few.hip); the gated product (d: w13, N = 2 I) leaves act [M][I] and
+// pmax [M][I / 8], bit patterns of the maxima of 8 columns of |act|; the down product (d: w2, K = I, a
+// unused) quantizes act itself
+bool dense_few_fits(int64_t M, int64_t ld_a);
+hipError_t launch_dense_few(const DenseArgs& d, hipStream_t stream);
+hipError_t launch_gated_few(const DenseArgs& d, int64_t I, float* act, uint32_t* pmax, hipStream_t stream);
+hipError_t launch_down_few(const DenseArgs& d, float* act, uint32_t* pmax, hipStream_t stream);
+
 // norms before and after a block (norm.hip).  Without r: the norm of x.  With it: out from x
 // (the block's result) and r, and, where `weight` is set, the norm of out.
 constexpr int64_t kNormMaxH = 32768;     // 1024 threads, 4 chunks of 8 values each

@@ -29,11 +29,15 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t uniform_rsrc(const void* base,
   return buffer_rsrc(reinterpret_cast<const void*>(((uint64_t)hi << 32) | lo), (uint32_t)__builtin_amdgcn_readfirstlane(bytes));
 }
 
+// what a tile leaves: y (fp32 or bf16), or act of the gated product
 enum Out : int { kOutF32 = 0, kOutBf16 = 1, kOutAct = 2 };
+
+// s_waitcnt's field for at most n vector memory operations in flight (n < 64), with lgkmcnt(l)
+constexpr int vm_wait(int n, int l) { return (n & 15) | ((n >> 4) << 14) | 0x70 | (l << 8); }
 
 // kOutAct: the tile's columns are 16 gate rows and the 16 up rows of the same act columns in
 // turn, and the result is act = silu(gate) up, fp32 [M][I]; otherwise y, with an addend (kAdd).
-template <int kBM, int kBN, int kWM, int kWN, int kOut, bool kAdd>
+template <int kBM, int kBN, int kWM, int kWN, int kSlots, int kOut, bool kAdd>
 __global__ __launch_bounds__(64 * kWM * kWN) void dense_i8_kernel(const DenseArgs d, int64_t I,
                                                                   float* __restrict__ act, int mblocks, int nblocks) {
   constexpr bool kGated = kOut == kOutAct;
@@ -42,7 +46,7 @@ __global__ __launch_bounds__(64 * kWM * kWN) void dense_i8_kernel(const DenseArg
   constexpr int kSlot = (kBM + kBN) * kBK;
   constexpr int kALoads = kBM / 8 / kWaves, kWLoads = kBN / 8 / kWaves;    // instructions of 8 rows per wave
   constexpr int kScaleBytes = 4 * (2 * kBN + kBM);                         // w_scale, bias, a_scale of a tile
-  extern __shared__ __attribute__((aligned(16))) uint8_t sm[];             // two slots, two tiles' scales
+  extern __shared__ __attribute__((aligned(16))) uint8_t sm[];             // the slots, two tiles' scales
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int lr = lane & 15, lq = lane >> 4;
   const int K = (int)d.K, steps = (K + kBK - 1) / kBK;
@@ -63,7 +67,9 @@ __global__ __launch_bounds__(64 * kWM * kWN) void dense_i8_kernel(const DenseArg
     const int wr = kGated ? 16 * (r >> 5) + (r & 15) : r;
     woff[q] = (uint32_t)(wr * K + 16 * ((lane & 7) ^ swz(r)));
   }
-  static_assert(kWLoads % 4 == 0 || !kGated, "the wave's loads go two by two over gate and up rows");
+  // gated: a wave's loads go two by two over gate and up rows, or are all of one kind
+  constexpr bool kBoth = kGated && kWLoads % 4 == 0;
+  static_assert(kBoth || !kGated || kWLoads <= 2, "gate and up rows");
   __amdgpu_buffer_rsrc_t ra, rw0, rw1;
   int64_t m0 = 0, n0 = 0;
 
@@ -78,10 +84,11 @@ __global__ __launch_bounds__(64 * kWM * kWN) void dense_i8_kernel(const DenseArg
     ra = uniform_rsrc(d.a + m0 * d.ld_a, (rows - 1) * (int)d.ld_a + K);
     const int64_t c0 = kGated ? n0 / 2 : n0;
     const int wrows = kGated ? cols / 2 : cols;
-    rw0 = uniform_rsrc(d.w + c0 * K, wrows * K);
-    if (kGated) rw1 = uniform_rsrc(d.w + (I + c0) * K, wrows * K);
+    const bool up = kGated && !kBoth && ((kWLoads * wave) >> 1) % 2;
+    rw0 = uniform_rsrc(d.w + ((up ? I : 0) + c0) * K, wrows * K);
+    if (kBoth) rw1 = uniform_rsrc(d.w + (I + c0) * K, wrows * K);
     // scales of the tile: 64 words to an instruction
-    uint8_t* sc = &sm[2 * kSlot + par * kScaleBytes];
+    uint8_t* sc = &sm[kSlots * kSlot + par * kScaleBytes];
     for (int c = wave; c < kBN / 64; c += kWaves) {
       // gated: the gate and up rows 32 c .. +31 of the tile's act columns, by 16
       const uint32_t o = kGated ? (uint32_t)(32 * c + 16 * (lq >> 1) + lr + (lq & 1) * (int)I) * 4u
@@ -94,26 +101,28 @@ __global__ __launch_bounds__(64 * kWM * kWN) void dense_i8_kernel(const DenseArg
       dma4(uniform_rsrc(d.a_scale + m0, rows * 4), (uint32_t)(64 * c + lane) * 4u, 0, sc + 8 * kBN + 256 * c);
   };
   constexpr int kLoads = kALoads + kWLoads;
-  auto load = [&](int s, int kt, int q) {                     // load q of the wave's kLoads of step kt
+  auto load = [&](int kt, int q) {                            // load q of the wave's kLoads of step kt
     const uint32_t k = (uint32_t)(kt * kBK);
+    uint8_t* slot = &sm[(kt % kSlots) * kSlot];
     if (q < kALoads) {
-      dma16(ra, aoff[q], k, &sm[s * kSlot + 8 * (kALoads * wave + q) * kBK]);
+      dma16(ra, aoff[q], k, slot + 8 * (kALoads * wave + q) * kBK);
     } else {
       const int u = q - kALoads;
-      uint8_t* to = &sm[s * kSlot + (kBM + 8 * (kWLoads * wave + u)) * kBK];
-      if (kGated && ((u >> 1) & 1)) dma16(rw1, woff[u], k, to);
+      uint8_t* to = slot + (kBM + 8 * (kWLoads * wave + u)) * kBK;
+      if (kBoth && ((u >> 1) & 1)) dma16(rw1, woff[u], k, to);
       else dma16(rw0, woff[u], k, to);
     }
   };
-  // the first loads of a tile: step 0's, and of step 1 those that a step issues for the step
-  // after the next one
-  constexpr int kAhead = 4, kPerRegion = (kLoads + 2 * kAhead - 1) / (2 * kAhead), kEarly = kAhead * kPerRegion;
+  // The first loads of a tile: those that the steps before would have issued.  A step kt issues
+  // the rest of step kt + kSlots - 1, and from its barrier on the first kEarly of step kt + kSlots.
+  constexpr int kAhead = FM < 4 ? FM : 4, kPerRegion = (kLoads + 2 * kAhead - 1) / (2 * kAhead), kEarly = kAhead * kPerRegion;
   auto begin = [&]() {
+    for (int kt = 0; kt < min(kSlots - 1, steps); ++kt)
 #pragma unroll
-    for (int q = 0; q < kLoads; ++q) load(0, 0, q);
-    if (steps > 1) {
+      for (int q = 0; q < kLoads; ++q) load(kt, q);
+    if (kSlots - 1 < steps) {
 #pragma unroll
-      for (int q = 0; q < kEarly; ++q) load(1, 1, q);
+      for (int q = 0; q < kEarly; ++q) load(kSlots - 1, q);
     }
   };
   const int wm = WM * (wave / kWN), wn = WN * (wave % kWN);
@@ -126,7 +135,7 @@ __global__ __launch_bounds__(64 * kWM * kWN) void dense_i8_kernel(const DenseArg
   int par = 0;
   if (!kGated && !d.bias) {                                    // a bias of zero
     for (int c = tid; c < 2 * kBN; c += 64 * kWaves)
-      reinterpret_cast<float*>(&sm[2 * kSlot + (c / kBN) * kScaleBytes])[kBN + c % kBN] = 0.0f;
+      reinterpret_cast<float*>(&sm[kSlots * kSlot + (c / kBN) * kScaleBytes])[kBN + c % kBN] = 0.0f;
     __builtin_amdgcn_s_waitcnt(0xC07F);                        // (read after the barriers of the first tile)
   }
   point(start, par);
@@ -144,15 +153,18 @@ __global__ __launch_bounds__(64 * kWM * kWN) void dense_i8_kernel(const DenseArg
     // one barrier, and from there on the next step's operands are read, at the pace of the
     // others, and the slot is filled again.
     constexpr int kRegions = 2 * FM, kLast = kRegions - kAhead, kPerA = (FN + kAhead - 1) / kAhead;
-    static_assert(FM % kAhead == 0 && kRegions % 8 == 0, "regions");
-    i32x4 a[8], b[2][FN];
+    constexpr int kHeld = kRegions < 8 ? kRegions : 8;
+    static_assert(FM % kAhead == 0 && kRegions % kHeld == 0 && FN % 2 == 0, "regions");
+    i32x4 a[kHeld], b[2][FN];
     auto read_a = [&](int s, int r) {
-      a[r & 7] = lds_load<i32x4>(&sm[s * kSlot + (wm + lr + 16 * (r % FM)) * kBK + 16 * ((2 * lq + r / FM) ^ fs)]);
+      a[r % kHeld] = lds_load<i32x4>(&sm[s * kSlot + (wm + lr + 16 * (r % FM)) * kBK + 16 * ((2 * lq + r / FM) ^ fs)]);
     };
     auto read_b = [&](int s, int h, int j) {
       b[h][j] = lds_load<i32x4>(&sm[s * kSlot + (kBM + wn + lr + 16 * j) * kBK + 16 * ((2 * lq + h) ^ fs)]);
     };
-    __builtin_amdgcn_s_waitcnt(0x0F70);
+    // step 0 has landed when only the loads after it are in flight (and stores of the last tile)
+    if (steps >= kSlots) __builtin_amdgcn_s_waitcnt(vm_wait((kSlots - 2) * kLoads + kEarly, 15));
+    else __builtin_amdgcn_s_waitcnt(vm_wait(0, 15));
     barrier_loads_in_flight();
 #pragma unroll
     for (int r = 0; r < kAhead; ++r) {
@@ -162,51 +174,55 @@ __global__ __launch_bounds__(64 * kWM * kWN) void dense_i8_kernel(const DenseArg
         if (j / kPerA == r) read_b(0, 0, j);
     }
     __builtin_amdgcn_sched_barrier(0);
-    auto step = [&](auto Last_, int kt) {
-      constexpr bool kTail = decltype(Last_)::value;          // the last step: bytes past K are zeros
-      const int s = kt & 1;
+    const int64_t tm0 = m0, tn0 = n0;                         // (the last step points to the next tile)
+    // kPhase: 0 while a step issues loads of both later steps, 1 the one that issues the last
+    // loads, 2 those after it, 3 the tile's last step (where bytes past K are zeros)
+    auto step = [&](auto Phase_, int kt) {
+      constexpr int kPhase = decltype(Phase_)::value;
+      const int s = kt % kSlots, next = (kt + 1) % kSlots;
 #pragma unroll
       for (int r = 0; r < kRegions; ++r) {
         const int h = r / FM, i = r % FM;
         if (r == kLast) {
-          __builtin_amdgcn_s_waitcnt(kTail ? 0xC07F : 0x0070);  // lgkmcnt(0), and vmcnt(0)
+          // (of the steps after the next one, all loads may be in flight)
+          __builtin_amdgcn_s_waitcnt(vm_wait(kPhase == 3 ? 63 : kPhase == 2 ? 0 : (kSlots - 2) * kLoads, 0));
           barrier_loads_in_flight();
-          if (kTail && t + grid < total) {                    // the next tile's first loads
+          if (kPhase == 3 && t + grid < total) {              // the next tile's first loads
             point(t + grid, par ^ 1);
             begin();
           }
         }
-        // loads of the next step (regions 0 ..), and from the barrier on of the one after it
-        if constexpr (!kTail) {
 #pragma unroll
-          for (int q = 0; q < kLoads; ++q) {
-            if (r < kLast && q >= kEarly && (q - kEarly) / kPerRegion == r) load(s ^ 1, kt + 1, q);
-            if (r >= kLast && q < kEarly && q / kPerRegion == r - kLast && kt + 2 < steps) load(s, kt + 2, q);
-          }
+        for (int q = 0; q < kLoads; ++q) {
+          if (kPhase < 2 && r < kLast && q >= kEarly && (q - kEarly) / kPerRegion == r) load(kt + kSlots - 1, q);
+          if (kPhase < 1 && r >= kLast && q < kEarly && q / kPerRegion == r - kLast) load(kt + kSlots, q);
         }
         if (r < kLast) read_a(s, r + kAhead);
-        else if (!kTail) read_a(s ^ 1, r - kLast);
+        else if (kPhase < 3) read_a(next, r - kLast);
 #pragma unroll
         for (int j = 0; j < FN; ++j) {
           if (r >= FM - kAhead && r < FM && j / kPerA == r - (FM - kAhead)) read_b(s, 1, j);
-          if (!kTail && r >= kLast && j / kPerA == r - kLast) read_b(s ^ 1, 0, j);
+          if (kPhase < 3 && r >= kLast && j / kPerA == r - kLast) read_b(next, 0, j);
         }
-        if (kTail && kt * kBK + 16 * (2 * lq + h) >= K) a[r & 7] = i32x4{0, 0, 0, 0};
+        if (kPhase == 3 && kt * kBK + 16 * (2 * lq + h) >= K) a[r % kHeld] = i32x4{0, 0, 0, 0};
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int j = 0; j < FN; ++j) acc[i][j] = mfma_i8_16x16x64(b[h][j], a[r & 7], acc[i][j]);
+        for (int j = 0; j < FN; ++j) acc[i][j] = mfma_i8_16x16x64(b[h][j], a[r % kHeld], acc[i][j]);
         __builtin_amdgcn_sched_barrier(0);
       }
     };
-    for (int kt = 0; kt + 1 < steps; ++kt) step(std::false_type{}, kt);
-    const int64_t tm0 = m0, tn0 = n0;
-    step(std::true_type{}, steps - 1);
+    int kt = 0;
+    for (; kt + kSlots < steps; ++kt) step(std::integral_constant<int, 0>{}, kt);
+    for (; kt + kSlots == steps; ++kt) step(std::integral_constant<int, 1>{}, kt);
+    if constexpr (kSlots > 2)
+      for (; kt + 1 < steps; ++kt) step(std::integral_constant<int, 2>{}, kt);
+    step(std::integral_constant<int, 3>{}, steps - 1);
     // ---- epilogue: D lane holds row lr of its row block, outputs 4 lq .. +3 of its column block
     // (lane roles taken afresh: addresses built from them are not kept through the products)
     int lr = lane & 15, lq = lane >> 4;
     asm volatile("" : "+v"(lr), "+v"(lq));
-    const float* sc = reinterpret_cast<const float*>(&sm[2 * kSlot + par * kScaleBytes]) + wn + 4 * lq;
-    const float* as = reinterpret_cast<const float*>(&sm[2 * kSlot + par * kScaleBytes]) + 2 * kBN + wm + lr;
+    const float* sc = reinterpret_cast<const float*>(&sm[kSlots * kSlot + par * kScaleBytes]) + wn + 4 * lq;
+    const float* as = reinterpret_cast<const float*>(&sm[kSlots * kSlot + par * kScaleBytes]) + 2 * kBN + wm + lr;
     const int mleft = (int)min(d.M - tm0 - wm, (int64_t)WM);  // rows of the wave
     const int nleft = (int)min(d.N - tn0 - wn, (int64_t)WN);  // columns of the wave
     const int64_t row0 = tm0 + wm + lr;
@@ -328,27 +344,47 @@ __global__ __launch_bounds__(256) void act_quant_kernel(const float* __restrict_
   if (threadIdx.x == 0) s[blockIdx.x] = scale;
 }
 
-template <int kBM, int kBN, int kWM, int kWN, int kOut, bool kAdd>
-hipError_t launch_tiles(const DenseArgs& d, int64_t I, float* act, int per_cu, hipStream_t stream) {
+template <int kBM, int kBN, int kWM, int kWN, int kSlots, int kPerCu, int kOut, bool kAdd>
+hipError_t launch_tiles(const DenseArgs& d, int64_t I, float* act, hipStream_t stream) {
   const int64_t mb = (d.M + kBM - 1) / kBM, nb = (d.N + kBN - 1) / kBN;
-  auto kernel = dense_i8_kernel<kBM, kBN, kWM, kWN, kOut, kAdd>;
-  constexpr int kLds = 2 * (kBM + kBN) * kBK + 2 * 4 * (2 * kBN + kBM);
+  auto kernel = dense_i8_kernel<kBM, kBN, kWM, kWN, kSlots, kOut, kAdd>;
+  constexpr int kLds = kSlots * (kBM + kBN) * kBK + 2 * 4 * (2 * kBN + kBM);
+  static_assert(kPerCu * kLds <= 160 * 1024, "LDS");
   if constexpr (kLds > 65536) {
     static const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
                                                     hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
     if (e != hipSuccess) return e;
   }
-  const int64_t slots = 256 * per_cu, tiles = mb * nb;
+  const int64_t slots = 256 * kPerCu, tiles = mb * nb;
   hipLaunchKernelGGL(kernel, dim3((unsigned)(tiles < slots ? tiles : slots)), dim3(64 * kWM * kWN), kLds, stream, d, I,
                      act, (int)mb, (int)nb);
   return hipGetLastError();
 }
 
+// The tile that ends first: the tiles go over the 256 CUs in rounds, and a round costs the tile's
+// time per step.  Measured at K = 6144 (us a step, one tile on each CU): 64 x 64 0.20, 128 x 64
+// 0.33, 128 x 128 0.46, 256 x 128 0.63 to 0.84, 256 x 256 1.15 to 1.35 (the larger the nearer to
+// the card's power limit).  6144 outputs (us; the tile chosen first, then the next best): 128 rows
+// 11.7 with 64 x 64, 16.4 with 128 x 64; 256 rows 17.2 with 128 x 64, 19.5 with 64 x 64; 512 rows
+// 22.8 with 128 x 128, 32.7 with 128 x 64; 1024 rows 37.8 with 256 x 128, 42.3 with 128 x 128; 2048
+// rows 64.9 with 256 x 256, 73.3 with 128 x 128; 3000 rows 113.7 with 256 x 128, 129.9 with 256 x 256.
 template <int kOut, bool kAdd>
 hipError_t launch_product(const DenseArgs& d, int64_t I, float* act, hipStream_t stream) {
-  const int64_t big = ((d.M + 255) / 256) * ((d.N + 255) / 256);
-  if (d.M > 128 && big >= 192) return launch_tiles<256, 256, 2, 4, kOut, kAdd>(d, I, act, 1, stream);
-  return launch_tiles<128, 128, 2, 2, kOut, kAdd>(d, I, act, 2, stream);
+  auto cost = [&](int bm, int bn, double step) {
+    return step * (double)((((d.M + bm - 1) / bm) * ((d.N + bn - 1) / bn) + 255) / 256);
+  };
+  const double c[5] = {cost(64, 64, 0.20), cost(128, 64, 0.33), cost(128, 128, 0.46), cost(256, 128, 0.75),
+                       cost(256, 256, 1.32)};
+  int best = 0;
+  for (int i = 1; i < 5; ++i)
+    if (c[i] < c[best]) best = i;
+  switch (best) {
+    case 0: return launch_tiles<64, 64, 2, 2, 4, 2, kOut, kAdd>(d, I, act, stream);
+    case 1: return launch_tiles<128, 64, 2, 2, 4, 1, kOut, kAdd>(d, I, act, stream);
+    case 2: return launch_tiles<128, 128, 2, 2, 4, 1, kOut, kAdd>(d, I, act, stream);
+    case 3: return launch_tiles<256, 128, 4, 2, 3, 1, kOut, kAdd>(d, I, act, stream);
+    default: return launch_tiles<256, 256, 2, 4, 2, 1, kOut, kAdd>(d, I, act, stream);
+  }
 }
 
 }  // namespace
@@ -356,6 +392,7 @@ hipError_t launch_product(const DenseArgs& d, int64_t I, float* act, hipStream_t
 int64_t dense_i8_workspace_bytes(int64_t, int64_t, int64_t) { return 0; }
 
 hipError_t launch_dense_i8(const DenseArgs& d, hipStream_t stream) {
+  if (dense_few_fits(d.M, d.ld_a)) return launch_dense_few(d, stream);
   if (d.y_bf16)
     return d.add ? launch_product<kOutBf16, true>(d, 0, nullptr, stream)
                  : launch_product<kOutBf16, false>(d, 0, nullptr, stream);
@@ -363,7 +400,7 @@ hipError_t launch_dense_i8(const DenseArgs& d, hipStream_t stream) {
                : launch_product<kOutF32, false>(d, 0, nullptr, stream);
 }
 
-// act fp32 [M][I], codes [M][I], scales [M]
+// act fp32 [M][I], then codes [M][I] and scales [M], or the maxima of 8 columns of act [M][I / 8]
 int64_t mlp_i8_workspace_bytes(int64_t M, int64_t, int64_t I) { return M * (5 * I + 4); }
 
 hipError_t launch_mlp_i8(const MlpArgs& p, hipStream_t stream) {
@@ -371,10 +408,15 @@ hipError_t launch_mlp_i8(const MlpArgs& p, hipStream_t stream) {
   uint8_t* q = reinterpret_cast<uint8_t*>(act + p.M * p.I);
   float* s = reinterpret_cast<float*>(q + p.M * p.I);
   const DenseArgs up{p.a, p.a_scale, p.M, p.H, p.ld_a, p.w13, p.s13, nullptr, 2 * p.I, nullptr, nullptr, 0, nullptr};
-  if (const hipError_t e = launch_product<kOutAct, false>(up, p.I, act, stream); e != hipSuccess) return e;
-  hipLaunchKernelGGL(act_quant_kernel, dim3((unsigned)p.M), dim3(256), 0, stream, act, p.I, q, s);
   const DenseArgs down{reinterpret_cast<int8_t*>(q), s, p.M, p.I, p.I, p.w2, p.s2, nullptr, p.H, p.add, p.y, p.y_bf16,
                        nullptr};
+  if (dense_few_fits(p.M, p.ld_a)) {
+    uint32_t* pmax = reinterpret_cast<uint32_t*>(q);
+    if (const hipError_t e = launch_gated_few(up, p.I, act, pmax, stream); e != hipSuccess) return e;
+    return launch_down_few(down, act, pmax, stream);
+  }
+  if (const hipError_t e = launch_product<kOutAct, false>(up, p.I, act, stream); e != hipSuccess) return e;
+  hipLaunchKernelGGL(act_quant_kernel, dim3((unsigned)p.M), dim3(256), 0, stream, act, p.I, q, s);
   return launch_dense_i8(down, stream);
 }
 
