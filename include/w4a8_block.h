@@ -39,16 +39,12 @@ extern "C" {
  *   y        : [M][N], fp32 or bf16 (y_dtype W4A8_Y_F32 or W4A8_Y_BF16; rounded to
  *              nearest even), aligned to its elements; no overlap with a, w and the
  *              vectors (not checked).
- *   workspace : device memory of w4a8_moe_dense_i8_workspace_bytes(M, N, K) bytes,
- *              16-byte aligned; NULL where that is 0.  Its contents need no
- *              initialisation; calls that overlap must not share one.
  *   Rules    : M >= 0, 0 < N <= 2^24, 0 < K < 2^17, K % 16 == 0, M * N <= 2^40.
  *   Rows of a_scale that are not finite reach their own row of y only.
  */
-int64_t w4a8_moe_dense_i8_workspace_bytes(int64_t M, int64_t N, int64_t K);
 int w4a8_moe_dense_i8(const int8_t* a, const float* a_scale, int64_t M, int64_t K, int64_t ld_a, const int8_t* w,
                       const float* w_scale, const float* bias, int64_t N, const void* add, void* y, int32_t y_dtype,
-                      void* workspace, int64_t workspace_bytes, void* stream);
+                      void* stream);
 
 /*
  * w4a8_moe_mlp_i8 -- the gated feed-forward block on such weights (a shared expert, the
@@ -81,8 +77,9 @@ int w4a8_moe_mlp_i8(const int8_t* a, const float* a_scale, int64_t M, int64_t H,
  *     n[t, :] = weight * x[t, :] / sqrt(mean(x[t, :]^2) + eps)   (fp32);
  *     xn[t, :] = n rounded to bf16 (the router's and the layer's input);
  *     scale and codes of n, as it is before that rounding: sx[t] = fl32(max |n| / 448)
- *     (_i8: / 127), 1.0 if that is 0; qx = E4M3 (_i8: the integer) nearest to n / sx,
- *     ties to even, the quotient rounded to fp32 first; _i8: rowsum[t] = sum of qx[t, :].
+ *     (_i8: / 127), 1.0 if that is 0; qx = E4M3 (_i8: the integer) nearest to 448 n / max |n|
+ *     (127 n / max |n|), ties to even, the quotient correct to fp32's rounding; _i8:
+ *     rowsum[t] = sum of qx[t, :].
  *   x       : [T][ld_x], fp32 or bf16 (x_dtype: W4A8_Y_F32, W4A8_Y_BF16), 16-byte aligned
  *             rows (ld_x % 8 == 0 in bf16, % 4 in fp32), ld_x >= H.
  *   weight  : fp32 [H], 16-byte aligned.

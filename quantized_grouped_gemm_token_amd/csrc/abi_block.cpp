@@ -118,14 +118,9 @@ int run_residual(const char* name, int codes, const void* y, int32_t y_dtype, in
 
 extern "C" {
 
-int64_t w4a8_moe_dense_i8_workspace_bytes(int64_t M, int64_t N, int64_t K) {
-  if (check_dense("dense_i8", M, N, K, K, W4A8_Y_F32) != W4A8_OK) return -1;
-  return w4a8::dense_i8_workspace_bytes(M, N, K);
-}
-
 int w4a8_moe_dense_i8(const int8_t* a, const float* a_scale, int64_t M, int64_t K, int64_t ld_a, const int8_t* w,
                       const float* w_scale, const float* bias, int64_t N, const void* add, void* y, int32_t y_dtype,
-                      void* workspace, int64_t workspace_bytes, void* stream) {
+                      void* stream) {
   if (int st = check_dense("dense_i8", M, N, K, ld_a, y_dtype)) return st;
   if (M == 0) return ok();
   if (!a || !a_scale || !w || !w_scale || !y) return fail(W4A8_ERR_NULL, "dense_i8: null pointer");
@@ -133,11 +128,9 @@ int w4a8_moe_dense_i8(const int8_t* a, const float* a_scale, int64_t M, int64_t 
   if (!aligned(a, 16) || !aligned(w, 16) || !aligned(a_scale, 4) || !aligned(w_scale, 4) || !aligned(bias, 4) ||
       !aligned(add, e) || !aligned(y, e))
     return fail(W4A8_ERR_ALIGN, "dense_i8: a and w must be 16-byte aligned, the rest to their elements");
-  if (int st = check_workspace("dense_i8", workspace, workspace_bytes, w4a8::dense_i8_workspace_bytes(M, N, K)))
-    return st;
   if (int st = check_device()) return st;
   (void)hipGetLastError();
-  const w4a8::DenseArgs d{a, a_scale, M, K, ld_a, w, w_scale, bias, N, add, y, y_dtype == W4A8_Y_BF16, workspace};
+  const w4a8::DenseArgs d{a, a_scale, M, K, ld_a, w, w_scale, bias, N, add, y, y_dtype == W4A8_Y_BF16};
   return launched(w4a8::launch_dense_i8(d, as_stream(stream)), "dense_i8");
 }
 

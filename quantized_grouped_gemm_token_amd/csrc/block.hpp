@@ -24,9 +24,7 @@ struct DenseArgs {
   const void* add;        // or null
   void* y;
   int y_bf16;
-  void* workspace;
 };
-int64_t dense_i8_workspace_bytes(int64_t M, int64_t N, int64_t K);
 hipError_t launch_dense_i8(const DenseArgs& d, hipStream_t stream);
 
 struct MlpArgs {

@@ -389,8 +389,6 @@ hipError_t launch_product(const DenseArgs& d, int64_t I, float* act, hipStream_t
 
 }  // namespace
 
-int64_t dense_i8_workspace_bytes(int64_t, int64_t, int64_t) { return 0; }
-
 hipError_t launch_dense_i8(const DenseArgs& d, hipStream_t stream) {
   if (dense_few_fits(d.M, d.ld_a)) return launch_dense_few(d, stream);
   if (d.y_bf16)
@@ -407,9 +405,8 @@ hipError_t launch_mlp_i8(const MlpArgs& p, hipStream_t stream) {
   float* act = static_cast<float*>(p.workspace);
   uint8_t* q = reinterpret_cast<uint8_t*>(act + p.M * p.I);
   float* s = reinterpret_cast<float*>(q + p.M * p.I);
-  const DenseArgs up{p.a, p.a_scale, p.M, p.H, p.ld_a, p.w13, p.s13, nullptr, 2 * p.I, nullptr, nullptr, 0, nullptr};
-  const DenseArgs down{reinterpret_cast<int8_t*>(q), s, p.M, p.I, p.I, p.w2, p.s2, nullptr, p.H, p.add, p.y, p.y_bf16,
-                       nullptr};
+  const DenseArgs up{p.a, p.a_scale, p.M, p.H, p.ld_a, p.w13, p.s13, nullptr, 2 * p.I, nullptr, nullptr, 0};
+  const DenseArgs down{reinterpret_cast<int8_t*>(q), s, p.M, p.I, p.I, p.w2, p.s2, nullptr, p.H, p.add, p.y, p.y_bf16};
   if (dense_few_fits(p.M, p.ld_a)) {
     uint32_t* pmax = reinterpret_cast<uint32_t*>(q);
     if (const hipError_t e = launch_gated_few(up, p.I, act, pmax, stream); e != hipSuccess) return e;

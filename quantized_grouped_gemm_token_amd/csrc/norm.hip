@@ -2,9 +2,9 @@
 // the residual sum of a block's result, normed and gated, followed by the next block's norm.
 //
 // A row is read once and held in registers by a group of threads (a wave for up to 2048
-// values, 256 threads up to 16384, 1024 up to 32768), 8 values to a chunk of 16 or 32 bytes:
-//   before: n = weight x rsqrt(mean x^2 + eps); max |n|; codes.
-//   after:  p = post y rsqrt(mean y^2 + eps); out = r_scale r + token_gate gate p; then the
+// values, 256 to 1024 threads beyond), 8 values to a chunk of 16 or 32 bytes:
+//   before: n = weight x / sqrt(mean x^2 + eps); max |n|; codes.
+//   after:  p = post y / sqrt(mean y^2 + eps); out = r_scale r + token_gate gate p; then the
 //           same of out.
 // Each mean, and the maximum, is one reduction over the group.  Sums are fp32; a row whose
 // sum of squares is not below infinity is summed again times 2^-80, where 32768 squares of
@@ -40,29 +40,48 @@ __device__ __forceinline__ float group_max(float v, float* red) {
 
 // 8 values of a row as they lie in memory, and as fp32
 struct Raw {
-  uint4 a, b;
+  u32x4 a, b;
 };
+// kNt: read once
+template <bool kNt>
+__device__ __forceinline__ u32x4 load16(const u32x4* p) {
+  return kNt ? __builtin_nontemporal_load(p) : *p;
+}
+template <bool kNt>
 __device__ __forceinline__ Raw load_raw(const void* row, int bf16, int chunk) {
+  const u32x4* p = static_cast<const u32x4*>(row);
   Raw v;
   if (bf16) {
-    v.a = static_cast<const uint4*>(row)[chunk];
-    v.b = make_uint4(0u, 0u, 0u, 0u);
+    v.a = load16<kNt>(p + chunk);
+    v.b = u32x4{0u, 0u, 0u, 0u};
   } else {
-    v.a = static_cast<const uint4*>(row)[2 * chunk];
-    v.b = static_cast<const uint4*>(row)[2 * chunk + 1];
+    v.a = load16<kNt>(p + 2 * chunk);
+    v.b = load16<kNt>(p + 2 * chunk + 1);
   }
   return v;
 }
+template <bool kNt, int kThr, int kPer>
+__device__ __forceinline__ void load_row(Raw (&raw)[kPer], const void* row, int bf16, int tid, int chunks) {
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int c = tid + kThr * i;
+    raw[i] = c < chunks ? load_raw<kNt>(row, bf16, c) : Raw{};
+  }
+}
+template <bool kNt, typename T>
+__device__ __forceinline__ void store(T* p, T v) {
+  if constexpr (kNt) __builtin_nontemporal_store(v, p);
+  else *p = v;
+}
 __device__ __forceinline__ void widen(const Raw& v, int bf16, float (&f)[8]) {
-  const uint32_t a[4] = {v.a.x, v.a.y, v.a.z, v.a.w}, b[4] = {v.b.x, v.b.y, v.b.z, v.b.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     if (bf16) {
-      f[2 * i] = bf16_lo(a[i]);
-      f[2 * i + 1] = bf16_hi(a[i]);
+      f[2 * i] = bf16_lo(v.a[i]);
+      f[2 * i + 1] = bf16_hi(v.a[i]);
     } else {
-      f[i] = __uint_as_float(a[i]);
-      f[4 + i] = __uint_as_float(b[i]);
+      f[i] = __uint_as_float(v.a[i]);
+      f[4 + i] = __uint_as_float(v.b[i]);
     }
   }
 }
@@ -70,52 +89,41 @@ __device__ __forceinline__ void load_vector(const float* v, int chunk, float (&f
   const float4 a = reinterpret_cast<const float4*>(v)[2 * chunk], b = reinterpret_cast<const float4*>(v)[2 * chunk + 1];
   f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
 }
-__device__ __forceinline__ uint4 bf16x8(const float (&f)[8]) {
-  return make_uint4(bf16_pair(f[0], f[1]), bf16_pair(f[2], f[3]), bf16_pair(f[4], f[5]), bf16_pair(f[6], f[7]));
+__device__ __forceinline__ u32x4 bf16x8(const float (&f)[8]) {
+  return u32x4{bf16_pair(f[0], f[1]), bf16_pair(f[2], f[3]), bf16_pair(f[4], f[5]), bf16_pair(f[6], f[7])};
 }
 
-// the values of a row times 1 / sqrt(mean square + eps) and times `weight`; false where the
-// row holds a NaN or an infinity
+// What a row is multiplied by for its norm (weights apart): 1 / sqrt(mean square + eps); not fine
+// where the row holds a NaN or an infinity.  The values may be scaled on the way, the factor too.
+struct RowNorm {
+  float f;
+  bool fine;
+};
 template <int kThr, int kPer>
-__device__ __forceinline__ bool normalize(float (&v)[kPer][8], int chunks, int tid, float H, float eps,
-                                          const float* weight, float* red, float* red2) {
+__device__ __forceinline__ RowNorm row_norm(float (&v)[kPer][8], float H, float eps, float* red, float* red2) {
   float ss = 0.0f;
 #pragma unroll
   for (int i = 0; i < kPer; ++i)
 #pragma unroll
     for (int j = 0; j < 8; ++j) ss = fmaf(v[i][j], v[i][j], ss);
   ss = group_sum<kThr>(ss, red);
-  float f;
-  if (ss < INFINITY) {
-    f = __builtin_amdgcn_rsqf(ss / H + eps);
-  } else {                                                  // (the same for the whole group)
-    constexpr float kDown = 0x1p-80f;
-    ss = 0.0f;
+  if (ss < INFINITY) return RowNorm{__builtin_amdgcn_rsqf(ss / H + eps), true};
+  constexpr float kDown = 0x1p-80f;                         // (the same for the whole group)
+  ss = 0.0f;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i)
+  for (int i = 0; i < kPer; ++i)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        v[i][j] *= kDown;
-        ss = fmaf(v[i][j], v[i][j], ss);
-      }
-    ss = group_sum<kThr>(ss, red2);
-    f = __builtin_amdgcn_rsqf(ss / H);
-  }
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const int c = tid + kThr * i;
-    if (c < chunks) {
-      float w[8];
-      load_vector(weight, c, w);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] = v[i][j] * f * w[j];
+    for (int j = 0; j < 8; ++j) {
+      v[i][j] *= kDown;
+      ss = fmaf(v[i][j], v[i][j], ss);
     }
-  }
-  return ss < INFINITY;
+  ss = group_sum<kThr>(ss, red2);
+  return RowNorm{__builtin_amdgcn_rsqf(ss / H), ss < INFINITY};
 }
 
-// kRes: with r (the residual form).  A block holds one group, or four of a wave.
-template <int kThr, int kPer, bool kRes, int kCodes>
+// kRes: with r (the residual form).  kNt: rows and results are marked as read and written once.  A
+// block holds one group, or four of a wave.
+template <int kThr, int kPer, bool kRes, int kCodes, bool kNt>
 __global__ __launch_bounds__(kThr < 256 ? 256 : kThr) void norm_kernel(const NormArgs n) {
   __shared__ float red[5][16];
   constexpr int kGroups = kThr < 256 ? 256 / kThr : 1;
@@ -127,24 +135,27 @@ __global__ __launch_bounds__(kThr < 256 ? 256 : kThr) void norm_kernel(const Nor
   const char* xr = static_cast<const char*>(n.x) + t * n.ld_x * (n.x_bf16 ? 2 : 4);
   float v[kPer][8];
   Raw raw[kPer], raw_r[kRes ? kPer : 1];
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const int c = tid + kThr * i;
-    raw[i] = c < chunks ? load_raw(xr, n.x_bf16, c) : Raw{};
-  }
-  if constexpr (kRes) {
-    const char* rr = static_cast<const char*>(n.r) + t * n.ld_r * (n.r_bf16 ? 2 : 4);
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int c = tid + kThr * i;
-      raw_r[i] = c < chunks ? load_raw(rr, n.r_bf16, c) : Raw{};
-    }
-  }
+  const char* rr = static_cast<const char*>(n.r) + t * n.ld_r * (n.r_bf16 ? 2 : 4);
+  load_row<kNt, kThr>(raw, xr, n.x_bf16, tid, chunks);
+  if constexpr (kRes) load_row<kNt, kThr>(raw_r, rr, n.r_bf16, tid, chunks);
 #pragma unroll
   for (int i = 0; i < kPer; ++i) widen(raw[i], n.x_bf16, v[i]);
   bool fine = true;
   if constexpr (kRes) {
-    if (n.post) fine = normalize<kThr, kPer>(v, chunks, tid, H, n.eps, n.post, red[0], red[1]);
+    if (n.post) {
+      const RowNorm r = row_norm<kThr, kPer>(v, H, n.eps, red[0], red[1]);
+      fine = r.fine;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const int c = tid + kThr * i;
+        if (c < chunks) {
+          float w[8];
+          load_vector(n.post, c, w);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) v[i][j] = v[i][j] * r.f * w[j];
+        }
+      }
+    }
     const float tg = n.token_gate ? n.token_gate[t] : 1.0f;
     char* outr = static_cast<char*>(n.out) + t * n.ld_out * (n.r_bf16 ? 2 : 4);
 #pragma unroll
@@ -162,7 +173,7 @@ __global__ __launch_bounds__(kThr < 256 ? 256 : kThr) void norm_kernel(const Nor
           v[i][j] = fmaf(n.r_scale, r[j], p);
         }
         if (n.r_bf16) {
-          reinterpret_cast<uint4*>(outr)[c] = bf16x8(v[i]);
+          store<kNt>(reinterpret_cast<u32x4*>(outr) + c, bf16x8(v[i]));
         } else {
           reinterpret_cast<float4*>(outr)[2 * c] = make_float4(v[i][0], v[i][1], v[i][2], v[i][3]);
           reinterpret_cast<float4*>(outr)[2 * c + 1] = make_float4(v[i][4], v[i][5], v[i][6], v[i][7]);
@@ -171,37 +182,57 @@ __global__ __launch_bounds__(kThr < 256 ? 256 : kThr) void norm_kernel(const Nor
     }
     if (!n.weight) return;
   }
-  fine &= normalize<kThr, kPer>(v, chunks, tid, H, n.eps, n.weight, red[2], red[3]);
-  if (n.xn) {
-    uint4* xnr = reinterpret_cast<uint4*>(n.xn + t * n.H);
+  // n = f x weight, with f = g 2^e: the products (2^e x) weight are taken exactly, as a sum of two
+  // fp32 values, and g, which every quotient n / max |n| lacks, only enters xn and the scale.  So a
+  // code is the nearest to the row's true quotient, where three rounded products and a rounded
+  // quotient would put it on the other side of a border a few times in a million.
+  const RowNorm r = row_norm<kThr, kPer>(v, H, n.eps, red[2], red[3]);
+  fine &= r.fine;
+  const float e2 = __uint_as_float(__float_as_uint(r.f) & 0x7f800000u), g = r.f / e2;
+  float lo[kCodes != kCodesNone ? kPer : 1][8], m = 0.0f;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i)
-      if (tid + kThr * i < chunks) xnr[tid + kThr * i] = bf16x8(v[i]);
+  for (int i = 0; i < kPer; ++i) {
+    const int c = tid + kThr * i;
+    if (c < chunks) {
+      float w[8], o[8];
+      load_vector(n.weight, c, w);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float x = v[i][j] * e2, p = x * w[j];
+        if constexpr (kCodes != kCodesNone) {
+          lo[i][j] = fmaf(x, w[j], -p);
+          m = fmaxf(m, fabsf(p));
+        }
+        v[i][j] = p;
+        o[j] = p * g;
+      }
+      if (n.xn) store<kNt>(reinterpret_cast<u32x4*>(n.xn + t * n.H) + c, bf16x8(o));
+    }
   }
   if constexpr (kCodes != kCodesNone) {
     constexpr bool kInt8 = kCodes == kCodesI8;
-    float m = 0.0f;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(v[i][j]));    // (0 past the row)
+    constexpr float kTop = kInt8 ? 127.0f : kFp8Max;
     m = group_max<kThr>(m, red[4]);
-    const float scale = row_scale<kInt8>(m);
-    const RowDivisor d = row_divisor(scale);
-    uint2* qr = reinterpret_cast<uint2*>(n.q + t * n.H);
+    const float scale = row_scale<kInt8>(m * g);
+    // kTop / m as a sum of two as well; rows of very small values are scaled first, where it would
+    // not be finite
+    const float by = m < 0x1p-80f ? 0x1p100f : 1.0f, top = m * by;
+    const float c0 = top > 0.0f ? kTop / top : 0.0f, c1 = top > 0.0f ? fmaf(-c0, top, kTop) / top : 0.0f;
+    uint64_t* qr = reinterpret_cast<uint64_t*>(n.q + t * n.H);
     int sum = 0;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       const int c = tid + kThr * i;
       if (c < chunks) {
-        if (d.by != 1.0f) {
+        float o[8];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) v[i][j] *= d.by;
+        for (int j = 0; j < 8; ++j) {
+          const float p = v[i][j] * by, l = lo[i][j] * by;
+          o[j] = fmaf(p, c0, fmaf(p, c1, l * c0));
         }
-        const uint2 q = make_uint2(codes4<kInt8>(v[i][0], v[i][1], v[i][2], v[i][3], d.s, d.r),
-                                   codes4<kInt8>(v[i][4], v[i][5], v[i][6], v[i][7], d.s, d.r));
+        const uint2 q = make_uint2(nearest4<kInt8>(o[0], o[1], o[2], o[3]), nearest4<kInt8>(o[4], o[5], o[6], o[7]));
         if constexpr (kInt8) sum = __builtin_amdgcn_sdot4(q.x, 0x01010101, __builtin_amdgcn_sdot4(q.y, 0x01010101, sum, false), false);
-        qr[c] = q;
+        store<kNt>(qr + c, q.x | (uint64_t)q.y << 32);
       }
     }
     if (tid == 0) n.s[t] = fine ? scale : __uint_as_float(0x7fc00000u);
@@ -222,32 +253,56 @@ __global__ __launch_bounds__(kThr < 256 ? 256 : kThr) void norm_kernel(const Nor
   }
 }
 
-template <int kThr, int kPer>
+template <int kThr, int kPer, bool kNt>
 static void launch_norm_form(const NormArgs& n, hipStream_t stream) {
   constexpr int kGroups = kThr < 256 ? 256 / kThr : 1;
   const dim3 grid((unsigned)((n.T + kGroups - 1) / kGroups)), block(kThr * kGroups);
   auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, block, 0, stream, n); };
   if (n.r) {
-    if (n.codes == kCodesFp8) go(norm_kernel<kThr, kPer, true, kCodesFp8>);
-    else if (n.codes == kCodesI8) go(norm_kernel<kThr, kPer, true, kCodesI8>);
-    else go(norm_kernel<kThr, kPer, true, kCodesNone>);
+    if (n.codes == kCodesFp8) go(norm_kernel<kThr, kPer, true, kCodesFp8, kNt>);
+    else if (n.codes == kCodesI8) go(norm_kernel<kThr, kPer, true, kCodesI8, kNt>);
+    else go(norm_kernel<kThr, kPer, true, kCodesNone, kNt>);
   } else {
-    if (n.codes == kCodesFp8) go(norm_kernel<kThr, kPer, false, kCodesFp8>);
-    else if (n.codes == kCodesI8) go(norm_kernel<kThr, kPer, false, kCodesI8>);
-    else go(norm_kernel<kThr, kPer, false, kCodesNone>);
+    if (n.codes == kCodesFp8) go(norm_kernel<kThr, kPer, false, kCodesFp8, kNt>);
+    else if (n.codes == kCodesI8) go(norm_kernel<kThr, kPer, false, kCodesI8, kNt>);
+    else go(norm_kernel<kThr, kPer, false, kCodesNone, kNt>);
   }
 }
 
+// A row has as many threads as keep it in a few registers: 256 of bf16, 512 where fp32 is among the
+// rows (norms on both sides of 8192 rows of 6144, fp32: 149 against 158 us; 16384 bf16 rows, norm
+// alone: 89 against 86).  While there is a CU for every row, as many as it has chunks, up to 1024 (128
+// rows of 6144: the norm 3.6 against 4.0 us with 256, between two blocks 5.5 against 7.0).
+constexpr int64_t kFewRows = 256;
+template <bool kNt>
+static void launch_bf16_rows(const NormArgs& n, hipStream_t stream) {
+  if (n.H <= 4096) launch_norm_form<256, 2, kNt>(n, stream);
+  else if (n.H <= 6144) launch_norm_form<256, 3, kNt>(n, stream);
+  else if (n.H <= 8192) launch_norm_form<256, 4, kNt>(n, stream);
+  else launch_norm_form<256, 8, kNt>(n, stream);
+}
+
+// From here on bf16 rows and their results are marked as read or written once: they would only push
+// each other out of the 256 MB last-level cache (16384 rows of 6144 90 against 97 us; norm, a
+// product of 6144 outputs and the residual of 8192 rows 327 against 341 us).  Below, the reader of
+// the results finds them there (2048 rows 90 against 98 us).  fp32 rows gain nothing.
+constexpr int64_t kStreamBytes = (int64_t)192 << 20;
+
 hipError_t launch_norm(const NormArgs& n, hipStream_t stream) {
   if (n.T == 0) return hipSuccess;
-  if (n.H <= 512) launch_norm_form<64, 1>(n, stream);
-  else if (n.H <= 1024) launch_norm_form<64, 2>(n, stream);
-  else if (n.H <= 2048) launch_norm_form<64, 4>(n, stream);
-  else if (n.H <= 4096) launch_norm_form<256, 2>(n, stream);
-  else if (n.H <= 6144) launch_norm_form<256, 3>(n, stream);
-  else if (n.H <= 8192) launch_norm_form<256, 4>(n, stream);
-  else if (n.H <= 16384) launch_norm_form<256, 8>(n, stream);
-  else launch_norm_form<1024, 4>(n, stream);
+  const bool bf16 = n.x_bf16 && (!n.r || n.r_bf16);
+  const int64_t bytes = n.T * n.H * (2 + (n.r ? 4 : 0) + (n.xn ? 2 : 0) + (n.q ? 1 : 0));
+  if (n.H <= 512) launch_norm_form<64, 1, false>(n, stream);
+  else if (n.H <= 1024) launch_norm_form<64, 2, false>(n, stream);
+  else if (n.H <= 2048) launch_norm_form<64, 4, false>(n, stream);
+  else if (n.H > 16384) launch_norm_form<1024, 4, false>(n, stream);
+  else if (n.T <= kFewRows && n.H <= 8192) launch_norm_form<1024, 1, false>(n, stream);
+  else if (n.T <= kFewRows) launch_norm_form<1024, 2, false>(n, stream);
+  else if (bf16 && bytes > kStreamBytes) launch_bf16_rows<true>(n, stream);
+  else if (bf16) launch_bf16_rows<false>(n, stream);
+  else if (n.H <= 4096) launch_norm_form<512, 1, false>(n, stream);
+  else if (n.H <= 8192) launch_norm_form<512, 2, false>(n, stream);
+  else launch_norm_form<512, 4, false>(n, stream);
   return hipGetLastError();
 }
 

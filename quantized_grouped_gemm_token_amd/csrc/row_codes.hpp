@@ -16,22 +16,26 @@ __device__ __forceinline__ float div_by(float x, float s, float r) {
   return fmaf(fmaf(-q, s, x), r, q);
 }
 
-// four codes of four values of a row with scale s (r = 1 / s), the first in byte 0.
-// The FP8 conversion instruction rounds to nearest even like e4m3_encode (equal on
-// every fp32 magnitude up to 448).  No clamp: a quotient is at most a rounding above
-// 448 (127), which rounds to the largest code.
+// the codes nearest to four quotients, the first in byte 0.  The FP8 conversion instruction rounds
+// to nearest even like e4m3_encode (equal on every fp32 magnitude up to 448).  No clamp: a
+// quotient is at most a rounding above 448 (127), which rounds to the largest code.
 template <bool kInt8>
-__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d, float s, float r) {
-  const float v[4] = {div_by(a, s, r), div_by(b, s, r), div_by(c, s, r), div_by(d, s, r)};
+__device__ __forceinline__ uint32_t nearest4(float a, float b, float c, float d) {
   if constexpr (kInt8) {
+    const float v[4] = {a, b, c, d};
     uint32_t o = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) o |= ((uint32_t)(int)rintf(v[i]) & 0xffu) << (8 * i);
     return o;
   } else {
-    const int o = __builtin_amdgcn_cvt_pk_fp8_f32(v[0], v[1], 0, false);
-    return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(v[2], v[3], o, true);
+    const int o = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+    return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, o, true);
   }
+}
+// four codes of four values of a row with scale s (r = 1 / s)
+template <bool kInt8>
+__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d, float s, float r) {
+  return nearest4<kInt8>(div_by(a, s, r), div_by(b, s, r), div_by(c, s, r), div_by(d, s, r));
 }
 
 template <bool kInt8>

@@ -99,8 +99,7 @@ _NORM = [_c_p, _i32, _i64, _i64, _i64, _c_p, ctypes.c_float]
 _RESIDUAL = [_c_p, _i32, _i64, _c_p, _i32, _i64, _i64, _i64, _c_p, _c_p, _c_p, ctypes.c_float, ctypes.c_float, _c_p,
              _i64]
 _BLOCK_SIGNATURES = {
-    "w4a8_moe_dense_i8_workspace_bytes": (ctypes.c_int64, [_i64, _i64, _i64]),
-    "w4a8_moe_dense_i8": (ctypes.c_int, _DENSE + [_c_p, _i64, _c_p, _c_p, _i32, _c_p, _i64, _c_p]),
+    "w4a8_moe_dense_i8": (ctypes.c_int, _DENSE + [_c_p, _i64, _c_p, _c_p, _i32, _c_p]),
     "w4a8_moe_mlp_i8_workspace_bytes": (ctypes.c_int64, [_i64, _i64, _i64]),
     "w4a8_moe_mlp_i8": (ctypes.c_int, _DENSE + [_c_p, _c_p, _i64, _c_p, _c_p, _i32, _c_p, _i64, _c_p]),
     "w4a8_moe_norm_quant": (ctypes.c_int, _NORM + [_c_p, _c_p, _c_p, _c_p]),
@@ -1223,53 +1222,26 @@ def _no_overlap(out, name: str, *inputs) -> None:
                 raise ValueError(f"{name} must not overlap {other}")
 
 
-def _dense_out(y, y_dtype, M: int, N: int, add, dev, x: torch.Tensor, inputs: tuple):
-    """y (given, or allocated) with its type's code; add has its type and shape, and is y or apart from it."""
-    if y is None:
-        if add is not None and isinstance(add, torch.Tensor) and add.dtype is not y_dtype:
-            raise TypeError(f"add must have y's type {y_dtype}")
-        if y_dtype is not _BF16 and y_dtype is not _F32:
-            raise TypeError("y must be float32 or bfloat16")
-        y = x.new_empty((M, N), dtype=y_dtype)
-    else:
-        if not isinstance(y, torch.Tensor) or y.dtype not in (_F32, _BF16):
-            raise TypeError("y must be a float32 or bfloat16 tensor")
-        _is(y, "y", y.dtype, (M, N), dev)
-        if M and N:
-            apart = () if add is None or (isinstance(add, torch.Tensor) and add.data_ptr() == y.data_ptr()) else \
-                (("add", add),)
-            _no_overlap(y, "y", *inputs, *apart)
-    if add is not None:
-        _is(add, "add", y.dtype, (M, N), dev)
-    return y, W4A8_Y_F32 if y.dtype is _F32 else W4A8_Y_BF16
+def _new_y(y_dtype, M: int, N: int, add, a: torch.Tensor) -> torch.Tensor:
+    if y_dtype is not _BF16 and y_dtype is not _F32:
+        raise TypeError("y must be float32 or bfloat16")
+    return a.new_empty((M, N), dtype=y_dtype)
 
 
-def w4a8_moe_dense_i8_workspace_bytes(M: int, N: int, K: int) -> int:
-    n = _function("w4a8_moe_dense_i8_workspace_bytes")(M, N, K)
-    if n < 0:
-        raise ValueError(f"sizes outside the rules of the dense product: M={M} N={N} K={K}")
-    return n
-
-
-def _workspace(given, name: str, dev, *sizes):
-    """(pointer, bytes, tensor) of the workspace of a call: given, or allocated where it needs one."""
-    if given is not None:
-        _need(given, "workspace", _U8, 1, dev)
-        return given.data_ptr(), given.numel(), given
-    f = _functions.get(name)
-    if f is None:
-        f = _functions[name] = _function(name)
-    n = f(*sizes)                                            # (-1 on sizes that the call refuses)
-    if n <= 0:
-        return None, 0, None
-    t = torch.empty((n,), dtype=_U8, device=dev)
-    return t.data_ptr(), n, t
+def _given_y(y, M: int, N: int, add, dev, **inputs) -> None:
+    """A given result: its type and shape, and its memory apart from the inputs' (add may be y itself)."""
+    if not isinstance(y, torch.Tensor) or y.dtype not in (_F32, _BF16):
+        raise TypeError("y must be a float32 or bfloat16 tensor")
+    _is(y, "y", y.dtype, (M, N), dev)
+    if M:
+        if add is not None and not (isinstance(add, torch.Tensor) and add.data_ptr() == y.data_ptr()):
+            inputs["add"] = add
+        _no_overlap(y, "y", *inputs.items())
 
 
 def w4a8_moe_dense_i8(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor,
                       bias: torch.Tensor | None = None, add: torch.Tensor | None = None,
-                      y: torch.Tensor | None = None, y_dtype: torch.dtype = torch.float32,
-                      workspace: torch.Tensor | None = None):
+                      y: torch.Tensor | None = None, y_dtype: torch.dtype = torch.float32):
     """int8 activation codes a [M, K] (rows any multiple of 16 elements apart) with scales fp32 [M] times int8
     weights w [N, K] with scales fp32 [N], plus bias fp32 [N] and add [M, N] (y's type; it may be y) -> y [M, N]
     (fp32 or bf16).  The integer sums are exact."""
@@ -1283,11 +1255,14 @@ def w4a8_moe_dense_i8(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor, w
     _is(w_scale, "w_scale", _F32, (N,), dev)
     if bias is not None:
         _is(bias, "bias", _F32, (N,), dev)
-    y, code = _dense_out(y, y_dtype, M, N, add, dev, a,
-                         (("a", a), ("a_scale", a_scale), ("w", w), ("w_scale", w_scale), ("bias", bias)))
-    ws, nbytes, held = _workspace(workspace, "w4a8_moe_dense_i8_workspace_bytes", dev, M, N, K)
+    if y is None:
+        y = _new_y(y_dtype, M, N, add, a)
+    else:
+        _given_y(y, M, N, add, dev, a=a, a_scale=a_scale, w=w, w_scale=w_scale, bias=bias)
+    if add is not None:
+        _is(add, "add", y.dtype, (M, N), dev)
     _call_on(dev, "w4a8_moe_dense_i8", a.data_ptr(), a_scale.data_ptr(), M, K, ld, w.data_ptr(), w_scale.data_ptr(),
-             _p(bias), N, _p(add), y.data_ptr(), code, ws, nbytes)
+             _p(bias), N, _p(add), y.data_ptr(), W4A8_Y_F32 if y.dtype is _F32 else W4A8_Y_BF16)
     return y
 
 
@@ -1315,11 +1290,27 @@ def w4a8_moe_mlp_i8(a: torch.Tensor, a_scale: torch.Tensor, w13: torch.Tensor, s
     _is(a_scale, "a_scale", _F32, (M,), dev)
     _is(s13, "s13", _F32, (2 * I,), dev)
     _is(s2, "s2", _F32, (H,), dev)
-    y, code = _dense_out(y, y_dtype, M, H, add, dev, a, (("a", a), ("a_scale", a_scale), ("w13", w13), ("s13", s13),
-                                                         ("w2", w2), ("s2", s2)))
-    ws, nbytes, held = _workspace(workspace, "w4a8_moe_mlp_i8_workspace_bytes", dev, M, H, I)
+    if y is None:
+        y = _new_y(y_dtype, M, H, add, a)
+    else:
+        _given_y(y, M, H, add, dev, a=a, a_scale=a_scale, w13=w13, s13=s13, w2=w2, s2=s2)
+    if add is not None:
+        _is(add, "add", y.dtype, (M, H), dev)
+    if workspace is None:
+        f = _functions.get("w4a8_moe_mlp_i8_workspace_bytes")
+        if f is None:
+            f = _functions["w4a8_moe_mlp_i8_workspace_bytes"] = _function("w4a8_moe_mlp_i8_workspace_bytes")
+        nbytes = max(f(M, H, I), 16)                         # (-1 on sizes that the library refuses below)
+        workspace = a.new_empty((nbytes,))
+    else:
+        _need(workspace, "workspace", _U8, 1, dev)
+        nbytes = workspace.numel()
+        if M:
+            _no_overlap(workspace, "workspace", ("a", a), ("a_scale", a_scale), ("w13", w13), ("s13", s13), ("w2", w2),
+                        ("s2", s2), ("add", add), ("y", y))
     _call_on(dev, "w4a8_moe_mlp_i8", a.data_ptr(), a_scale.data_ptr(), M, H, ld, w13.data_ptr(), s13.data_ptr(),
-             w2.data_ptr(), s2.data_ptr(), I, _p(add), y.data_ptr(), code, ws, nbytes)
+             w2.data_ptr(), s2.data_ptr(), I, _p(add), y.data_ptr(), W4A8_Y_F32 if y.dtype is _F32 else W4A8_Y_BF16,
+             workspace.data_ptr(), nbytes)
     return y
 
 
@@ -1330,37 +1321,34 @@ def _code(t: torch.Tensor) -> int:
     return W4A8_Y_BF16 if t.dtype is _BF16 else W4A8_Y_F32
 
 
-def _coded_rows(x: torch.Tensor, T: int, H: int, codes, xn, q, s, dev):
-    """The outputs of a norm before a block: given, or allocated."""
-    if xn is None:
-        xn = x.new_empty((T, H), dtype=_BF16)
-    else:
-        _is(xn, "xn", _BF16, (T, H), dev)
-    if q is None:
-        q = x.new_empty((T, H), dtype=codes)
-    else:
-        _is(q, "qx", codes, (T, H), dev)
-    if s is None:
-        s = x.new_empty((T,), dtype=_F32)
-    else:
-        _is(s, "sx", _F32, (T,), dev)
-    return xn, q, s
+def _given_codes(T: int, H: int, codes, dev, xn, qx, sx, rowsum, **inputs) -> None:
+    """Given outputs of a norm before a block: types, shapes, and memory apart from the inputs' and each other's."""
+    for n, t, dt, shape in (("xn", xn, _BF16, (T, H)), ("qx", qx, codes, (T, H)), ("sx", sx, _F32, (T,)),
+                            ("rowsum", rowsum, _I32, (T,))):
+        if t is not None:
+            _is(t, n, dt, shape, dev)
+            if T:
+                _no_overlap(t, n, *inputs.items())
+            inputs[n] = t
 
 
 def _norm_quant(name, codes, x, weight, eps, xn, qx, sx, rowsum):
     T, H, ld = _rows(x, "x", _FLOATS, 8)
     dev = x.device
     _is(weight, "weight", _F32, (H,), dev)
-    given = [(n, t) for n, t in (("xn", xn), ("qx", qx), ("sx", sx), ("rowsum", rowsum)) if t is not None]
-    xn, qx, sx = _coded_rows(x, T, H, codes, xn, qx, sx, dev)
-    if rowsum is not None:
-        _is(rowsum, "rowsum", _I32, (T,), dev)
-    if T:
-        for i, (n, t) in enumerate(given):
-            _no_overlap(t, n, ("x", x), ("weight", weight), *given[:i])
-    tail = (_p(rowsum),) if codes is _I8 else ()
-    _call_on(dev, name, x.data_ptr(), _code(x), T, H, ld, weight.data_ptr(), eps, xn.data_ptr(), qx.data_ptr(),
-             sx.data_ptr(), *tail)
+    if xn is not None or qx is not None or sx is not None or rowsum is not None:
+        _given_codes(T, H, codes, dev, xn, qx, sx, rowsum, x=x, weight=weight)
+    if xn is None:
+        xn = x.new_empty((T, H), dtype=_BF16)
+    if qx is None:
+        qx = x.new_empty((T, H), dtype=codes)
+    if sx is None:
+        sx = weight.new_empty((T,))
+    args = (x.data_ptr(), _code(x), T, H, ld, weight.data_ptr(), eps, xn.data_ptr(), qx.data_ptr(), sx.data_ptr())
+    if codes is _I8:
+        _call_on(dev, name, *args, _p(rowsum))
+    else:
+        _call_on(dev, name, *args)
     return xn, qx, sx
 
 
@@ -1384,39 +1372,49 @@ def _residual(name, codes, y, r, next_weight, post_weight, gate, token_gate, r_s
     T, H, ld_y = _rows(y, "y", _FLOATS, 8)
     dev = y.device
     Tr, Hr, ld_r = _rows(r, "r", _FLOATS, 8)
-    if (Tr, Hr) != (T, H) or r.device != dev:
+    if Tr != T or Hr != H or r.device != dev:
         raise ValueError(f"r must be [{T}, {H}] on {dev} like y, got {list(r.shape)} on {r.device}")
-    for n, v, size in (("post_weight", post_weight, H), ("gate", gate, H), ("token_gate", token_gate, T)):
-        if v is not None:
-            _is(v, n, _F32, (size,), dev)
-    vectors = (("post_weight", post_weight), ("gate", gate), ("token_gate", token_gate))
+    if post_weight is not None:
+        _is(post_weight, "post_weight", _F32, (H,), dev)
+    if gate is not None:
+        _is(gate, "gate", _F32, (H,), dev)
+    if token_gate is not None:
+        _is(token_gate, "token_gate", _F32, (T,), dev)
+    if codes is not None:
+        _is(next_weight, "next_weight", _F32, (H,), dev)
     if out is None:
-        out, ld_out = r.new_empty((T, H)), -(-H // 8) * 8
+        ld_out = -(-H // 8) * 8
+        out = r.new_empty((T, H))
     else:
         To, Ho, ld_out = _rows(out, "out", (r.dtype,), 8)
         if (To, Ho) != (T, H) or out.device != dev:
             raise ValueError(f"out must be [{T}, {H}] on {dev}, got {list(out.shape)} on {out.device}")
         if T:
             # out may be r or y themselves: a row is read whole before it is written
-            same = lambda t, ld: t.data_ptr() == out.data_ptr() and t.dtype is out.dtype and ld == ld_out  # noqa: E731
-            _no_overlap(out, "out", *(() if same(r, ld_r) else (("r", r),)), *(() if same(y, ld_y) else (("y", y),)),
-                        *vectors)
+            inputs = dict(post_weight=post_weight, gate=gate, token_gate=token_gate, next_weight=next_weight)
+            for n, t, ld in (("r", r, ld_r), ("y", y, ld_y)):
+                if t.data_ptr() != out.data_ptr() or t.dtype is not out.dtype or ld != ld_out:
+                    inputs[n] = t
+            _no_overlap(out, "out", *inputs.items())
     args = (y.data_ptr(), _code(y), ld_y, r.data_ptr(), _code(r), ld_r, T, H, _p(post_weight), _p(gate),
             _p(token_gate), r_scale, eps, out.data_ptr(), ld_out)
     if codes is None:
         _call_on(dev, name, *args)
         return out
-    _is(next_weight, "next_weight", _F32, (H,), dev)
-    given = [(n, t) for n, t in (("xn", xn), ("qx", qx), ("sx", sx), ("rowsum", rowsum)) if t is not None]
-    xn, qx, sx = _coded_rows(y, T, H, codes, xn, qx, sx, dev)
-    if rowsum is not None:
-        _is(rowsum, "rowsum", _I32, (T,), dev)
-    if T:
-        _no_overlap(out, "out", ("next_weight", next_weight))
-        for i, (n, t) in enumerate(given):
-            _no_overlap(t, n, ("y", y), ("r", r), ("out", out), ("next_weight", next_weight), *vectors, *given[:i])
-    tail = (_p(rowsum),) if codes is _I8 else ()
-    _call_on(dev, name, *args, next_weight.data_ptr(), xn.data_ptr(), qx.data_ptr(), sx.data_ptr(), *tail)
+    if xn is not None or qx is not None or sx is not None or rowsum is not None:
+        _given_codes(T, H, codes, dev, xn, qx, sx, rowsum, y=y, r=r, out=out, next_weight=next_weight,
+                     post_weight=post_weight, gate=gate, token_gate=token_gate)
+    if xn is None:
+        xn = y.new_empty((T, H), dtype=_BF16)
+    if qx is None:
+        qx = y.new_empty((T, H), dtype=codes)
+    if sx is None:
+        sx = next_weight.new_empty((T,))
+    args += (next_weight.data_ptr(), xn.data_ptr(), qx.data_ptr(), sx.data_ptr())
+    if codes is _I8:
+        _call_on(dev, name, *args, _p(rowsum))
+    else:
+        _call_on(dev, name, *args)
     return out, xn, qx, sx
 
 

@@ -73,12 +73,15 @@ E4M3 = np.array([(m / 8 * 2.0 ** -6 if e == 0 else (1 + m / 8) * 2.0 ** (e - 7))
                 [:127])
 
 
-def check_codes(n, rel, q, s, fp8, what=""):
-    """Codes q (bytes) and scales s of rows n that the kernel holds to within rel of each row's largest value."""
+def check_codes(n, rel, absolute, q, s, fp8, what=""):
+    """Codes q (bytes) and scales s of rows n that the kernel holds to within rel |n| + absolute max |n|.
+
+    A quotient n / s is then off by rel |n / s| and by absolute max |n| / s, which is absolute times the largest code
+    whatever n is, and by the scale's own error, rel + absolute and two roundings of it."""
     top = np.abs(n).max(1)
     want = np.where(top > 0, top / (448.0 if fp8 else 127.0), 1.0)
-    # the scale is the error of the row's largest value and a rounding (a step of the smallest fp32 where it is tiny)
-    assert np.all(np.abs(s - want) <= (rel + 2 * HALF_F32) * want + 2.0 ** -149), f"{what}: scales"
+    # (a step of the smallest fp32 where the scale is tiny)
+    assert np.all(np.abs(s - want) <= (rel + absolute + 2 * HALF_F32) * want + 2.0 ** -149), f"{what}: scales"
     if fp8:
         mag, val = E4M3[q & 0x7F], np.abs(n) / s[:, None]
         assert np.all(((q & 0x7F) != 0x7F)), f"{what}: a code is NaN"
@@ -90,6 +93,6 @@ def check_codes(n, rel, q, s, fp8, what=""):
         mag, val, gap = np.abs(q.astype(np.float64)), np.abs(n) / s[:, None], 1.0
         assert np.all((np.sign(q) == np.sign(n)) | (q == 0)), f"{what}: signs"
     err = np.abs(mag - val)
-    bad = ~(err <= gap / 2 + 2 * (rel + 2 * HALF_F32) * np.abs(val) + 2.0 ** -20 * rel)
+    bad = ~(err <= gap / 2 + (2 * rel + absolute + 4 * HALF_F32) * val + 1.01 * absolute * (448 if fp8 else 127))
     bad[top <= 2.0 ** -120] = False                          # scales of a few bits: the codes' steps are theirs
     assert not bad.any(), f"{what}: {int(bad.sum())} codes are not the nearest, first at {np.argwhere(bad)[0]}"

@@ -5,7 +5,6 @@
 
 namespace w4a8 {
 
-int64_t dense_i8_workspace_bytes(int64_t M, int64_t, int64_t) { return 16 * M; }
 int64_t mlp_i8_workspace_bytes(int64_t M, int64_t, int64_t I) { return 5 * M * I; }
 hipError_t launch_dense_i8(const DenseArgs&, hipStream_t) { return hipErrorNoDevice; }
 hipError_t launch_mlp_i8(const MlpArgs&, hipStream_t) { return hipErrorNoDevice; }

@@ -45,7 +45,7 @@ def check_norm(n, xn, q, s, fp8, what, rel=NORM_REL, absolute=0.0):
     tol = tol + HALF_BF16 * (np.abs(n) + tol) + 2.0 ** -134   # (half a step of bf16's smallest)
     bad = ~(np.abs(f64(xn) - n) <= tol)
     assert not bad.any(), f"{what}: {int(bad.sum())} of xn off"
-    check_codes(n, rel + absolute, q.cpu().numpy(), f64(s), fp8, what)
+    check_codes(n, rel, absolute, q.cpu().numpy(), f64(s), fp8, what)
 
 
 SIZES = [(1, 8, 0), (1, 6144, 0), (3, 16, 8), (5, 64, 0), (4, 504, 8), (7, 512, 0), (6, 520, 0), (9, 1024, 16),
@@ -211,6 +211,33 @@ def test_graph_and_stream(T):
     torch.cuda.synchronize()
     for a, b in zip(other, eager):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("y,r", [("bf16", "bf16"), ("f32", "f32")])
+@pytest.mark.parametrize("T,H", [(300, 4096), (257, 4104), (300, 6144), (300, 8192), (300, 16384), (260, 20000),
+                                 (17000, 2056)])
+def test_many_rows(T, H, y, r):
+    """More rows than CUs, each number of threads to a row, and rows marked as read once (the largest)."""
+    g = np.random.Generator(np.random.PCG64(T + H))
+    base = rows(g, min(T, 300), H, y), rows(g, min(T, 300), H, r)
+    yt, rt = (b.repeat(-(-T // b.shape[0]), 1)[:T].contiguous() for b in base)
+    nw, pw = vec(g, H), vec(g, H)
+    say(f"residual_norm_quant T={T} H={H} {y} {r}")
+    got = ops.w4a8_moe_residual_norm_quant(yt, rt, nw, pw, r_scale=0.5)
+    n = base[0].shape[0]
+    want, tol = residual_ref(base[0], base[1], pw, None, None, 0.5)
+    bound = tol + (HALF_BF16 * (np.abs(want) + tol) if r == "bf16" else 0)
+    assert np.all(np.abs(f64(got[0][:n]) - want) <= bound)
+    ref = rms(want, f64(nw), EPS)
+    off = tol.max(1) / np.sqrt((want * want).mean(1) + EPS)
+    absolute = float((off * np.abs(f64(nw)).max() / np.abs(ref).max(1)).max())
+    check_norm(ref, got[1][:n], got[2][:n], got[3][:n], True, "next norm", NORM_REL + 1.01 * float(off.max()),
+               1.01 * absolute)
+    for t in got:                                            # the same rows again
+        for k in range(n, T - n + 1, n):
+            assert torch.equal(t[k:k + n], t[:n])
+    x8 = ops.w4a8_moe_norm_quant_i8(yt, nw, EPS)
+    check_norm(rms(f64(base[0]), f64(nw), EPS), x8[0][:n], x8[1][:n], x8[2][:n], False, "norm")
 
 
 def test_no_rows_and_largest():
