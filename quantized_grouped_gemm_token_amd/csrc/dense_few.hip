@@ -75,7 +75,7 @@ __global__ __launch_bounds__(kFewRowsThreads) void dense_few_kernel(const FewRow
   constexpr int kRows = kGated ? 8 : 16;       // outputs of a step
   using Lds = FewLds<kForm, kParts>;
   constexpr int kFewSlots = Lds::kSlots;
-  extern __shared__ __attribute__((aligned(16))) uint8_t sm[];   // the rings, then the waves' regions
+  __shared__ __attribute__((aligned(16))) uint8_t sm[Lds::kBytes];   // the rings, then the waves' regions
   __shared__ float row_s[16], row_f[16][3];   // down: a row's scale, what its values are divided by
   uint8_t* regions = sm + kFewRowsWaves * Lds::kRing;
   const DenseArgs& d = f.d;
@@ -303,15 +303,11 @@ hipError_t launch_few_steps(const FewRowsArgs& f, hipStream_t stream) {
   const int64_t outs = kForm == kFewGated ? f.I : f.d.N, rows = kForm == kFewGated ? 8 : 16;
   const int64_t steps = (outs + rows - 1) / rows;
   auto kernel = dense_few_kernel<kForm, GW, kParts>;
-  constexpr int kLds = FewLds<kForm, kParts>::kBytes;
-  static const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
-                                                  hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
-  if (e != hipSuccess) return e;
   // One workgroup on a CU at most, each the same number of steps: a second one would fetch the
   // activations again (16 x 6144 x 6144 10.5 against 12.6 us with two, 9000 x 5120 11.0 against
   // 12.6; 6144 x 2048 5.2 against 4.9).  Rings of 5, 6 or 8 units changed nothing.
   const int64_t rounds = (steps + 255) / 256;
-  hipLaunchKernelGGL(kernel, dim3((unsigned)((steps + rounds - 1) / rounds)), dim3(kFewRowsThreads), kLds, stream, f);
+  hipLaunchKernelGGL(kernel, dim3((unsigned)((steps + rounds - 1) / rounds)), dim3(kFewRowsThreads), 0, stream, f);
   return hipGetLastError();
 }
 

@@ -46,7 +46,7 @@ __global__ __launch_bounds__(64 * kWM * kWN) void dense_i8_kernel(const DenseArg
   constexpr int kSlot = (kBM + kBN) * kBK;
   constexpr int kALoads = kBM / 8 / kWaves, kWLoads = kBN / 8 / kWaves;    // instructions of 8 rows per wave
   constexpr int kScaleBytes = 4 * (2 * kBN + kBM);                         // w_scale, bias, a_scale of a tile
-  extern __shared__ __attribute__((aligned(16))) uint8_t sm[];             // the slots, two tiles' scales
+  __shared__ __attribute__((aligned(16))) uint8_t sm[kSlots * kSlot + 2 * kScaleBytes];   // the slots, two tiles' scales
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int lr = lane & 15, lq = lane >> 4;
   const int K = (int)d.K, steps = (K + kBK - 1) / kBK;
@@ -348,15 +348,9 @@ template <int kBM, int kBN, int kWM, int kWN, int kSlots, int kPerCu, int kOut, 
 hipError_t launch_tiles(const DenseArgs& d, int64_t I, float* act, hipStream_t stream) {
   const int64_t mb = (d.M + kBM - 1) / kBM, nb = (d.N + kBN - 1) / kBN;
   auto kernel = dense_i8_kernel<kBM, kBN, kWM, kWN, kSlots, kOut, kAdd>;
-  constexpr int kLds = kSlots * (kBM + kBN) * kBK + 2 * 4 * (2 * kBN + kBM);
-  static_assert(kPerCu * kLds <= 160 * 1024, "LDS");
-  if constexpr (kLds > 65536) {
-    static const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
-                                                    hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
-    if (e != hipSuccess) return e;
-  }
+  static_assert(kPerCu * (kSlots * (kBM + kBN) * kBK + 2 * 4 * (2 * kBN + kBM)) <= 160 * 1024, "LDS");
   const int64_t slots = 256 * kPerCu, tiles = mb * nb;
-  hipLaunchKernelGGL(kernel, dim3((unsigned)(tiles < slots ? tiles : slots)), dim3(64 * kWM * kWN), kLds, stream, d, I,
+  hipLaunchKernelGGL(kernel, dim3((unsigned)(tiles < slots ? tiles : slots)), dim3(64 * kWM * kWN), 0, stream, d, I,
                      act, (int)mb, (int)nb);
   return hipGetLastError();
 }

@@ -35,6 +35,14 @@ the steps as before (uses_few).  front, fused and scatter are about the steps on
 The call's results differ from the steps' by rounding; it fills none of buffers(T),
 and takes its workspace from torch's allocator at every forward (from the graph's
 pool in a captured one).
+
+A forward given codes (of w4a8_moe_norm_quant, or its _i8 form with row sums) takes them
+in place of quantizing x: its steps are route and permute, then the GEMMs.
+
+W8A8Mlp is the gated feed-forward block on 8-bit weights (a shared expert, a dense
+layer's), and MoEBlock the whole routed half of a decoder block: the norm before it with
+its codes, the routed experts, a shared expert added to their sum, the norm after it with
+gates and residual, and the next block's norm in the same pass.
 """
 from __future__ import annotations
 
@@ -113,6 +121,16 @@ class W4A8MoE:
         """The step names of a forward over T tokens, as its events are keyed: ("few",) or self.steps."""
         return ("few",) if self.uses_few(T, algo) else self.steps
 
+    CODES = torch.uint8                                   # the type of the quantized rows
+
+    def _given(self, codes, T):
+        # the GEMMs read rows of these by token numbers, which no later check sees
+        qx, sx = codes[:2]
+        dev = self.w13.device
+        ops._is(qx, "codes[0]", self.CODES, (T, self.H), dev)
+        ops._is(sx, "codes[1]", torch.float32, (T,), dev)
+        return codes
+
     def _forward_few(self, x, logits, y, y_dtype, events):
         # the call allocates its workspace: forwards on several streams, or captured
         # into several graphs, share none
@@ -128,17 +146,21 @@ class W4A8MoE:
 
     def forward(self, x: torch.Tensor, logits: torch.Tensor, y: torch.Tensor | None = None,
                 y_dtype: torch.dtype = torch.float32, algo: int = ops.W4A8_GG_AUTO,
-                events: dict | None = None) -> torch.Tensor:
+                events: dict | None = None, codes: tuple | None = None) -> torch.Tensor:
         """x bf16 [T, H], router logits fp32 [T, E] -> y [T, H].
 
         events, if given, maps step names (of steps_for(T, algo)) to (start, end) CUDA
         events that are recorded on the current stream around each step.
+        codes, if given, are the quantized rows (qx uint8 [T, H], sx fp32 [T]) that the experts
+        multiply, x's codes or a norm's before its rounding to x; the steps are then "route",
+        "permute" and those behind them, also for a few tokens.
         """
         T = x.shape[0]
-        if self.uses_few(T, algo):
+        if codes is None and self.uses_few(T, algo):
             return self._forward_few(x, logits, y, y_dtype, events)
         b = self.buffers(T)
         R = T * self.k
+        qx, sx = (b["qx"], b["sx"]) if codes is None else self._given(codes, T)
 
         def step(name, fn, *args):
             ev = events.get(name) if events else None
@@ -149,20 +171,21 @@ class W4A8MoE:
                 ev[1].record()
             return r
 
-        if self.front:
+        if self.front and codes is None:
             step("front", ops.w4a8_moe_front, x, logits, self.k, b["counter"], self.renormalize, False, b["qx"],
                  b["sx"], None, b["ids"], b["w"], b["offsets"], b["row_token"], b["inv_pos"], b["workspace"])
         else:
-            step("quant_act", ops.w4a8_moe_quant_act, x, b["qx"], b["sx"])
+            if codes is None:
+                step("quant_act", ops.w4a8_moe_quant_act, x, b["qx"], b["sx"])
             step("route", ops.w4a8_moe_route, logits, self.k, self.renormalize, b["ids"], b["w"])
             step("permute", ops.w4a8_moe_permute, b["ids"], self.E, b["offsets"], b["row_token"], b["inv_pos"],
                  b["workspace"])
         if self.fused:
-            step("gemm_gate_up", self.GEMM_SWIGLU, b["qx"], b["sx"], b["row_token"], b["offsets"],
+            step("gemm_gate_up", self.GEMM_SWIGLU, qx, sx, b["row_token"], b["offsets"],
                  self.w13, self.s13, R, b["act"], b["pmax"], algo)
             step("swiglu", ops.w4a8_moe_requant, b["act"], b["pmax"], b["qa"], b["sa"])
         else:
-            step("gemm_gate_up", self.GEMM, b["qx"], b["sx"], b["row_token"], b["offsets"],
+            step("gemm_gate_up", self.GEMM, qx, sx, b["row_token"], b["offsets"],
                  self.w13, self.s13, R, b["h"], algo)
             step("swiglu", ops.w4a8_moe_swiglu, b["h"], b["qa"], b["sa"])
         if self.uses_scatter(T):
@@ -198,6 +221,12 @@ class W4A8MoEChannel(W4A8MoE):
     """The per-channel INT4 x per-token INT8 variant: s13 [E, 2I] and s2 [E, H]
     are per-channel scales; steps 1, 4, 5 and 6 use the INT8 calls."""
     FEW = staticmethod(ops.w4a8_moe_few_i8_prepacked)
+    CODES = torch.int8
+
+    def _given(self, codes, T):
+        qx, sx, rx = super()._given(codes, T) if len(codes) == 3 else (*codes, None)
+        ops._is(rx, "codes[2]", torch.int32, (T,), self.w13.device)
+        return qx, sx, rx
 
     @staticmethod
     def prepack(w13, s13, w2, s2):
@@ -217,12 +246,14 @@ class W4A8MoEChannel(W4A8MoE):
 
     def forward(self, x: torch.Tensor, logits: torch.Tensor, y: torch.Tensor | None = None,
                 y_dtype: torch.dtype = torch.float32, algo: int = ops.W4A8_GG_AUTO,
-                events: dict | None = None) -> torch.Tensor:
+                events: dict | None = None, codes: tuple | None = None) -> torch.Tensor:
+        """As W4A8MoE.forward; codes are (qx int8 [T, H], sx fp32 [T], row sums int32 [T])."""
         T = x.shape[0]
-        if self.uses_few(T, algo):
+        if codes is None and self.uses_few(T, algo):
             return self._forward_few(x, logits, y, y_dtype, events)
         b = self.buffers(T)
         R = T * self.k
+        qx, sx, rx = (b["qx"], b["sx"], b["rx"]) if codes is None else self._given(codes, T)
 
         def step(name, fn, *args):
             ev = events.get(name) if events else None
@@ -233,20 +264,21 @@ class W4A8MoEChannel(W4A8MoE):
                 ev[1].record()
             return r
 
-        if self.front:
+        if self.front and codes is None:
             step("front", ops.w4a8_moe_front, x, logits, self.k, b["counter"], self.renormalize, True, b["qx"],
                  b["sx"], b["rx"], b["ids"], b["w"], b["offsets"], b["row_token"], b["inv_pos"], b["workspace"])
         else:
-            step("quant_act", ops.w4a8_moe_quant_act_i8, x, b["qx"], b["sx"], b["rx"])
+            if codes is None:
+                step("quant_act", ops.w4a8_moe_quant_act_i8, x, b["qx"], b["sx"], b["rx"])
             step("route", ops.w4a8_moe_route, logits, self.k, self.renormalize, b["ids"], b["w"])
             step("permute", ops.w4a8_moe_permute, b["ids"], self.E, b["offsets"], b["row_token"], b["inv_pos"],
                  b["workspace"])
         if self.fused:
-            step("gemm_gate_up", ops.w4a8_moe_grouped_gemm_swiglu_i8_prepacked, b["qx"], b["sx"], b["rx"],
+            step("gemm_gate_up", ops.w4a8_moe_grouped_gemm_swiglu_i8_prepacked, qx, sx, rx,
                  b["row_token"], b["offsets"], self.w13, self.s13, R, b["act"], b["pmax"], algo)
             step("swiglu", ops.w4a8_moe_requant_i8, b["act"], b["pmax"], b["qa"], b["sa"], b["ra"])
         else:
-            step("gemm_gate_up", ops.w4a8_moe_grouped_gemm_i8_prepacked, b["qx"], b["sx"], b["rx"],
+            step("gemm_gate_up", ops.w4a8_moe_grouped_gemm_i8_prepacked, qx, sx, rx,
                  b["row_token"], b["offsets"], self.w13, self.s13, b["h"], R, algo)
             step("swiglu", ops.w4a8_moe_swiglu_i8, b["h"], b["qa"], b["sa"], b["ra"])
         if self.uses_scatter(T):
@@ -279,3 +311,84 @@ class W4A8MoEMxfp4(W4A8MoE):
         w13b, s13b = ops.w4a8_moe_prepack_mxfp4(w13, s13)
         w2b, s2b = ops.w4a8_moe_prepack_mxfp4(w2, s2)
         return w13b, s13b, w2b, s2b
+
+
+class W8A8Mlp:
+    """The gated feed-forward block on int8 weights: w13 int8 [2I, H] (gate rows, then up rows) with fp32 scales
+    s13 [2I], w2 int8 [H, I] with s2 [H] (w4a8_moe_quant_act_i8 makes both from bf16 rows)."""
+
+    def __init__(self, w13: torch.Tensor, s13: torch.Tensor, w2: torch.Tensor, s2: torch.Tensor):
+        if w13.dim() != 2 or w2.dim() != 2 or w13.shape[0] != 2 * w2.shape[1] or w13.shape[1] != w2.shape[0]:
+            raise ValueError("w13 must be [2I, H] and w2 [H, I]")
+        self.w13, self.s13, self.w2, self.s2 = w13, s13, w2, s2
+        self.H, self.I = w2.shape
+
+    def forward(self, q: torch.Tensor, s: torch.Tensor, add: torch.Tensor | None = None,
+                y: torch.Tensor | None = None, y_dtype: torch.dtype = torch.float32) -> torch.Tensor:
+        """int8 codes q [T, H] with scales s fp32 [T], plus add [T, H] (it may be y) -> y [T, H].  The workspace is
+        the call's own: forwards on several streams, or captured into several graphs, share none."""
+        return ops.w4a8_moe_mlp_i8(q, s, self.w13, self.s13, self.w2, self.s2, add, y, y_dtype)
+
+    __call__ = forward
+
+
+class MoEBlock:
+    """The routed half of a decoder block on a residual stream r [T, H] (fp32 or bf16):
+
+        xn = norm(r) with weight (fp32 [H]), and its 8-bit codes
+        y = moe(xn, router(xn)) + shared(codes)
+        out = r_scale r + token_gate gate norm(y)          (norm with post_weight; y as it is without one)
+
+    moe is a W4A8MoE (any form), router a function from xn (bf16 [T, H]) to the router's logits (fp32 [T, E]), shared
+    a W8A8Mlp or None, post_weight and gate fp32 [H] or None.  The codes are int8 where there is a shared expert (the
+    per-channel experts take them too) or the experts are per-channel, else FP8; experts of the other type quantize
+    xn themselves, as they do for a few tokens (moe.few)."""
+
+    def __init__(self, moe: W4A8MoE, weight: torch.Tensor, shared: W8A8Mlp | None = None,
+                 post_weight: torch.Tensor | None = None, gate: torch.Tensor | None = None, r_scale: float = 1.0,
+                 eps: float = 1e-6):
+        if shared is not None and shared.H != moe.H:
+            raise ValueError(f"the shared expert's hidden size {shared.H} must be the experts' {moe.H}")
+        self.moe, self.weight, self.shared = moe, weight, shared
+        self.post_weight, self.gate, self.r_scale, self.eps = post_weight, gate, r_scale, eps
+        self.channel = isinstance(moe, W4A8MoEChannel)
+        self.int8 = shared is not None or self.channel
+
+    def before(self, r: torch.Tensor) -> tuple:
+        """(xn, q, s, row sums or None) of the norm before this block."""
+        if not self.int8:
+            return (*ops.w4a8_moe_norm_quant(r, self.weight, self.eps), None)
+        rowsum = self._rowsum(r)
+        return (*ops.w4a8_moe_norm_quant_i8(r, self.weight, self.eps, rowsum=rowsum), rowsum)
+
+    def _rowsum(self, r):
+        return r.new_empty((r.shape[0],), dtype=torch.int32) if self.channel else None
+
+    def forward(self, r: torch.Tensor, router, token_gate: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                normed: tuple | None = None, following: MoEBlock | None = None):
+        """The residual stream behind the block (in out if given; it may be r).  normed, if given, is what before(r)
+        returns.  With following (the block that takes the result) its before() is made in the same pass: returns
+        (out, normed) then."""
+        xn, q, s, rowsum = self.before(r) if normed is None else normed
+        logits = router(xn)
+        moe = self.moe
+        if moe.uses_few(xn.shape[0]) or self.int8 != self.channel:
+            y = moe(xn, logits)
+        else:
+            y = moe(xn, logits, codes=(q, s, rowsum) if self.channel else (q, s))
+        if self.shared is not None:
+            self.shared(q, s, add=y, y=y)
+        how = dict(post_weight=self.post_weight, gate=self.gate, token_gate=token_gate, r_scale=self.r_scale,
+                   eps=self.eps, out=out)
+        if following is None:
+            return ops.w4a8_moe_residual_norm(y, r, **how)
+        if following.eps != self.eps:
+            raise ValueError("the norms of one pass have one eps")
+        if not following.int8:
+            out, *coded = ops.w4a8_moe_residual_norm_quant(y, r, following.weight, **how)
+            return out, (*coded, None)
+        rowsum = following._rowsum(r)
+        out, *coded = ops.w4a8_moe_residual_norm_quant_i8(y, r, following.weight, rowsum=rowsum, **how)
+        return out, (*coded, rowsum)
+
+    __call__ = forward

@@ -85,6 +85,48 @@ def test_bias_and_addend(M, N, K, pad, y):
     assert torch.equal(inplace, got)
 
 
+# rows and outputs past every tile's edge (64 x 64, 128 x 64, 128 x 128, 256 x 128 and 256 x 256), K of an odd number
+# of steps, few K steps, and for 16 rows and fewer each number of K units of a wave
+@pytest.mark.parametrize("M,N,K", [(100, 333, 1008), (500, 2999, 400), (500, 6011, 144), (1000, 6011, 208),
+                                   (3001, 3999, 16), (2999, 6001, 400), (4097, 8193, 272), (1025, 12290, 1040),
+                                   (3, 260, 2064), (16, 333, 4112), (2, 100, 8208), (7, 77, 12288), (16, 129, 12304),
+                                   (9, 4100, 16384), (1, 300, 16400), (16, 35, 40000)])
+@pytest.mark.parametrize("y", ["f32", "bf16"])
+def test_every_tile(M, N, K, y):
+    a, sa, w, sw = _large(M, N, K, M + N + K)
+    gen = torch.Generator(device=DEV).manual_seed(N)
+    bias = torch.randn(N, device=DEV, generator=gen)
+    buf = torch.randn((M + 2) * N, device=DEV, generator=gen).to(TYPES[y])
+    edges = buf[:N].clone(), buf[-N:].clone()
+    add = buf[N:-N].view(M, N)
+    say(f"dense_i8 M={M} N={N} K={K} {y}")
+    sums = a.double() @ w.double().t()
+    assert torch.equal(ops.w4a8_moe_dense_i8(a, sa, w, sw, y_dtype=TYPES[y]),
+                       (sums.float() * sa[:, None] * sw).to(TYPES[y]))
+    # with bias and addend check_dense's bound: three half steps of the product, one of each sum, one of bf16
+    p = sums * sa.double()[:, None] * sw.double()
+    first = p + bias
+    want = first + add
+    tol = 1.001 * 2.0 ** -24 * (3 * p.abs() + first.abs() + want.abs()) + 2.0 ** -149
+    if y == "bf16":
+        tol += 2.0 ** -8 * (want.abs() + tol)
+    assert ops.w4a8_moe_dense_i8(a, sa, w, sw, bias=bias, add=add, y=add) is add
+    assert bool(((add - want).abs() <= tol).all())
+    assert torch.equal(buf[:N], edges[0]) and torch.equal(buf[-N:], edges[1])
+
+
+@pytest.mark.parametrize("M,H,I", [(2, 64, 20480), (16, 32, 12288), (5, 20480, 128), (11, 12304, 256), (1, 8208, 640),
+                                   (16, 80, 65536), (40, 80, 20480)])
+def test_gated_block_of_long_rows(M, H, I):
+    """The few-row kernels' parts of K, on either side of the activation."""
+    g = np.random.Generator(np.random.PCG64(M + H + I))
+    a, w13, w2 = codes(g, M, H), codes(g, 2 * I, H), codes(g, H, I)
+    sa, s13, s2 = scales(g, M, H), scales(g, 2 * I, H), scales(g, H, I)
+    say(f"mlp_i8 M={M} H={H} I={I}")
+    got = ops.w4a8_moe_mlp_i8(dev(a), dev(sa), dev(w13), dev(s13), dev(w2), dev(s2))
+    check_mlp(f64(got), a, sa, w13, s13, w2, s2, None, False, f"M={M} H={H} I={I}")
+
+
 def test_extreme_codes_and_longest_rows():
     """-128 everywhere over the longest rows: the largest sum, 2^14 (2^17 - 16), is exact."""
     K = (1 << 17) - 16
