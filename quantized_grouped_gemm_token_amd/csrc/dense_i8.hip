@@ -72,6 +72,11 @@ __global__ __launch_bounds__(64 * kWM * kWN) void dense_i8_kernel(const DenseArg
   static_assert(kBoth || !kGated || kWLoads <= 2, "gate and up rows");
   __amdgpu_buffer_rsrc_t ra, rw0, rw1;
   int64_t m0 = 0, n0 = 0;
+  // Column blocks of the largest tiles begin at K steps of their own, each one further, and turn
+  // over K (sums of integers do not care): their loads then meet on fewer memory channels.  8192 x
+  // 12288 x 6144 462 to 454 us, 4096 x 6144 x 6144 133 to 131; the smaller tiles lose 1 to 4%.
+  constexpr bool kTurns = kBM * kBN == 65536;
+  int turn = 0;
 
   // Tile t of the workgroups' order: workgroups go to the 8 XCDs in turn, and each XCD takes a
   // window of neighbouring tiles.  The tiles go in groups of 4 row blocks that walk the column
@@ -80,6 +85,7 @@ __global__ __launch_bounds__(64 * kWM * kWN) void dense_i8_kernel(const DenseArg
   auto point = [&](int t, int par) {
     const int per = 4 * nblocks, group = t / per, gm = min(4, mblocks - 4 * group), in = t - group * per;
     m0 = (int64_t)(4 * group + in % gm) * kBM, n0 = (int64_t)(in / gm) * kBN;
+    if (kTurns && K % kBK == 0) turn = (in / gm) % steps;      // (a part of a step stays the last)
     const int rows = (int)min((int64_t)kBM, d.M - m0), cols = (int)min((int64_t)kBN, d.N - n0);
     ra = uniform_rsrc(d.a + m0 * d.ld_a, (rows - 1) * (int)d.ld_a + K);
     const int64_t c0 = kGated ? n0 / 2 : n0;
@@ -102,7 +108,7 @@ __global__ __launch_bounds__(64 * kWM * kWN) void dense_i8_kernel(const DenseArg
   };
   constexpr int kLoads = kALoads + kWLoads;
   auto load = [&](int kt, int q) {                            // load q of the wave's kLoads of step kt
-    const uint32_t k = (uint32_t)(kt * kBK);
+    const uint32_t k = (uint32_t)((kTurns && kt + turn >= steps ? kt + turn - steps : kt + turn) * kBK);
     uint8_t* slot = &sm[(kt % kSlots) * kSlot];
     if (q < kALoads) {
       dma16(ra, aoff[q], k, slot + 8 * (kALoads * wave + q) * kBK);
