@@ -45,7 +45,8 @@ __global__ __launch_bounds__(64 * kWM * kWN) void dense_i8_kernel(const DenseArg
   constexpr int WM = kBM / kWM, WN = kBN / kWN, FM = WM / 16, FN = WN / 16;
   constexpr int kSlot = (kBM + kBN) * kBK;
   constexpr int kALoads = kBM / 8 / kWaves, kWLoads = kBN / 8 / kWaves;    // instructions of 8 rows per wave
-  constexpr int kScaleBytes = 4 * (2 * kBN + kBM);                         // w_scale, bias, a_scale of a tile
+  constexpr int kCols = kBN < 64 ? 64 : kBN;
+  constexpr int kScaleBytes = 4 * (2 * kCols + kBM);                       // w_scale, bias, a_scale of a tile
   __shared__ __attribute__((aligned(16))) uint8_t sm[kSlots * kSlot + 2 * kScaleBytes];   // the slots, two tiles' scales
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int lr = lane & 15, lq = lane >> 4;
@@ -95,16 +96,16 @@ __global__ __launch_bounds__(64 * kWM * kWN) void dense_i8_kernel(const DenseArg
     if (kBoth) rw1 = uniform_rsrc(d.w + (I + c0) * K, wrows * K);
     // scales of the tile: 64 words to an instruction
     uint8_t* sc = &sm[kSlots * kSlot + par * kScaleBytes];
-    for (int c = wave; c < kBN / 64; c += kWaves) {
+    for (int c = wave; c < kCols / 64; c += kWaves) {
       // gated: the gate and up rows 32 c .. +31 of the tile's act columns, by 16
       const uint32_t o = kGated ? (uint32_t)(32 * c + 16 * (lq >> 1) + lr + (lq & 1) * (int)I) * 4u
                                 : (uint32_t)(64 * c + lane) * 4u;
       const int bytes = kGated ? (int)(I + wrows) * 4 : cols * 4;
       dma4(uniform_rsrc(d.w_scale + c0, bytes), o, 0, sc + 256 * c);
-      if (!kGated && d.bias) dma4(uniform_rsrc(d.bias + n0, cols * 4), o, 0, sc + 4 * kBN + 256 * c);
+      if (!kGated && d.bias) dma4(uniform_rsrc(d.bias + n0, cols * 4), o, 0, sc + 4 * kCols + 256 * c);
     }
     for (int c = wave; c < kBM / 64; c += kWaves)
-      dma4(uniform_rsrc(d.a_scale + m0, rows * 4), (uint32_t)(64 * c + lane) * 4u, 0, sc + 8 * kBN + 256 * c);
+      dma4(uniform_rsrc(d.a_scale + m0, rows * 4), (uint32_t)(64 * c + lane) * 4u, 0, sc + 8 * kCols + 256 * c);
   };
   constexpr int kLoads = kALoads + kWLoads;
   auto load = [&](int kt, int q) {                            // load q of the wave's kLoads of step kt
@@ -140,8 +141,8 @@ __global__ __launch_bounds__(64 * kWM * kWN) void dense_i8_kernel(const DenseArg
   const int start = grid % 8 == 0 ? first : (int)blockIdx.x;
   int par = 0;
   if (!kGated && !d.bias) {                                    // a bias of zero
-    for (int c = tid; c < 2 * kBN; c += 64 * kWaves)
-      reinterpret_cast<float*>(&sm[kSlots * kSlot + (c / kBN) * kScaleBytes])[kBN + c % kBN] = 0.0f;
+    for (int c = tid; c < 2 * kCols; c += 64 * kWaves)
+      reinterpret_cast<float*>(&sm[kSlots * kSlot + (c / kCols) * kScaleBytes])[kCols + c % kCols] = 0.0f;
     __builtin_amdgcn_s_waitcnt(0xC07F);                        // (read after the barriers of the first tile)
   }
   point(start, par);
@@ -228,7 +229,7 @@ __global__ __launch_bounds__(64 * kWM * kWN) void dense_i8_kernel(const DenseArg
     int lr = lane & 15, lq = lane >> 4;
     asm volatile("" : "+v"(lr), "+v"(lq));
     const float* sc = reinterpret_cast<const float*>(&sm[kSlots * kSlot + par * kScaleBytes]) + wn + 4 * lq;
-    const float* as = reinterpret_cast<const float*>(&sm[kSlots * kSlot + par * kScaleBytes]) + 2 * kBN + wm + lr;
+    const float* as = reinterpret_cast<const float*>(&sm[kSlots * kSlot + par * kScaleBytes]) + 2 * kCols + wm + lr;
     const int mleft = (int)min(d.M - tm0 - wm, (int64_t)WM);  // rows of the wave
     const int nleft = (int)min(d.N - tn0 - wn, (int64_t)WN);  // columns of the wave
     const int64_t row0 = tm0 + wm + lr;
@@ -241,7 +242,7 @@ __global__ __launch_bounds__(64 * kWM * kWN) void dense_i8_kernel(const DenseArg
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         ws[e] = lds_load<f32x4>(sc + 16 * (j + e));
-        if constexpr (!kGated) bs[e] = lds_load<f32x4>(sc + kBN + 16 * (j + e));
+        if constexpr (!kGated) bs[e] = lds_load<f32x4>(sc + kCols + 16 * (j + e));
       }
       const bool whole = 16 * j + 32 <= nleft;                 // (the same for the whole wave)
 #pragma unroll
@@ -354,7 +355,7 @@ template <int kBM, int kBN, int kWM, int kWN, int kSlots, int kPerCu, int kOut, 
 hipError_t launch_tiles(const DenseArgs& d, int64_t I, float* act, hipStream_t stream) {
   const int64_t mb = (d.M + kBM - 1) / kBM, nb = (d.N + kBN - 1) / kBN;
   auto kernel = dense_i8_kernel<kBM, kBN, kWM, kWN, kSlots, kOut, kAdd>;
-  static_assert(kPerCu * (kSlots * (kBM + kBN) * kBK + 2 * 4 * (2 * kBN + kBM)) <= 160 * 1024, "LDS");
+  static_assert(kPerCu * (kSlots * (kBM + kBN) * kBK + 2 * 4 * (2 * (kBN < 64 ? 64 : kBN) + kBM)) <= 160 * 1024, "LDS");
   const int64_t slots = 256 * kPerCu, tiles = mb * nb;
   hipLaunchKernelGGL(kernel, dim3((unsigned)(tiles < slots ? tiles : slots)), dim3(64 * kWM * kWN), 0, stream, d, I,
                      act, (int)mb, (int)nb);
@@ -362,9 +363,12 @@ hipError_t launch_tiles(const DenseArgs& d, int64_t I, float* act, hipStream_t s
 }
 
 // The tile that ends first: the tiles go over the 256 CUs in rounds, and a round costs the tile's
-// time per step.  Measured at K = 6144 (us a step, one tile on each CU): 64 x 64 0.20, 128 x 64
+// time per step.  Measured at K = 6144 (us a step, one tile on each CU): 64 x 32 0.19, 64 x 64 0.20, 128 x 64
 // 0.33, 128 x 128 0.46, 256 x 128 0.63 to 0.84, 256 x 256 1.15 to 1.35 (the larger the nearer to
-// the card's power limit).  6144 outputs (us; the tile chosen first, then the next best): 128 rows
+// the card's power limit).  A CU reads weights from memory at 25 to 35 GB/s however many loads it
+// has in flight, so the narrow tile, up to one for each CU, is for few rows: 64 x 6144 x 6144 10.8 us against 11.7 with
+// 64 x 64, and 15.0 against 18.7 where the weights come from memory and not from a cache (20 rows 11.4
+// against 15.9; of 8, 6 and 4 slots, 8).  6144 outputs (us; the tile chosen first, then the next best): 128 rows
 // 11.7 with 64 x 64, 16.4 with 128 x 64; 256 rows 17.2 with 128 x 64, 19.5 with 64 x 64; 512 rows
 // 22.8 with 128 x 128, 32.7 with 128 x 64; 1024 rows 37.8 with 256 x 128, 42.3 with 128 x 128; 2048
 // rows 64.9 with 256 x 256, 73.3 with 128 x 128; 3000 rows 113.7 with 256 x 128, 129.9 with 256 x 256.
@@ -373,16 +377,17 @@ hipError_t launch_product(const DenseArgs& d, int64_t I, float* act, hipStream_t
   auto cost = [&](int bm, int bn, double step) {
     return step * (double)((((d.M + bm - 1) / bm) * ((d.N + bn - 1) / bn) + 255) / 256);
   };
-  const double c[5] = {cost(64, 64, 0.20), cost(128, 64, 0.33), cost(128, 128, 0.46), cost(256, 128, 0.75),
-                       cost(256, 256, 1.32)};
+  const double c[6] = {cost(64, 32, 0.19),   cost(64, 64, 0.20),   cost(128, 64, 0.33),
+                       cost(128, 128, 0.46), cost(256, 128, 0.75), cost(256, 256, 1.32)};
   int best = 0;
-  for (int i = 1; i < 5; ++i)
+  for (int i = 1; i < 6; ++i)
     if (c[i] < c[best]) best = i;
   switch (best) {
-    case 0: return launch_tiles<64, 64, 2, 2, 4, 2, kOut, kAdd>(d, I, act, stream);
-    case 1: return launch_tiles<128, 64, 2, 2, 4, 1, kOut, kAdd>(d, I, act, stream);
-    case 2: return launch_tiles<128, 128, 2, 2, 4, 1, kOut, kAdd>(d, I, act, stream);
-    case 3: return launch_tiles<256, 128, 4, 2, 3, 1, kOut, kAdd>(d, I, act, stream);
+    case 0: return launch_tiles<64, 32, 4, 1, 8, 1, kOut, kAdd>(d, I, act, stream);
+    case 1: return launch_tiles<64, 64, 2, 2, 4, 2, kOut, kAdd>(d, I, act, stream);
+    case 2: return launch_tiles<128, 64, 2, 2, 4, 1, kOut, kAdd>(d, I, act, stream);
+    case 3: return launch_tiles<128, 128, 2, 2, 4, 1, kOut, kAdd>(d, I, act, stream);
+    case 4: return launch_tiles<256, 128, 4, 2, 3, 1, kOut, kAdd>(d, I, act, stream);
     default: return launch_tiles<256, 256, 2, 4, 2, 1, kOut, kAdd>(d, I, act, stream);
   }
 }
