@@ -9,6 +9,12 @@
 // activations stay in registers as operands of 16x16x64 INT8 products; the eight partial 16x16
 // tiles (int32, exact) are summed in LDS at the end of a step, with the workgroup's one barrier.
 //
+// One workgroup a CU, persistent.  131072 x 6144 with one row takes 115 us (7.0 TB/s, what a plain
+// read of whole lines reaches); 6144 x 6144 9.2 us with one row and 10.6 with 16, of which 3 are the
+// launch and the first loads' way; 12288 x 6144 14.4 us.  Weights in a cache and 16 rows of more than 8192 outputs
+// would go faster in the tiled kernel (16 x 12288 x 6144 13.2 against 15.7 us); read from memory, as a
+// model's weights are, they do not (17.4 against 16.6; 16 x 24576 x 6144 31.9 against 27.3).
+//
 // The gated block is two kernels: the gated product leaves act (fp32) and the maxima of 8
 // columns of it; the down product's workgroups quantize act themselves, each wave its part of K,
 // while their weights are in flight.

@@ -1,8 +1,24 @@
 // Dense products in 8-bit integers and the gated feed-forward block on them (w4a8_block.h).
 //
 // One workgroup of kWM x kWN waves computes a tile of kBM rows x kBN weight rows (output
-// columns), in 16x16x64 INT8 products with int32 sums.  K goes in steps of 128 bytes through
-// two LDS slots, filled by loads straight into LDS one step ahead.
+// columns), in 16x16x64 INT8 products with int32 sums (exact, so K may be taken in any order).  K
+// goes in steps of 128 bytes, a cache line of each row, through a ring of kSlots slots in LDS that
+// loads straight into LDS fill kSlots - 1 steps ahead; operands are read from LDS four blocks of
+// 16 rows ahead of their products, with one barrier a step.  Workgroups stay for all their tiles
+// (a multiple of 256): a tile's first loads are issued ahead of the last one's epilogue.
+//
+// What bounds it.  Many rows (256 x 256): the card's power.  The INT8 products alone, from registers
+// of random codes, run at 3250 to 3750 TOP/s (4530 to 4670 on zeros, the clock being held); 8192 x
+// 12288 x 6144 takes 454 to 481 us, 2570 to 2720 TOP/s with loads, LDS and epilogue (zeros: 382 us).
+// The smaller tiles: what a CU gets from its L2 (130 to 150 GB/s), 100 to 300 rows the latency of the
+// loads at a step each (128 x 6144 x 6144 11.5 us in 192 tiles of 64 x 64).  Weights that come
+// from memory reach one CU at 25 to 35 GB/s.
+//
+// Measured and not taken, 8192 x 12288 x 6144 unless named: 4 waves of 128 x 128 (593 against 532
+// us at that stage), steps of 64 bytes in 4 slots (half lines double the L2's requests: 503
+// against 484), lines touched ahead into L2 (482 against 472), wave priorities, XCDs out of step and
+// nontemporal stores (nothing); K split over workgroups with a second kernel for the sums (128 x
+// 6144 x 6144 16.4 against 11.7); tiles of 128 x 32, 64 x 128 and 128 x 256.
 #include "block.hpp"
 #include "gemm_common.hpp"
 #include "lds_dma.hpp"
@@ -236,29 +252,34 @@ __global__ __launch_bounds__(64 * kWM * kWN) void dense_i8_kernel(const DenseArg
     float sa[FM];
 #pragma unroll
     for (int i = 0; i < FM; ++i) sa[i] = as[16 * i];
+    constexpr bool kBf16 = kOut == kOutBf16;
+    using E = std::conditional_t<kBf16, uint16_t, float>;
+    using Four = std::conditional_t<kBf16, uint2, f32x4>;      // 4 values of y's type
+    // (the column blocks of a row one after the other: whole lines of y and of the addend, 8192 x
+    // 6144 x 1024 54.6 us, row blocks one after the other 62.2; with an addend 88.7 and 94.9.
+    // Addends read 2 to 8 blocks ahead, or touched during the products, gave 92 to 104: they
+    // come at the rate that memory has for them and the results together.)
+    f32x4 ws[FN], bs[kGated ? 1 : FN];
 #pragma unroll
-    for (int j = 0; j < FN; j += 2) {                          // two column blocks: gate and up, or 32 outputs
-      f32x4 ws[2], bs[2];
+    for (int j = 0; j < FN; ++j) {
+      ws[j] = lds_load<f32x4>(sc + 16 * j);
+      if constexpr (!kGated) bs[j] = lds_load<f32x4>(sc + kCols + 16 * j);
+    }
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        ws[e] = lds_load<f32x4>(sc + 16 * (j + e));
-        if constexpr (!kGated) bs[e] = lds_load<f32x4>(sc + kCols + 16 * (j + e));
-      }
-      const bool whole = 16 * j + 32 <= nleft;                 // (the same for the whole wave)
+    for (int i = 0; i < FM; ++i) {
+      const bool live = 16 * i + lr < mleft;
 #pragma unroll
-      for (int i = 0; i < FM; ++i) {
-        const bool live = 16 * i + lr < mleft;
+      for (int j = 0; j < FN; j += 2) {                        // two column blocks: gate and up, or 32 outputs
+        const bool whole = 16 * j + 32 <= nleft;               // (the same for the whole wave)
         if constexpr (kGated) {
           f32x4 o;
 #pragma unroll
           for (int v = 0; v < 4; ++v)
-            o[v] = silu_mul((float)acc[i][j][v] * sa[i] * ws[0][v], (float)acc[i][j + 1][v] * sa[i] * ws[1][v]);
+            o[v] = silu_mul((float)acc[i][j][v] * sa[i] * ws[j][v], (float)acc[i][j + 1][v] * sa[i] * ws[j + 1][v]);
           // (a block of 32 columns is all inside the 2 I, or none)
           if (live && whole)
             *reinterpret_cast<f32x4*>(act + (row0 + 16 * i) * I + (tn0 + wn) / 2 + 8 * j + 4 * lq) = o;
         } else {
-          constexpr bool kBf16 = kOut == kOutBf16;
-          using E = std::conditional_t<kBf16, uint16_t, float>;
           const int64_t at = (row0 + 16 * i) * d.N + tn0 + wn + 16 * j;
           const E* add = static_cast<const E*>(d.add) + at;
           E* y = static_cast<E*>(d.y) + at;
@@ -266,20 +287,21 @@ __global__ __launch_bounds__(64 * kWM * kWN) void dense_i8_kernel(const DenseArg
 #pragma unroll
           for (int e = 0; e < 2; ++e)
 #pragma unroll
-            for (int v = 0; v < 4; ++v) o[e][v] = (float)acc[i][j + e][v] * sa[i] * ws[e][v] + bs[e][v];
+            for (int v = 0; v < 4; ++v) o[e][v] = (float)acc[i][j + e][v] * sa[i] * ws[j + e][v] + bs[j + e][v];
           if (whole) {
-            if (kAdd && live) {
+            if constexpr (kAdd) {
+              Four w[2];
+              if (live) {
+                __builtin_memcpy(&w[0], add + 4 * lq, sizeof(Four));
+                __builtin_memcpy(&w[1], add + 16 + 4 * lq, sizeof(Four));
+              }
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
                 if constexpr (kBf16) {
-                  uint2 w;
-                  __builtin_memcpy(&w, add + 16 * e + 4 * lq, 8);
-                  o[e][0] += bf16_lo(w.x), o[e][1] += bf16_hi(w.x), o[e][2] += bf16_lo(w.y), o[e][3] += bf16_hi(w.y);
+                  o[e][0] += bf16_lo(w[e].x), o[e][1] += bf16_hi(w[e].x), o[e][2] += bf16_lo(w[e].y), o[e][3] += bf16_hi(w[e].y);
                 } else {
-                  f32x4 w;
-                  __builtin_memcpy(&w, add + 16 * e + 4 * lq, 16);
 #pragma unroll
-                  for (int v = 0; v < 4; ++v) o[e][v] += w[v];
+                  for (int v = 0; v < 4; ++v) o[e][v] += w[e][v];
                 }
               }
             }
