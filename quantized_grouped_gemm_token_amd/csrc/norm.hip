@@ -18,28 +18,51 @@
 
 namespace w4a8 {
 
-// all values of a group of kThr threads; a buffer serves one reduction
-template <int kThr, typename F>
-__device__ __forceinline__ float group_reduce(float v, float* red, F wave, float (*join)(float, float)) {
-  v = wave(v);
-  if constexpr (kThr > kWave) {
-    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
-    __syncthreads();
-    v = red[0];
-#pragma unroll
-    for (int w = 1; w < kThr / kWave; ++w) v = join(v, red[w]);
+// A value of another lane of the row of 16 (DPP).
+template <int kCtrl>
+__device__ __forceinline__ float dpp(float v) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), kCtrl, 0xf, 0xf, false));
+}
+struct Sum {
+  static __device__ __forceinline__ float of(float a, float b) { return a + b; }
+};
+struct Max {
+  static __device__ __forceinline__ float of(float a, float b) { return fmaxf(a, b); }
+};
+// The reduction of kLanes neighbouring lanes in each of them, in registers: quads by their
+// permutations, rows of 16 by rotations, rows by swaps (with shuffles through LDS a norm of one row
+// takes 4.8 us, so 3.7).
+template <typename Op, int kLanes>
+__device__ __forceinline__ float lanes_reduce(float v) {
+  if constexpr (kLanes > 1) v = Op::of(v, dpp<0xB1>(v));
+  if constexpr (kLanes > 2) v = Op::of(v, dpp<0x4E>(v));
+  if constexpr (kLanes > 4) v = Op::of(v, dpp<0x124>(v));
+  if constexpr (kLanes > 8) v = Op::of(v, dpp<0x128>(v));
+  if constexpr (kLanes > 16) {
+    const auto s = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = Op::of(__uint_as_float(s[0]), __uint_as_float(s[1]));
+  }
+  if constexpr (kLanes > 32) {
+    const auto s = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = Op::of(__uint_as_float(s[0]), __uint_as_float(s[1]));
   }
   return v;
 }
-__device__ __forceinline__ float join_sum(float a, float b) { return a + b; }
-__device__ __forceinline__ float join_max(float a, float b) { return fmaxf(a, b); }
-template <int kThr>
-__device__ __forceinline__ float group_sum(float v, float* red) {
-  return group_reduce<kThr>(v, red, [](float x) { return wave_sum(x); }, join_sum);
+
+// all values of a group of kThr threads; a buffer serves one reduction
+template <int kThr, typename Op>
+__device__ __forceinline__ float group_reduce(float v, float* red) {
+  v = lanes_reduce<Op, kWave>(v);
+  if constexpr (kThr > kWave) {
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+    __syncthreads();
+    v = lanes_reduce<Op, kThr / kWave>(red[threadIdx.x % (kThr / kWave)]);
+  }
+  return v;
 }
 template <int kThr>
-__device__ __forceinline__ float group_max(float v, float* red) {
-  return group_reduce<kThr>(v, red, [](float x) { return wave_max(x); }, join_max);
+__device__ __forceinline__ float group_sum(float v, float* red) {
+  return group_reduce<kThr, Sum>(v, red);
 }
 
 // 8 values of a row as they lie in memory, and as fp32
@@ -125,11 +148,28 @@ __device__ __forceinline__ RowNorm row_norm(float (&v)[kPer][8], float H, float 
   return RowNorm{__builtin_amdgcn_rsqf(ss / H), ss < INFINITY};
 }
 
+// the largest value of a group, held as a sum of two: the larger m, of equal ones the larger rest,
+// which is only asked for where m is a wave's largest
+template <int kThr, typename F>
+__device__ __forceinline__ float2 group_max_pair(float m, F rest_of, float* red) {
+  float top = lanes_reduce<Max, kWave>(m);
+  float rest = lanes_reduce<Max, kWave>(m == top ? rest_of(m) : -INFINITY);
+  if constexpr (kThr > kWave) {
+    float2* r = reinterpret_cast<float2*>(red);
+    if ((threadIdx.x & 63) == 0) r[threadIdx.x >> 6] = make_float2(top, rest);
+    __syncthreads();
+    const float2 o = r[threadIdx.x % (kThr / kWave)];
+    top = lanes_reduce<Max, kThr / kWave>(o.x);
+    rest = lanes_reduce<Max, kThr / kWave>(o.x == top ? o.y : -INFINITY);
+  }
+  return make_float2(top, rest);
+}
+
 // kRes: with r (the residual form).  kNt: rows and results are marked as read and written once.  A
 // block holds one group, or four of a wave.
 template <int kThr, int kPer, bool kRes, int kCodes, bool kNt>
 __global__ __launch_bounds__(kThr < 256 ? 256 : kThr) void norm_kernel(const NormArgs n) {
-  __shared__ float red[5][16];
+  __shared__ __attribute__((aligned(8))) float red[6][16];    // (the last two for one reduction of pairs)
   constexpr int kGroups = kThr < 256 ? 256 / kThr : 1;
   const int tid = kGroups > 1 ? threadIdx.x % kThr : threadIdx.x;
   const int64_t t = (int64_t)blockIdx.x * kGroups + (kGroups > 1 ? threadIdx.x / kThr : 0);
@@ -187,16 +227,18 @@ __global__ __launch_bounds__(kThr < 256 ? 256 : kThr) void norm_kernel(const Nor
     if (!n.weight) return;
   }
   // n = f x weight, with f = g 2^e: the products (2^e x) weight are taken exactly, as a sum of two
-  // fp32 values, and g, which every quotient n / max |n| lacks, only enters xn and the scale.  So a
-  // code is the nearest to the row's true quotient, where three rounded products and a rounded
-  // quotient would put it on the other side of a border a few times in a million.
+  // fp32 values, and g, which every quotient n / max |n| lacks, only enters xn and the scale.  The
+  // largest product is taken exactly too, and a quotient that fp32 rounds to a border between two
+  // codes leaves it for its own side.  So a code is the nearest to the row's true quotient
+  // (rounded products and quotients put 0.8 of a million on the other side of a border).
   const RowNorm r = row_norm<kThr, kPer>(v, H, n.eps, red[2], red[3]);
   fine &= r.fine;
   const float e2 = __uint_as_float(__float_as_uint(r.f) & 0x7f800000u), g = r.f / e2;
-  float lo[kCodes != kCodesNone ? kPer : 1][8], m = 0.0f;
+  float lo[kCodes != kCodesNone ? kPer : 1][8], top_of[kPer], m = 0.0f;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     const int c = tid + kThr * i;
+    top_of[i] = 0.0f;
     if (c < chunks) {
       float w[8], o[8];
       load_vector(n.weight, c, w);
@@ -205,7 +247,7 @@ __global__ __launch_bounds__(kThr < 256 ? 256 : kThr) void norm_kernel(const Nor
         const float x = v[i][j] * e2, p = x * w[j];
         if constexpr (kCodes != kCodesNone) {
           lo[i][j] = fmaf(x, w[j], -p);
-          m = fmaxf(m, fabsf(p));
+          top_of[i] = fmaxf(top_of[i], fabsf(p));
         }
         v[i][j] = p;
         o[j] = p * g;
@@ -216,12 +258,26 @@ __global__ __launch_bounds__(kThr < 256 ? 256 : kThr) void norm_kernel(const Nor
   if constexpr (kCodes != kCodesNone) {
     constexpr bool kInt8 = kCodes == kCodesI8;
     constexpr float kTop = kInt8 ? 127.0f : kFp8Max;
-    m = group_max<kThr>(m, red[4]);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) m = fmaxf(m, top_of[i]);
+    const float2 largest = group_max_pair<kThr>(m, [&](float at) {
+      float rest = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i)
+        if (top_of[i] == at) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (fabsf(v[i][j]) == at) rest = fmaxf(rest, v[i][j] < 0.0f ? -lo[i][j] : lo[i][j]);
+        }
+      return rest;
+    }, red[4]);
+    m = largest.x;
     const float scale = row_scale<kInt8>(m * g);
-    // kTop / m as a sum of two as well; rows of very small values are scaled first, where it would
-    // not be finite
-    const float by = m < 0x1p-80f ? 0x1p100f : 1.0f, top = m * by;
-    const float c0 = top > 0.0f ? kTop / top : 0.0f, c1 = top > 0.0f ? fmaf(-c0, top, kTop) / top : 0.0f;
+    // kTop / m as a sum of two as well, to 2^-44 of it; rows of very small or large values are scaled
+    // first, where a reciprocal would not be finite or normal
+    const float by = m < 0x1p-80f ? 0x1p100f : m > 0x1p80f ? 0x1p-100f : 1.0f, top = m * by;
+    const float c = top > 0.0f ? __builtin_amdgcn_rcpf(top) : 0.0f, c0 = kTop * c;
+    const float c1 = fmaf(-c0, largest.y * by, fmaf(-c0, top, kTop)) * c;
     uint64_t* qr = reinterpret_cast<uint64_t*>(n.q + t * n.H);
     int sum = 0;
 #pragma unroll
@@ -233,6 +289,29 @@ __global__ __launch_bounds__(kThr < 256 ? 256 : kThr) void norm_kernel(const Nor
         for (int j = 0; j < 8; ++j) {
           const float p = v[i][j] * by, l = lo[i][j] * by;
           o[j] = fmaf(p, c0, fmaf(p, c1, l * c0));
+        }
+        // (a border has 8 leading bits at most, of E4M3 5; zeros and the largest value need no care)
+        constexpr int kLead = kInt8 ? 16 : 13;
+        uint32_t low = ~0u;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) low = min(low, __float_as_uint(o[j]) << kLead);
+        if (low == 0) {
+          bool near = false;
+          auto at_border = [&](int j) {
+            return __float_as_uint(o[j]) << kLead == 0 && o[j] != 0.0f && fabsf(o[j]) < kTop;
+          };
+#pragma unroll
+          for (int j = 0; j < 8; ++j) near |= at_border(j);
+          if (near) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const float p = v[i][j] * by, l = lo[i][j] * by;
+              const float over = fmaf(p, c0, -o[j]) + fmaf(p, c1, l * c0);     // (of a tie, 2^-44 of o may be left)
+              const uint32_t u = __float_as_uint(o[j]);
+              if (at_border(j) && fabsf(over) > 0x1p-43f * fabsf(o[j]))
+                o[j] = __uint_as_float((over > 0.0f) == (o[j] > 0.0f) ? u + 1 : u - 1);
+            }
+          }
         }
         const uint2 q = make_uint2(nearest4<kInt8>(o[0], o[1], o[2], o[3]), nearest4<kInt8>(o[4], o[5], o[6], o[7]));
         if constexpr (kInt8) sum = __builtin_amdgcn_sdot4(q.x, 0x01010101, __builtin_amdgcn_sdot4(q.y, 0x01010101, sum, false), false);

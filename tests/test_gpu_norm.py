@@ -240,6 +240,29 @@ def test_many_rows(T, H, y, r):
     check_norm(rms(f64(base[0]), f64(nw), EPS), x8[0][:n], x8[1][:n], x8[2][:n], False, "norm")
 
 
+@pytest.mark.parametrize("i8", [False, True], ids=["fp8", "i8"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("T,H", [(2000, 6144), (300, 264), (40, 32768)])
+def test_codes_are_the_nearest(i8, dtype, T, H):
+    """The code of every value is the nearest to its quotient by the row's largest value (the norm's factor is in
+    neither): products of two fp32 values are exact in 64 bits, the quotient is off by 2^-52 of itself, and quotients
+    within 2^-42 of a border (the kernel takes 2^-43 for a tie) may have either code."""
+    gen = torch.Generator(device=DEV).manual_seed(T + H)
+    x = torch.randn(T, H, device=DEV, generator=gen).to(dtype)
+    w = 1 + 0.2 * torch.randn(H, device=DEV, generator=gen)
+    say(f"nearest codes T={T} H={H} {dtype} i8={i8}")
+    _, q, _ = (ops.w4a8_moe_norm_quant_i8 if i8 else ops.w4a8_moe_norm_quant)(x, w, 1e-5)
+    n = x.double() * w.double()
+    v = n / n.abs().amax(1, keepdim=True) * (127.0 if i8 else 448.0)
+    if i8:
+        got, step = q.double(), torch.ones_like(v)
+    else:
+        got = q.view(torch.float8_e4m3fn).double()
+        e = (torch.frexp(v)[1] - 1).clamp_min(-6)              # 3 bits behind the leading one, 2^-9 the smallest step
+        step = torch.ldexp(torch.ones_like(v), e - 3)
+    assert bool(((got - v).abs() <= step / 2 + 2.0 ** -42 * v.abs()).all())
+
+
 def test_no_rows_and_largest():
     w = torch.ones(64, device=DEV)
     xn, q, s = ops.w4a8_moe_norm_quant(torch.empty(0, 64, device=DEV), w)
