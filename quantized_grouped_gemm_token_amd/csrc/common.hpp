@@ -82,13 +82,6 @@ __device__ __forceinline__ float max16(float v) {
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
-// two fp32 values -> bf16, round to nearest even (a NaN stays one), the first in the low half
-typedef float f32x2 __attribute__((ext_vector_type(2)));
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
-  return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{lo, hi}), bf16x2));
-}
-
 // fp32 -> bf16 bits, round to nearest even (inputs are finite)
 __device__ __forceinline__ uint32_t f32_to_bf16(float f) {
   const uint32_t b = __float_as_uint(f);

@@ -1,5 +1,5 @@
-// Loads straight into LDS and the barrier that leaves them in flight, shared by the tiled
-// GEMM kernels (gemm_tiled.hip, dense_i8.hip).
+// Loads straight into LDS and the barrier that leaves them in flight, for the dense products
+// (dense_i8.hip, dense_few.hip).  gemm_tiled.hip holds its own: its counter summaries are tied to its text.
 #pragma once
 
 #include "common.hpp"

@@ -11,8 +11,8 @@
 // the largest fp32 values stay finite (eps no longer matters then).
 //
 // Bound by the bytes of the rows where they are many (16384 rows of 6144 bf16, norm and codes: 503 MB in
-// 86 us, 5.8 TB/s, above a copy's 5.15), by a launch, one trip to memory and two reductions where they are
-// few (one row 3.2 us; 128 rows between two blocks 5.7 us).
+// 89 us, 5.7 TB/s, above a copy's 5.15), by a launch, one trip to memory and two reductions where they are
+// few (one row 3.6 us; 128 rows between two blocks 5.9 us).
 #include "block.hpp"
 #include "row_codes.hpp"
 
@@ -354,7 +354,7 @@ static void launch_norm_form(const NormArgs& n, hipStream_t stream) {
 
 // A row has as many threads as keep it in a few registers: 256 of bf16, 512 where fp32 is among the
 // rows (norms on both sides of 8192 rows of 6144, fp32: 149 against 158 us; 16384 bf16 rows, norm
-// alone: 89 against 86).  While there is a CU for every row, as many as it has chunks, up to 1024 (128
+// alone: 89 against 86; 4 us more each since codes are exact).  While there is a CU for every row, as many as it has chunks, up to 1024 (128
 // rows of 6144: the norm 3.6 against 4.0 us with 256, between two blocks 5.5 against 7.0).
 constexpr int64_t kFewRows = 256;
 template <bool kNt>

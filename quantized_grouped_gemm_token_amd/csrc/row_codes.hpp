@@ -1,10 +1,17 @@
-// Codes of a row's values from its scale: the rule of row_quant.hpp with one reciprocal
+// Pairs of bf16; codes of a row's values from its scale: the rule of row_quant.hpp with one reciprocal
 // per row in place of a division per value (few.hip, norm.hip, dense_i8.hip).
 #pragma once
 
 #include "common.hpp"
 
 namespace w4a8 {
+
+// two fp32 values -> bf16, round to nearest even (a NaN stays one), the first in the low half
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{lo, hi}), bf16x2));
+}
 
 // x / s rounded to fp32 from r = 1 / s rounded: q = fl(x r), its residual x - q s in
 // one FMA, and the corrected quotient, which is the correctly rounded one (Markstein's

@@ -33,6 +33,7 @@
 
 namespace w4a8 {
 
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
 __device__ __forceinline__ v4f mfma_bf16(i32x4 a, i32x4 b, v4f c) {
