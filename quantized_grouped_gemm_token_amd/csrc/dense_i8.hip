@@ -9,7 +9,8 @@
 //
 // What bounds it.  Many rows (256 x 256): the card's power.  The INT8 products alone, from registers
 // of random codes, run at 3250 to 3750 TOP/s (4530 to 4670 on zeros, the clock being held); 8192 x
-// 12288 x 6144 takes 454 to 481 us, 2570 to 2720 TOP/s with loads, LDS and epilogue (zeros: 382 us).
+// 12288 x 6144 takes 436 to 474 us, 2610 to 2840 TOP/s with loads, LDS and epilogue, the matrix
+// cores busy 67% of the cycles at 1.9 GHz.
 // The smaller tiles: what a CU gets from its L2 (130 to 150 GB/s), 100 to 300 rows the latency of the
 // loads at a step each (128 x 6144 x 6144 11.5 us in 192 tiles of 64 x 64).  Weights that come
 // from memory reach one CU at 25 to 35 GB/s.
@@ -350,10 +351,12 @@ __device__ __forceinline__ uint32_t wave_max_uint(uint32_t v) {
 }
 
 // codes of act rows, one workgroup a row
-__global__ __launch_bounds__(256) void act_quant_kernel(const float* __restrict__ act, int64_t I,
+__global__ __launch_bounds__(256) void act_quant_kernel(const float* __restrict__ act, int64_t M, int64_t I,
                                                         uint8_t* __restrict__ q, float* __restrict__ s) {
   __shared__ uint32_t red[4];
-  const float4* ar = reinterpret_cast<const float4*>(act + blockIdx.x * I);
+  const int64_t row = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
+  if (row >= M) return;
+  const float4* ar = reinterpret_cast<const float4*>(act + row * I);
   uint32_t m = 0;
   for (int c = threadIdx.x; c < (int)(I >> 2); c += 256) {
     const float4 v = ar[c];
@@ -365,12 +368,12 @@ __global__ __launch_bounds__(256) void act_quant_kernel(const float* __restrict_
   m = max(max(red[0], red[1]), max(red[2], red[3]));
   const float scale = m == 0 ? 1.0f : __uint_as_float(m) / 127.0f;
   const RowDivisor d = row_divisor(scale);
-  uint32_t* qr = reinterpret_cast<uint32_t*>(q + blockIdx.x * I);
+  uint32_t* qr = reinterpret_cast<uint32_t*>(q + row * I);
   for (int c = threadIdx.x; c < (int)(I >> 2); c += 256) {
     const float4 v = ar[c];
     qr[c] = codes4<true>(v.x * d.by, v.y * d.by, v.z * d.by, v.w * d.by, d.s, d.r);
   }
-  if (threadIdx.x == 0) s[blockIdx.x] = scale;
+  if (threadIdx.x == 0) s[row] = scale;
 }
 
 template <int kBM, int kBN, int kWM, int kWN, int kSlots, int kPerCu, int kOut, bool kAdd>
@@ -440,7 +443,9 @@ hipError_t launch_mlp_i8(const MlpArgs& p, hipStream_t stream) {
     return launch_down_few(down, act, pmax, stream);
   }
   if (const hipError_t e = launch_product<kOutAct, false>(up, p.I, act, stream); e != hipSuccess) return e;
-  hipLaunchKernelGGL(act_quant_kernel, dim3((unsigned)p.M), dim3(256), 0, stream, act, p.I, q, s);
+  constexpr int64_t kWide = (int64_t)1 << 23;                 // (a launch has fewer than 2^32 threads in x)
+  const dim3 grid((unsigned)(p.M < kWide ? p.M : kWide), (unsigned)((p.M + kWide - 1) / kWide));
+  hipLaunchKernelGGL(act_quant_kernel, grid, dim3(256), 0, stream, act, p.M, p.I, q, s);
   return launch_dense_i8(down, stream);
 }
 

@@ -172,8 +172,9 @@ __global__ __launch_bounds__(kThr < 256 ? 256 : kThr) void norm_kernel(const Nor
   __shared__ __attribute__((aligned(8))) float red[6][16];    // (the last two for one reduction of pairs)
   constexpr int kGroups = kThr < 256 ? 256 / kThr : 1;
   const int tid = kGroups > 1 ? threadIdx.x % kThr : threadIdx.x;
-  const int64_t t = (int64_t)blockIdx.x * kGroups + (kGroups > 1 ? threadIdx.x / kThr : 0);
-  if (kGroups > 1 && t >= n.T) return;                      // (groups of a wave meet no barrier)
+  const int64_t block = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
+  const int64_t t = block * kGroups + (kGroups > 1 ? threadIdx.x / kThr : 0);
+  if (t >= n.T) return;                                     // (a whole block, or groups that meet no barrier)
   const int chunks = (int)(n.H >> 3);
   const float H = (float)n.H;
   const char* xr = static_cast<const char*>(n.x) + t * n.ld_x * (n.x_bf16 ? 2 : 4);
@@ -339,7 +340,10 @@ __global__ __launch_bounds__(kThr < 256 ? 256 : kThr) void norm_kernel(const Nor
 template <int kThr, int kPer, bool kNt>
 static void launch_norm_form(const NormArgs& n, hipStream_t stream) {
   constexpr int kGroups = kThr < 256 ? 256 / kThr : 1;
-  const dim3 grid((unsigned)((n.T + kGroups - 1) / kGroups)), block(kThr * kGroups);
+  // (a launch has fewer than 2^32 threads in x)
+  constexpr int64_t kWide = (int64_t)1 << 21;
+  const int64_t blocks = (n.T + kGroups - 1) / kGroups;
+  const dim3 grid((unsigned)(blocks < kWide ? blocks : kWide), (unsigned)((blocks + kWide - 1) / kWide)), block(kThr * kGroups);
   auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, block, 0, stream, n); };
   if (n.r) {
     if (n.codes == kCodesFp8) go(norm_kernel<kThr, kPer, true, kCodesFp8, kNt>);

@@ -342,7 +342,7 @@ class MoEBlock:
     moe is a W4A8MoE (any form), router a function from xn (bf16 [T, H]) to the router's logits (fp32 [T, E]), shared
     a W8A8Mlp or None, post_weight and gate fp32 [H] or None.  The codes are int8 where there is a shared expert (the
     per-channel experts take them too) or the experts are per-channel, else FP8; experts of the other type quantize
-    xn themselves, as they do for a few tokens (moe.few)."""
+    xn themselves, as they do for a few tokens (moe.few).  The steps of moe share its buffers: one forward at a time."""
 
     def __init__(self, moe: W4A8MoE, weight: torch.Tensor, shared: W8A8Mlp | None = None,
                  post_weight: torch.Tensor | None = None, gate: torch.Tensor | None = None, r_scale: float = 1.0,
@@ -369,6 +369,8 @@ class MoEBlock:
         """The residual stream behind the block (in out if given; it may be r).  normed, if given, is what before(r)
         returns.  With following (the block that takes the result) its before() is made in the same pass: returns
         (out, normed) then."""
+        if following is not None and following.eps != self.eps:
+            raise ValueError("the norms of one pass have one eps")
         xn, q, s, rowsum = self.before(r) if normed is None else normed
         logits = router(xn)
         moe = self.moe
@@ -382,8 +384,6 @@ class MoEBlock:
                    eps=self.eps, out=out)
         if following is None:
             return ops.w4a8_moe_residual_norm(y, r, **how)
-        if following.eps != self.eps:
-            raise ValueError("the norms of one pass have one eps")
         if not following.int8:
             out, *coded = ops.w4a8_moe_residual_norm_quant(y, r, following.weight, **how)
             return out, (*coded, None)

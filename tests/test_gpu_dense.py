@@ -305,3 +305,13 @@ def test_operands_past_32_bits_of_offset():
     say(f"dense_i8 rows {ld} bytes apart")
     y = ops.w4a8_moe_dense_i8(buf[:, :K], sb, w, sw)
     assert torch.equal(y, (b.double() @ w.double().t()).float() * sb[:, None] * sw)
+
+
+def test_gated_block_of_more_rows_than_a_launch_has_in_x():
+    M, H, I = (1 << 24) + 3, 16, 128
+    a, sa, w13, s13 = _large(M, 2 * I, H, 11)
+    w2, s2 = _large(H, H, I, 12)[:2]
+    say(f"mlp_i8 M={M} H={H} I={I}")
+    y = ops.w4a8_moe_mlp_i8(a, sa, w13, s13, w2, s2, y_dtype=torch.bfloat16)
+    for rows in (slice(0, 40), slice((1 << 23) - 20, (1 << 23) + 20), slice((1 << 24) - 20, M)):
+        assert torch.equal(y[rows], ops.w4a8_moe_mlp_i8(a[rows], sa[rows], w13, s13, w2, s2, y_dtype=torch.bfloat16))

@@ -276,3 +276,17 @@ def test_no_rows_and_largest():
     part = ops.w4a8_moe_norm_quant(x[:1000].contiguous(), w)
     for a, b in zip((xn, q, s), part):
         assert torch.equal(a[-1000:], b) and torch.equal(a[200000:201000], b)
+
+
+@pytest.mark.parametrize("T,H", [((1 << 26) + 5, 8), ((1 << 22) + 3, 2056)])
+def test_more_rows_than_a_launch_has_in_x(T, H):
+    gen = torch.Generator(device=DEV).manual_seed(H)
+    x = torch.empty(T, H, dtype=torch.bfloat16, device=DEV).normal_(generator=gen)
+    w = torch.rand(H, device=DEV, generator=gen)
+    say(f"norm T={T} H={H}")
+    whole = ops.w4a8_moe_norm_quant_i8(x, w)
+    res = ops.w4a8_moe_residual_norm(x, x, post_weight=w)
+    for rows in (slice(0, 300), slice((1 << 21) - 150, (1 << 21) + 150), slice(T - 300, T)):
+        for got, want in zip(whole, ops.w4a8_moe_norm_quant_i8(x[rows], w)):
+            assert torch.equal(got[rows], want)
+        assert torch.equal(res[rows], ops.w4a8_moe_residual_norm(x[rows], x[rows], post_weight=w))
