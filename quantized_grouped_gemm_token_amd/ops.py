@@ -1190,7 +1190,7 @@ def _rows(t, name: str, dtypes: tuple, quantum: int) -> tuple[int, int, int]:
     if not t.is_cuda:
         raise ValueError(f"{name} must be a GPU tensor")
     T, H = t.shape
-    if H > 1 and t.stride(1) != 1:
+    if T and H > 1 and t.stride(1) != 1:
         raise ValueError(f"{name} must have contiguous rows")
     # a single row has no distance to the next: any that the library admits
     return T, H, t.stride(0) if T > 1 else -(-H // quantum) * quantum

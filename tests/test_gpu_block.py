@@ -169,6 +169,24 @@ def test_rows_do_not_meet():
     assert bool(torch.isnan(got[3]).all())
 
 
+@pytest.mark.parametrize("form", FORMS)
+def test_no_rows_and_strided_rows(form):
+    """No token at all (whatever the strides of such a tensor are), and a stream and a result whose rows are apart."""
+    b, route = block(form, 91), router(91)
+    for none in (torch.empty(0, H, device=DEV), torch.from_numpy(np.zeros((5, H), np.float32)[:0]).to(DEV),
+                 torch.empty(H, 0, device=DEV).t()):
+        out, normed = b(none, route, following=b)
+        assert tuple(out.shape) == (0, H) and tuple(normed[1].shape) == (0, H)
+    r = stream_of(92, 20, torch.float32)
+    want = b(r, route)
+    wide = torch.full((20, H + 64), 7.0, device=DEV)
+    wide[:, :H] = r
+    assert torch.equal(b(wide[:, :H], route), want)
+    buf = torch.zeros(20, H + 64, device=DEV)
+    b(r, route, out=buf[:, :H])
+    assert torch.equal(buf[:, :H], want) and bool((buf[:, H:] == 0).all())
+
+
 def test_refusals():
     b = block("channel", 81)
     r = stream_of(82, 6, torch.float32)
