@@ -1,8 +1,8 @@
 // Norms before and after a block (w4a8_block.h): RMS norm of a row with its 8-bit codes; and
 // the residual sum of a block's result, normed and gated, followed by the next block's norm.
 //
-// A row is read once and held in registers by a group of threads (a wave for up to 2048
-// values, 256 to 1024 threads beyond), 8 values to a chunk of 16 or 32 bytes:
+// A row is read once and held in registers by a group of threads (a wave for up to 1024
+// values, 128 to 1024 threads beyond), 8 values to a chunk of 16 or 32 bytes:
 //   before: n = weight x / sqrt(mean x^2 + eps); max |n|; codes.
 //   after:  p = post y / sqrt(mean y^2 + eps); out = r_scale r + token_gate gate p; then the
 //           same of out.
@@ -168,9 +168,9 @@ __device__ __forceinline__ float2 group_max_pair(float m, F rest_of, float* red)
 // kRes: with r (the residual form).  kNt: rows and results are marked as read and written once.  A
 // block holds one group, or four of a wave.
 template <int kThr, int kPer, bool kRes, int kCodes, bool kNt>
-__global__ __launch_bounds__(kThr < 256 ? 256 : kThr) void norm_kernel(const NormArgs n) {
+__global__ __launch_bounds__(kThr == kWave ? 4 * kWave : kThr) void norm_kernel(const NormArgs n) {
   __shared__ __attribute__((aligned(8))) float red[6][16];    // (the last two for one reduction of pairs)
-  constexpr int kGroups = kThr < 256 ? 256 / kThr : 1;
+  constexpr int kGroups = kThr == kWave ? 4 : 1;
   const int tid = kGroups > 1 ? threadIdx.x % kThr : threadIdx.x;
   const int64_t block = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
   const int64_t t = block * kGroups + (kGroups > 1 ? threadIdx.x / kThr : 0);
@@ -337,36 +337,47 @@ __global__ __launch_bounds__(kThr < 256 ? 256 : kThr) void norm_kernel(const Nor
   }
 }
 
-template <int kThr, int kPer, bool kNt>
+// kBoth, or the norms alone, or the residual forms alone
+enum Forms : int { kBoth = 0, kNorms = 1, kResiduals = 2 };
+template <int kThr, int kPer, bool kNt, int kForms = kBoth>
 static void launch_norm_form(const NormArgs& n, hipStream_t stream) {
-  constexpr int kGroups = kThr < 256 ? 256 / kThr : 1;
+  constexpr int kGroups = kThr == kWave ? 4 : 1;
   // (a launch has fewer than 2^32 threads in x)
   constexpr int64_t kWide = (int64_t)1 << 21;
   const int64_t blocks = (n.T + kGroups - 1) / kGroups;
   const dim3 grid((unsigned)(blocks < kWide ? blocks : kWide), (unsigned)((blocks + kWide - 1) / kWide)), block(kThr * kGroups);
   auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, block, 0, stream, n); };
-  if (n.r) {
-    if (n.codes == kCodesFp8) go(norm_kernel<kThr, kPer, true, kCodesFp8, kNt>);
-    else if (n.codes == kCodesI8) go(norm_kernel<kThr, kPer, true, kCodesI8, kNt>);
-    else go(norm_kernel<kThr, kPer, true, kCodesNone, kNt>);
-  } else {
-    if (n.codes == kCodesFp8) go(norm_kernel<kThr, kPer, false, kCodesFp8, kNt>);
-    else if (n.codes == kCodesI8) go(norm_kernel<kThr, kPer, false, kCodesI8, kNt>);
-    else go(norm_kernel<kThr, kPer, false, kCodesNone, kNt>);
+  if constexpr (kForms != kNorms) {
+    if (n.r) {
+      if (n.codes == kCodesFp8) go(norm_kernel<kThr, kPer, true, kCodesFp8, kNt>);
+      else if (n.codes == kCodesI8) go(norm_kernel<kThr, kPer, true, kCodesI8, kNt>);
+      else go(norm_kernel<kThr, kPer, true, kCodesNone, kNt>);
+    }
+  }
+  if constexpr (kForms != kResiduals) {
+    if (!n.r) {
+      if (n.codes == kCodesFp8) go(norm_kernel<kThr, kPer, false, kCodesFp8, kNt>);
+      else if (n.codes == kCodesI8) go(norm_kernel<kThr, kPer, false, kCodesI8, kNt>);
+      else go(norm_kernel<kThr, kPer, false, kCodesNone, kNt>);
+    }
   }
 }
 
 // A row has as many threads as keep it in a few registers: 256 of bf16, 512 where fp32 is among the
 // rows (norms on both sides of 8192 rows of 6144, fp32: 149 against 158 us; 16384 bf16 rows, norm
 // alone: 89 against 86; 4 us more each since codes are exact).  While there is a CU for every row, as many as it has chunks, up to 1024 (128
-// rows of 6144: the norm 3.6 against 4.0 us with 256, between two blocks 5.5 against 7.0).
+// rows of 6144: the norm 3.6 against 4.0 us with 256, between two blocks 5.5 against 7.0).  Rows of 1025
+// to 2048 have 128 (24000 bf16 rows of 2048 between two blocks: 95 against 107 us with a wave each);
+// the residual forms, which hold two rows, 1024 beyond 8192 (4000 bf16 rows of 12288: 108 against 155
+// with 256, fp32 185 against 201 with 512; the norm alone is the faster with few, 93 against 107).
 constexpr int64_t kFewRows = 256;
 template <bool kNt>
 static void launch_bf16_rows(const NormArgs& n, hipStream_t stream) {
   if (n.H <= 4096) launch_norm_form<256, 2, kNt>(n, stream);
   else if (n.H <= 6144) launch_norm_form<256, 3, kNt>(n, stream);
   else if (n.H <= 8192) launch_norm_form<256, 4, kNt>(n, stream);
-  else launch_norm_form<256, 8, kNt>(n, stream);
+  else if (n.r) launch_norm_form<1024, 2, kNt, kResiduals>(n, stream);
+  else launch_norm_form<256, 8, kNt, kNorms>(n, stream);
 }
 
 // From here on bf16 rows and their results are marked as read or written once: they would only push
@@ -381,7 +392,7 @@ hipError_t launch_norm(const NormArgs& n, hipStream_t stream) {
   const int64_t bytes = n.T * n.H * (2 + (n.r ? 4 : 0) + (n.xn ? 2 : 0) + (n.q ? 1 : 0));
   if (n.H <= 512) launch_norm_form<64, 1, false>(n, stream);
   else if (n.H <= 1024) launch_norm_form<64, 2, false>(n, stream);
-  else if (n.H <= 2048) launch_norm_form<64, 4, false>(n, stream);
+  else if (n.H <= 2048) launch_norm_form<128, 2, false>(n, stream);
   else if (n.H > 16384) launch_norm_form<1024, 4, false>(n, stream);
   else if (n.T <= kFewRows && n.H <= 8192) launch_norm_form<1024, 1, false>(n, stream);
   else if (n.T <= kFewRows) launch_norm_form<1024, 2, false>(n, stream);
@@ -389,7 +400,8 @@ hipError_t launch_norm(const NormArgs& n, hipStream_t stream) {
   else if (bf16) launch_bf16_rows<false>(n, stream);
   else if (n.H <= 4096) launch_norm_form<512, 1, false>(n, stream);
   else if (n.H <= 8192) launch_norm_form<512, 2, false>(n, stream);
-  else launch_norm_form<512, 4, false>(n, stream);
+  else if (n.r) launch_norm_form<1024, 2, false, kResiduals>(n, stream);
+  else launch_norm_form<512, 4, false, kNorms>(n, stream);
   return hipGetLastError();
 }
 
