@@ -179,10 +179,15 @@ __global__ __launch_bounds__(kThr == kWave ? 4 * kWave : kThr) void norm_kernel(
   const float H = (float)n.H;
   const char* xr = static_cast<const char*>(n.x) + t * n.ld_x * (n.x_bf16 ? 2 : 4);
   float v[kPer][8];
-  Raw raw[kPer], raw_r[kRes ? kPer : 1];
+  // Rows beyond 16384 do not fit in the registers of 1024 threads with all that is known of them: their
+  // chunks of r are read as they are needed, and the weight twice for the products' second parts
+  // (2000 bf16 rows of 24576 between two blocks 124 against 164 us; rows of 8192 to 16384 would lose, 89
+  // to 116).
+  constexpr bool kHold = kThr * kPer <= 2048;
+  Raw raw[kPer], raw_r[kRes && kHold ? kPer : 1];
   const char* rr = static_cast<const char*>(n.r) + t * n.ld_r * (n.r_bf16 ? 2 : 4);
   load_row<kNt, kThr>(raw, xr, n.x_bf16, tid, chunks);
-  if constexpr (kRes) load_row<kNt, kThr>(raw_r, rr, n.r_bf16, tid, chunks);
+  if constexpr (kRes && kHold) load_row<kNt, kThr>(raw_r, rr, n.r_bf16, tid, chunks);
 #pragma unroll
   for (int i = 0; i < kPer; ++i) widen(raw[i], n.x_bf16, v[i]);
   bool fine = true;
@@ -208,7 +213,7 @@ __global__ __launch_bounds__(kThr == kWave ? 4 * kWave : kThr) void norm_kernel(
       const int c = tid + kThr * i;
       if (c < chunks) {
         float r[8], g[8];
-        widen(raw_r[i], n.r_bf16, r);
+        widen(kHold ? raw_r[kHold ? i : 0] : load_raw<kNt>(rr, n.r_bf16, c), n.r_bf16, r);
         if (n.gate) load_vector(n.gate, c, g);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
@@ -235,7 +240,7 @@ __global__ __launch_bounds__(kThr == kWave ? 4 * kWave : kThr) void norm_kernel(
   const RowNorm r = row_norm<kThr, kPer>(v, H, n.eps, red[2], red[3]);
   fine &= r.fine;
   const float e2 = __uint_as_float(__float_as_uint(r.f) & 0x7f800000u), g = r.f / e2;
-  float lo[kCodes != kCodesNone ? kPer : 1][8], top_of[kPer], m = 0.0f;
+  float lo[kCodes != kCodesNone && kHold ? kPer : 1][8], top_of[kPer], m = 0.0f;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     const int c = tid + kThr * i;
@@ -247,10 +252,10 @@ __global__ __launch_bounds__(kThr == kWave ? 4 * kWave : kThr) void norm_kernel(
       for (int j = 0; j < 8; ++j) {
         const float x = v[i][j] * e2, p = x * w[j];
         if constexpr (kCodes != kCodesNone) {
-          lo[i][j] = fmaf(x, w[j], -p);
+          if constexpr (kHold) lo[i][j] = fmaf(x, w[j], -p);
           top_of[i] = fmaxf(top_of[i], fabsf(p));
         }
-        v[i][j] = p;
+        v[i][j] = kHold ? p : x;
         o[j] = p * g;
       }
       if (n.xn) store<kNt>(reinterpret_cast<u32x4*>(n.xn + t * n.H) + c, bf16x8(o));
@@ -261,14 +266,26 @@ __global__ __launch_bounds__(kThr == kWave ? 4 * kWave : kThr) void norm_kernel(
     constexpr float kTop = kInt8 ? 127.0f : kFp8Max;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) m = fmaxf(m, top_of[i]);
+    // chunk i's products, as sums of two
+    auto products = [&](int i, float (&p)[8], float (&l)[8]) {
+      float w[8];
+      if constexpr (!kHold) load_vector(n.weight, tid + kThr * i, w);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        p[j] = kHold ? v[i][j] : v[i][j] * w[j];
+        l[j] = kHold ? lo[kHold ? i : 0][j] : fmaf(v[i][j], w[j], -p[j]);
+      }
+    };
     const float2 largest = group_max_pair<kThr>(m, [&](float at) {
       float rest = -INFINITY;
 #pragma unroll
       for (int i = 0; i < kPer; ++i)
-        if (top_of[i] == at) {
+        if (top_of[i] == at && tid + kThr * i < chunks) {
+          float p[8], l[8];
+          products(i, p, l);
 #pragma unroll
           for (int j = 0; j < 8; ++j)
-            if (fabsf(v[i][j]) == at) rest = fmaxf(rest, v[i][j] < 0.0f ? -lo[i][j] : lo[i][j]);
+            if (fabsf(p[j]) == at) rest = fmaxf(rest, p[j] < 0.0f ? -l[j] : l[j]);
         }
       return rest;
     }, red[4]);
@@ -285,11 +302,12 @@ __global__ __launch_bounds__(kThr == kWave ? 4 * kWave : kThr) void norm_kernel(
     for (int i = 0; i < kPer; ++i) {
       const int c = tid + kThr * i;
       if (c < chunks) {
-        float o[8];
+        float p[8], l[8], o[8];
+        products(i, p, l);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const float p = v[i][j] * by, l = lo[i][j] * by;
-          o[j] = fmaf(p, c0, fmaf(p, c1, l * c0));
+          p[j] *= by, l[j] *= by;
+          o[j] = fmaf(p[j], c0, fmaf(p[j], c1, l[j] * c0));
         }
         // (a border has 8 leading bits at most, of E4M3 5; zeros and the largest value need no care)
         constexpr int kLead = kInt8 ? 16 : 13;
@@ -306,8 +324,7 @@ __global__ __launch_bounds__(kThr == kWave ? 4 * kWave : kThr) void norm_kernel(
           if (near) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-              const float p = v[i][j] * by, l = lo[i][j] * by;
-              const float over = fmaf(p, c0, -o[j]) + fmaf(p, c1, l * c0);     // (of a tie, 2^-44 of o may be left)
+              const float over = fmaf(p[j], c0, -o[j]) + fmaf(p[j], c1, l[j] * c0);     // (of a tie, 2^-44 of o may be left)
               const uint32_t u = __float_as_uint(o[j]);
               if (at_border(j) && fabsf(over) > 0x1p-43f * fabsf(o[j]))
                 o[j] = __uint_as_float((over > 0.0f) == (o[j] > 0.0f) ? u + 1 : u - 1);
