@@ -29,15 +29,17 @@ struct Sum {
 struct Max {
   static __device__ __forceinline__ float of(float a, float b) { return fmaxf(a, b); }
 };
-// The reduction of kLanes neighbouring lanes in each of them, in registers: quads by their
-// permutations, rows of 16 by rotations, rows by swaps (with shuffles through LDS a norm of one row
-// takes 4.8 us, so 3.7).
+// The reduction of kLanes neighbouring lanes, in registers: quads by their permutations, rows of 16 by
+// mirrors, rows by swaps (with shuffles through LDS a norm of one row takes 4.8 us, so 3.7).  In every
+// step two lanes read each other and add the same two values, so all lanes end with the same bits, which
+// row_norm's branch and the codes rely on.  (Rows turned by 4 and 8 in place of the mirrors would add the
+// quads in two orders: fp32 sums that differ.)
 template <typename Op, int kLanes>
 __device__ __forceinline__ float lanes_reduce(float v) {
   if constexpr (kLanes > 1) v = Op::of(v, dpp<0xB1>(v));
   if constexpr (kLanes > 2) v = Op::of(v, dpp<0x4E>(v));
-  if constexpr (kLanes > 4) v = Op::of(v, dpp<0x124>(v));
-  if constexpr (kLanes > 8) v = Op::of(v, dpp<0x128>(v));
+  if constexpr (kLanes > 4) v = Op::of(v, dpp<0x141>(v));
+  if constexpr (kLanes > 8) v = Op::of(v, dpp<0x140>(v));
   if constexpr (kLanes > 16) {
     const auto s = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
     v = Op::of(__uint_as_float(s[0]), __uint_as_float(s[1]));
@@ -135,7 +137,7 @@ __device__ __forceinline__ RowNorm row_norm(float (&v)[kPer][8], float H, float 
     for (int j = 0; j < 8; ++j) ss = fmaf(v[i][j], v[i][j], ss);
   ss = group_sum<kThr>(ss, red);
   if (ss < INFINITY) return RowNorm{__builtin_amdgcn_rsqf(ss / H + eps), true};
-  constexpr float kDown = 0x1p-80f;                         // (the same for the whole group)
+  constexpr float kDown = 0x1p-80f;                         // (the whole group comes here, or none: one sum)
   ss = 0.0f;
 #pragma unroll
   for (int i = 0; i < kPer; ++i)
