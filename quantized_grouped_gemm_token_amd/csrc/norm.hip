@@ -7,8 +7,8 @@
 //   after:  p = post y / sqrt(mean y^2 + eps); out = r_scale r + token_gate gate p; then the
 //           same of out.
 // Each mean, and the maximum, is one reduction over the group.  Sums are fp32; a row whose
-// sum of squares is not below infinity is summed again times 2^-80, where 32768 squares of
-// the largest fp32 values stay finite (eps no longer matters then).
+// mean square and eps are not below infinity is summed again times 2^-80, where 32768 squares of
+// the largest fp32 values stay finite (an eps that is lost by that does not matter next to them).
 //
 // Bound by the bytes of the rows where they are many (16384 rows of 6144 bf16, norm and codes: 503 MB in
 // 89 us, 5.7 TB/s, above a copy's 5.15), by a launch, one trip to memory and two reductions where they are
@@ -136,7 +136,8 @@ __device__ __forceinline__ RowNorm row_norm(float (&v)[kPer][8], float H, float 
 #pragma unroll
     for (int j = 0; j < 8; ++j) ss = fmaf(v[i][j], v[i][j], ss);
   ss = group_sum<kThr>(ss, red);
-  if (ss < INFINITY) return RowNorm{__builtin_amdgcn_rsqf(ss / H + eps), true};
+  const float mean = ss / H + eps;
+  if (mean < INFINITY) return RowNorm{__builtin_amdgcn_rsqf(mean), true};
   constexpr float kDown = 0x1p-80f;                         // (the whole group comes here, or none: one sum)
   ss = 0.0f;
 #pragma unroll
@@ -147,7 +148,7 @@ __device__ __forceinline__ RowNorm row_norm(float (&v)[kPer][8], float H, float 
       ss = fmaf(v[i][j], v[i][j], ss);
     }
   ss = group_sum<kThr>(ss, red2);
-  return RowNorm{__builtin_amdgcn_rsqf(ss / H), ss < INFINITY};
+  return RowNorm{__builtin_amdgcn_rsqf(ss / H + eps * kDown * kDown), ss < INFINITY};
 }
 
 // the largest value of a group, held as a sum of two: the larger m, of equal ones the larger rest,

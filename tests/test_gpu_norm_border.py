@@ -107,3 +107,20 @@ def test_rows_whose_squares_come_next_to_the_largest_sum(T, H, i8):
     out = ops.w4a8_moe_residual_norm(x, torch.zeros_like(x), post_weight=w, eps=EPS)
     n = x.double() * w.double() / torch.sqrt((x.double() ** 2).mean(1, keepdim=True))
     assert bool(((out.double() - n).abs() <= (NORM_REL + HALF_F32) * n.abs()).all())
+
+
+@pytest.mark.parametrize("i8", [False, True], ids=["fp8", "i8"])
+@pytest.mark.parametrize("H,eps", [(8, 3.3e38), (64, 2.0 ** 127), (512, 1e30), (512, 1e36), (6144, 1e33), (20000, 1e35)])
+def test_eps_next_to_the_largest_squares(H, eps, i8):
+    """An eps that matters next to rows whose sum of squares overflows, or that overflows with a mean square."""
+    gen = torch.Generator(device=DEV).manual_seed(H)
+    w = 1 + 0.2 * torch.randn(H, device=DEV, generator=gen)
+    gains = torch.tensor([1e10, 1e15, 1e17, 1e18, 6e18, 1e19, 2e19, 1e20, 1e25, 1e36], device=DEV, dtype=torch.float64)
+    x = torch.randn(len(gains), H, device=DEV, generator=gen, dtype=torch.float64)
+    x = (x / x.abs().amax(1, keepdim=True) * gains[:, None]).float()
+    say(f"norms with eps={eps} H={H} i8={i8}")
+    fn = ops.w4a8_moe_norm_quant_i8 if i8 else ops.w4a8_moe_norm_quant
+    check(x, w, np.float32(eps).item(), *fn(x, w, eps), i8)
+    y = ops.w4a8_moe_residual_norm(x, torch.zeros_like(x), post_weight=w, eps=eps)
+    n = x.double() * w.double() / torch.sqrt((x.double() ** 2).mean(1, keepdim=True) + np.float32(eps).item())
+    assert bool(((y.double() - n).abs() <= (NORM_REL + HALF_F32) * n.abs()).all())
