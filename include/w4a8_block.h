@@ -79,8 +79,8 @@ int w4a8_moe_mlp_i8(const int8_t* a, const float* a_scale, int64_t M, int64_t H,
  *     scale and codes of n, as it is before that rounding: sx[t] = fl32(max |n| / 448)
  *     (_i8: / 127), 1.0 if that is 0; qx = E4M3 (_i8: the integer) nearest to 448 n / max |n|
  *     (127 n / max |n|), ties to even: to the exact quotient of weight * x, the norm's factor
- *     being in neither (one within 2^-42 of a tie counts as the tie; products below fp32's normal
- *     range are rounded); _i8: rowsum[t] = sum of qx[t, :].
+ *     being in neither (one within 2^-42 of a tie counts as the tie; where n is below 2^-100, of
+ *     the product to a multiple of fp32's smallest number); _i8: rowsum[t] = sum of qx[t, :].
  *   x       : [T][ld_x], fp32 or bf16 (x_dtype: W4A8_Y_F32, W4A8_Y_BF16), 16-byte aligned
  *             rows (ld_x % 8 == 0 in bf16, % 4 in fp32), ld_x >= H.
  *   weight  : fp32 [H], 16-byte aligned.

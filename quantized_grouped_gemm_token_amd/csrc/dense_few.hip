@@ -262,7 +262,6 @@ __global__ __launch_bounds__(kFewRowsThreads) void dense_few_kernel(const FewRow
         }
       }
     }
-    constexpr int kStride = Lds::kRegion / 4;  // words from one wave's tiles to the next's
     int* part = reinterpret_cast<int*>(regions) + buf * 256;
 #pragma unroll
     for (int r = 0; r < 4; ++r) part[wave * kStride + (4 * q + r) * 16 + col] = acc[r];

@@ -1222,7 +1222,7 @@ def _no_overlap(out, name: str, *inputs) -> None:
                 raise ValueError(f"{name} must not overlap {other}")
 
 
-def _new_y(y_dtype, M: int, N: int, add, a: torch.Tensor) -> torch.Tensor:
+def _new_y(y_dtype, M: int, N: int, a: torch.Tensor) -> torch.Tensor:
     if y_dtype is not _BF16 and y_dtype is not _F32:
         raise TypeError("y must be float32 or bfloat16")
     return a.new_empty((M, N), dtype=y_dtype)
@@ -1256,7 +1256,7 @@ def w4a8_moe_dense_i8(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor, w
     if bias is not None:
         _is(bias, "bias", _F32, (N,), dev)
     if y is None:
-        y = _new_y(y_dtype, M, N, add, a)
+        y = _new_y(y_dtype, M, N, a)
     else:
         _given_y(y, M, N, add, dev, a=a, a_scale=a_scale, w=w, w_scale=w_scale, bias=bias)
     if add is not None:
@@ -1291,7 +1291,7 @@ def w4a8_moe_mlp_i8(a: torch.Tensor, a_scale: torch.Tensor, w13: torch.Tensor, s
     _is(s13, "s13", _F32, (2 * I,), dev)
     _is(s2, "s2", _F32, (H,), dev)
     if y is None:
-        y = _new_y(y_dtype, M, H, add, a)
+        y = _new_y(y_dtype, M, H, a)
     else:
         _given_y(y, M, H, add, dev, a=a, a_scale=a_scale, w13=w13, s13=s13, w2=w2, s2=s2)
     if add is not None:
