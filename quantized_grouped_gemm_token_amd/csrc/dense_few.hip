@@ -13,7 +13,9 @@
 // read of whole lines reaches); 6144 x 6144 9.2 us with one row and 10.6 with 16, of which 3 are the
 // launch and the first loads' way; 12288 x 6144 14.4 us.  Weights in a cache and 16 rows of more than 8192 outputs
 // would go faster in the tiled kernel (16 x 12288 x 6144 13.2 against 15.7 us); read from memory, as a
-// model's weights are, they do not (17.4 against 16.6; 16 x 24576 x 6144 31.9 against 27.3).
+// model's weights are, they do not (17.4 against 16.6; 16 x 24576 x 6144 31.9 against 27.3).  Half of the
+// LDS cycles are bank conflicts: the operand reads take chunks q and 4 + q of a row, where dense_i8.hip's 2 q
+// and 2 q + 1 have none.  A unit's two reads a wave hide behind its weights (the head reads at memory's rate).
 //
 // The gated block is two kernels: the gated product leaves act (fp32) and the maxima of 8
 // columns of it; the down product's workgroups quantize act themselves, each wave its part of K,

@@ -9,7 +9,7 @@
 //
 // What bounds it.  Many rows (256 x 256): the card's power.  The INT8 products alone, from registers
 // of random codes, run at 3250 to 3750 TOP/s (4530 to 4670 on zeros, the clock being held); 8192 x
-// 12288 x 6144 takes 436 to 474 us, 2610 to 2840 TOP/s with loads, LDS and epilogue, the matrix
+// 12288 x 6144 takes 436 to 481 us, 2570 to 2840 TOP/s with loads, LDS and epilogue, the matrix
 // cores busy 67% of the cycles at 1.9 GHz.
 // The smaller tiles: what a CU gets from its L2 (130 to 150 GB/s), 100 to 300 rows the latency of the
 // loads at a step each (128 x 6144 x 6144 11.5 us in 192 tiles of 64 x 64).  Weights that come
@@ -19,7 +19,8 @@
 // us at that stage), steps of 64 bytes in 4 slots (half lines double the L2's requests: 503
 // against 484), lines touched ahead into L2 (482 against 472), wave priorities, XCDs out of step and
 // nontemporal stores (nothing); K split over workgroups with a second kernel for the sums (128 x
-// 6144 x 6144 16.4 against 11.7); tiles of 128 x 32, 64 x 128 and 128 x 256.
+// 6144 x 6144 16.4 against 11.7, weights in a cache); tiles of 128 x 32 in a ring of 4 (the same 14.2 against
+// 11.7, from memory 21.4 against 18.5), of 64 x 128 and 128 x 256.
 #include "block.hpp"
 #include "gemm_common.hpp"
 #include "lds_dma.hpp"
