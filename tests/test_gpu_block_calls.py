@@ -77,3 +77,53 @@ def test_outputs_left_out(T, H, i8):
             for i in keep:
                 assert torch.equal(part[i], whole[i]), (call.__name__, keep, i)
             assert out is None or torch.equal(again, out)
+
+
+def shifted(t, by=1):
+    """t's values in memory that starts `by` elements behind an allocation's start."""
+    buf = torch.empty(t.numel() + by, dtype=t.dtype, device=t.device)
+    buf[by:] = t.reshape(-1)
+    return buf[by:].view(t.shape)
+
+
+@pytest.mark.parametrize("M", [1, 16, 17, 64, 130, 300, 1500])
+def test_vectors_aligned_to_their_elements(M):
+    """Scales, bias, addend and result of the products at addresses of their elements' alignment only."""
+    g = np.random.Generator(np.random.PCG64(M))
+    K, I = 400, 384
+    c = lambda *s: torch.from_numpy(g.integers(-128, 128, size=s, dtype=np.int8)).to(DEV)  # noqa: E731
+    f = lambda *s: torch.from_numpy(g.normal(size=s).astype(np.float32)).to(DEV)  # noqa: E731
+    a, sa, w13, s13, w2, s2 = c(M, K), f(M), c(2 * I, K), 0.01 * f(2 * I), c(K, I), f(K)
+    bias, add = f(2 * I), f(M, K)
+    say(f"products with vectors at any element M={M}")
+    for dt in (torch.float32, torch.bfloat16):
+        want = ops.w4a8_moe_dense_i8(a, sa, w13, s13, bias=bias, y_dtype=dt)
+        y = shifted(torch.zeros(M, 2 * I, dtype=dt, device=DEV))
+        ops.w4a8_moe_dense_i8(a, shifted(sa), w13, shifted(s13, 3), bias=shifted(bias), y=y)
+        assert torch.equal(y, want)
+        want = ops.w4a8_moe_mlp_i8(a, sa, w13, s13, w2, s2, add=add.to(dt), y_dtype=dt)
+        y = shifted(add.to(dt))
+        ops.w4a8_moe_mlp_i8(a, shifted(sa, 2), w13, shifted(s13), w2, shifted(s2, 3), add=y, y=y)
+        assert torch.equal(y, want)
+
+
+@pytest.mark.parametrize("T,H", [(3, 512), (5, 2048), (2, 6144), (300, 6144), (300, 12288), (3, 20000)])
+def test_norm_vectors_aligned_to_their_elements(T, H):
+    g = np.random.Generator(np.random.PCG64(T + H))
+    f = lambda *s: torch.from_numpy(g.normal(size=s).astype(np.float32)).to(DEV)  # noqa: E731
+    y, r, w, gate, tg = f(T, H), f(T, H), f(H), f(H), f(T)
+    say(f"norms with vectors at any element T={T} H={H}")
+    for r_scale in (0.0, -1.5):
+        kw = dict(post_weight=w, gate=gate, r_scale=r_scale)
+        sums = torch.zeros(T, dtype=torch.int32, device=DEV)
+        want = ops.w4a8_moe_residual_norm_quant_i8(y, r, w, token_gate=tg, rowsum=sums, **kw)
+        q, s, more = shifted(torch.zeros_like(want[2]), 8), shifted(torch.zeros_like(want[3])), shifted(torch.zeros_like(sums))
+        got = ops.w4a8_moe_residual_norm_quant_i8(y, r, w, token_gate=shifted(tg), qx=q, sx=s, rowsum=more, **kw)
+        for a, b in zip((*got, more), (*want, sums)):
+            assert torch.equal(a, b)
+        n = y.double() * w.double() / torch.sqrt((y.double() ** 2).mean(1, keepdim=True) + 1e-6)
+        p = n * gate.double() * tg.double()[:, None]
+        out = r_scale * r.double() + p
+        # the norm's fp32 error and two products, then the sum's rounding (a term and the sum may be one FMA)
+        tol = (40 + 2) * 2.0 ** -24 * p.abs() + 2.0 ** -24 * out.abs()
+        assert bool(((got[0].double() - out).abs() <= tol).all())
